@@ -1,0 +1,80 @@
+// Problem descriptor of the gated delta kernels, and their launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace delta {
+
+constexpr int PS = 64;   // value columns of a walk's block (16 per wave)
+
+struct Problem {
+  // sizes
+  int B, L, H, P, G, N, nseqs, hpg;
+  int total;      // B * L rows
+  int nslots;     // chunk slots: the chunks of sequence s are slots start(s) / 64 + s, ...
+  int np;         // blocks of PS value columns
+  float scale;
+  int64_t q_sb, q_sl, k_sb, k_sl, v_sb, v_sl;
+  // inputs
+  const void *q, *k, *v, *dout;
+  const float *g, *beta, *h0, *dfinal;
+  const int32_t* seq_idx;
+  // outputs
+  void *o, *dq, *dk, *dv;
+  float *final, *dg, *dbeta, *dinit;
+  // workspace
+  int32_t* starts;   // (nseqs + 1) first rows (seq_idx given)
+  float* gates;      // (slots, H, GATES, 64)
+  uint4* tf;         // (slots, H, FRAG_PIECES): T' = (I + N diag(beta))^-1, rows in pair order
+  uint4* pf;         // the same of the causal scores, rows in order
+  uint4* ttf;        // transposed (I + diag(beta) N)^-1, rows in pair order (backward)
+  uint4* ptf;        // transposed scores, rows in pair order (backward)
+  uint4* e;          // (slots, H, np, 4 waves, 4, 64): the residuals, float32, accumulator layout (backward)
+  void* u;           // (slots, H, np * PS, 64) io dtype: beta * e, a column per row (backward)
+  void* s;           // (slots, H, np * PS, ND) 2 bf16 terms or float32: entering states (backward)
+  void* ds;          // (slots, H, np * PS, ND) io dtype: gradient of the state after the chunk (backward)
+  float* oo;         // (slots, H, np, 64): dout . o over the block's columns (backward)
+  float* dd;         // (slots, H, np, 64): dout . o - dv . v
+  float* be;         // (slots, H, np, 64): dbeta
+  float* phi;        // (slots, H, np): <entering state, its gradient>
+};
+
+// per slot and head: exp(c_i), exp(c_last - c_i), beta_i, and c_i in two floats
+enum { GATE_IN = 0, GATE_OUT = 1, GATE_BETA = 2, GATE_C = 3, GATE_CLO = 4, GATES = 5 };
+
+int launch_starts(const Problem& p, hipStream_t s);
+int launch_prep(const Problem& p, int io, bool backward, hipStream_t s);
+int launch_walk(const Problem& p, int io, bool backward, hipStream_t s);
+int launch_rwalk(const Problem& p, int io, hipStream_t s);
+int launch_grad(const Problem& p, int io, hipStream_t s);
+
+#ifdef __HIPCC__
+// first row of sequence s (s == nseqs: the end of the last)
+__device__ __forceinline__ int seq_start(const Problem& p, int s) { return p.seq_idx ? p.starts[s] : s * p.L; }
+__device__ __forceinline__ int slot_base(int start, int s) { return (start >> 6) + s; }
+
+struct Chunk {
+  int seq, row, len;   // sequence, first row (flat), rows of the chunk (0: the slot holds none)
+};
+// which chunk a slot holds
+__device__ __forceinline__ Chunk chunk_of(const Problem& p, int slot) {
+  int lo = 0, hi = p.nseqs;   // the last sequence whose slots begin at or before this one
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (slot_base(seq_start(p, mid), mid) <= slot) lo = mid; else hi = mid;
+  }
+  const int s0 = seq_start(p, lo), s1 = seq_start(p, lo + 1);
+  Chunk c{lo, s0 + 64 * (slot - slot_base(s0, lo)), 0};
+  c.len = s1 - c.row < 64 ? s1 - c.row : 64;
+  if (c.len < 0) c.len = 0;
+  return c;
+}
+// the batch row's base and the row inside it are taken once: a sequence lies in one batch row
+__device__ __forceinline__ int64_t row_offset(int row, int L, int64_t sb, int64_t sl) {
+  const int b = row / L;
+  return b * sb + static_cast<int64_t>(row - b * L) * sl;
+}
+#endif
+
+}  // namespace delta

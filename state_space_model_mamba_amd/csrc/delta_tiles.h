@@ -1,0 +1,241 @@
+// Register tiles, fragments and staging shared by the gated delta kernels.
+//
+// Every product here is a 16x16 MFMA tile over 32 values of the contraction.
+// A lane is (g, c) = (lane / 16, lane % 16).  An operand fragment holds, for
+// row (A) or column (B) c, the 8 contraction values 8 g + e; the accumulator
+// of a tile holds Out[4 g + r][c].  Two tiles whose A rows are taken in the
+// order
+//     row(t, m) = 32 (t / 2) + 8 (m / 4) + 4 (t % 2) + m % 4
+// therefore hold, together, rows 32 q + 8 g + e of column c in lane (g, c):
+// the layout of an operand fragment over those 32 rows, so a pair of
+// accumulator tiles becomes the operand of the next product without leaving
+// the lane (as B: contraction over its rows; as A: its transpose).
+//
+// With bf16 io, float32 values that feed a state or a gate's gradient enter
+// a product as two bf16 terms, x = hi + lo + O(2^-17 |x|): one MFMA more per
+// product with an exact bf16 operand, two more per product of two such values
+// (lo * lo is dropped).  Single bf16 operands would leave the float32 outputs
+// 3e-3 off; measured error with two terms: 2e-6 .. 4e-6.  With f32 io every
+// product is v_mfma_f32_16x16x4_f32.
+#pragma once
+
+#include "ssd_device.h"
+#include "ssd_tiles.h"
+
+namespace delta {
+
+using ssd::bf16_t;
+using ssd::bf16x8_t;
+using ssd::f32x4_t;
+using ssd::pack_bf16x2;
+using ssd::Vec16;
+using ssd::zero4;
+
+constexpr int CH = 64;   // rows of a chunk
+
+typedef float f32x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ int perm_row(int t, int m) { return 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3); }
+
+// 8 contraction values of one row or column: X as given, S an fp32 value (bf16 io: hi and lo terms)
+template <typename T> struct Fr;
+
+template <> struct Fr<bf16_t> {
+  typedef bf16x8_t X;
+  struct S { bf16x8_t hi, lo; };
+  static constexpr int NX = 1, NS = 2;   // 16-byte pieces of an X and of an S
+  static __device__ __forceinline__ X zero() { return ssd::Mma<bf16_t>::zero(); }
+  static __device__ __forceinline__ X load(const bf16_t* p) { return ssd::Mma<bf16_t>::load_k(p); }
+  // Rows row0 .. row0 + 3 of one column of a row-major LDS tile: column CS (c / 4) + c % 4 of base
+  // (CS 4: 16 columns side by side; CS 8: the columns of a tile in pair order).
+  template <int CS> static __device__ __forceinline__ ssd::s16x4_t tr4(const bf16_t* base, int ld, int row0) {
+    const int c = static_cast<int>(threadIdx.x) & 15;
+    return ssd::lds_read_tr16(base + (row0 + (c >> 2)) * ld + CS * (c & 3));
+  }
+  // rows row0 .. row0 + 7 of that column
+  template <int CS = 4> static __device__ __forceinline__ X load_tr(const bf16_t* base, int ld, int row0) {
+    union { ssd::s16x4_t h[2]; X x; } u;
+    u.h[0] = tr4<CS>(base, ld, row0);
+    u.h[1] = tr4<CS>(base, ld, row0 + 4);
+    return u.x;
+  }
+  static __device__ __forceinline__ f32x4_t load4_tr(const bf16_t* base, int ld, int row0) {
+    const ssd::s16x4_t v = tr4<4>(base, ld, row0);
+    f32x4_t f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) f[r] = ssd::bf16_to_f32(static_cast<bf16_t>(v[r]));
+    return f;
+  }
+  static __device__ __forceinline__ X round8(const float (&v)[8]) {
+    uint4 u = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    return __builtin_bit_cast(X, u);
+  }
+  static __device__ __forceinline__ S split(const float (&v)[8]) {
+    S s;
+    s.hi = round8(v);
+    const uint4 u = __builtin_bit_cast(uint4, s.hi);
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[2 * i] = v[2 * i] - __uint_as_float((&u.x)[i] << 16);
+      r[2 * i + 1] = v[2 * i + 1] - __uint_as_float((&u.x)[i] & 0xffff0000u);
+    }
+    s.lo = round8(r);
+    return s;
+  }
+  static __device__ __forceinline__ X hi(const S& s) { return s.hi; }
+  static __device__ __forceinline__ void pieces(const S& s, uint4 (&u)[2]) {
+    u[0] = __builtin_bit_cast(uint4, s.hi);
+    u[1] = __builtin_bit_cast(uint4, s.lo);
+  }
+  static __device__ __forceinline__ S from_pieces(const uint4 (&u)[2]) {
+    return S{__builtin_bit_cast(X, u[0]), __builtin_bit_cast(X, u[1])};
+  }
+  static __device__ __forceinline__ void floats(const S& s, float (&v)[8]) {
+    const uint4 h = __builtin_bit_cast(uint4, s.hi), l = __builtin_bit_cast(uint4, s.lo);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float((&h.x)[i] << 16) + __uint_as_float((&l.x)[i] << 16);
+      v[2 * i + 1] = __uint_as_float((&h.x)[i] & 0xffff0000u) + __uint_as_float((&l.x)[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void store(bf16_t* p, X x) { *reinterpret_cast<X*>(p) = x; }
+  static __device__ __forceinline__ void floats(X x, float (&v)[8]) {
+    const uint4 h = __builtin_bit_cast(uint4, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float((&h.x)[i] << 16);
+      v[2 * i + 1] = __uint_as_float((&h.x)[i] & 0xffff0000u);
+    }
+  }
+};
+
+template <> struct Fr<float> {
+  typedef f32x8_t X;
+  typedef f32x8_t S;
+  static constexpr int NX = 2, NS = 2;
+  static __device__ __forceinline__ X zero() { return X{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}; }
+  static __device__ __forceinline__ X load(const float* p) {
+    union { f32x4_t h[2]; X x; } u;
+    u.h[0] = *reinterpret_cast<const f32x4_t*>(p);
+    u.h[1] = *reinterpret_cast<const f32x4_t*>(p + 4);
+    return u.x;
+  }
+  template <int CS = 4> static __device__ __forceinline__ X load_tr(const float* base, int ld, int row0) {
+    const int c = static_cast<int>(threadIdx.x) & 15;
+    const float* p = base + row0 * ld + CS * (c >> 2) + (c & 3);
+    X x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = p[e * ld];
+    return x;
+  }
+  static __device__ __forceinline__ f32x4_t load4_tr(const float* base, int ld, int row0) {
+    const float* p = base + row0 * ld + (static_cast<int>(threadIdx.x) & 15);
+    return f32x4_t{p[0], p[ld], p[2 * ld], p[3 * ld]};
+  }
+  static __device__ __forceinline__ X round8(const float (&v)[8]) { return split(v); }
+  static __device__ __forceinline__ S split(const float (&v)[8]) {
+    S s;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = v[e];
+    return s;
+  }
+  static __device__ __forceinline__ X hi(const S& s) { return s; }
+  static __device__ __forceinline__ void pieces(const S& s, uint4 (&u)[2]) {
+    u[0] = __builtin_bit_cast(uint4, f32x4_t{s[0], s[1], s[2], s[3]});
+    u[1] = __builtin_bit_cast(uint4, f32x4_t{s[4], s[5], s[6], s[7]});
+  }
+  static __device__ __forceinline__ S from_pieces(const uint4 (&u)[2]) {
+    const f32x4_t a = __builtin_bit_cast(f32x4_t, u[0]), b = __builtin_bit_cast(f32x4_t, u[1]);
+    return S{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  }
+  static __device__ __forceinline__ void floats(const S& s, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = s[e];
+  }
+  static __device__ __forceinline__ void store(float* p, X x) {
+    *reinterpret_cast<f32x4_t*>(p) = f32x4_t{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
+  }
+};
+
+// acc += A B over the fragments' 32 contraction values
+__device__ __forceinline__ f32x4_t mma(bf16x8_t a, bf16x8_t b, f32x4_t c) { return ssd::Mma<bf16_t>::mma(a, b, c); }
+__device__ __forceinline__ f32x4_t mma(const Fr<bf16_t>::S& a, bf16x8_t b, f32x4_t c) { return mma(a.hi, b, mma(a.lo, b, c)); }
+__device__ __forceinline__ f32x4_t mma(bf16x8_t a, const Fr<bf16_t>::S& b, f32x4_t c) { return mma(a, b.hi, mma(a, b.lo, c)); }
+__device__ __forceinline__ f32x4_t mma(const Fr<bf16_t>::S& a, const Fr<bf16_t>::S& b, f32x4_t c) {
+  return mma(a.hi, b.hi, mma(a.hi, b.lo, mma(a.lo, b.hi, c)));
+}
+__device__ __forceinline__ f32x4_t mma(const f32x8_t& a, const f32x8_t& b, f32x4_t c) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c = ssd::Mma<float>::mma(a[e], b[e], c);
+  return c;
+}
+
+// first column of tile t among columns in pair order, for load_tr<8>
+__device__ __forceinline__ constexpr int pair_col(int t) { return 32 * (t >> 1) + 4 * (t & 1); }
+
+// a pair of accumulator tiles as 8 values in fragment order
+__device__ __forceinline__ void pair8(f32x4_t a, f32x4_t b, float (&v)[8]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) { v[r] = a[r]; v[4 + r] = b[r]; }
+}
+
+// A ROWS x COLS tile of rows `stride` elements apart, held in registers between its loads and its store
+// to LDS; rows >= nrows and columns >= ncols (a multiple of 16 bytes) are zero and not read.
+template <typename T, int ROWS, int COLS, int NTHR> struct Tile {
+  static constexpr int VEC = Vec16<T>::N, CV = COLS / VEC, NV = ROWS * CV, IT = (NV + NTHR - 1) / NTHR;
+  static constexpr int LD = COLS + VEC;   // row pitch in LDS: 16 bytes of padding
+  static constexpr int LDS_ELEMS = ROWS * LD;
+  uint4 buf[IT];
+  __device__ __forceinline__ void load(const T* base, int64_t stride, int nrows, int ncols) {
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = static_cast<int>(threadIdx.x) + k * NTHR, r = v / CV, cc = (v % CV) * VEC;
+      buf[k] = ssd::zero_u4();
+      if ((NV % NTHR == 0 || v < NV) && r < nrows && cc < ncols) buf[k] = ssd::ld_global16(base + r * stride + cc);
+    }
+  }
+  __device__ __forceinline__ void store(T* lds) const {
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = static_cast<int>(threadIdx.x) + k * NTHR;
+      if (NV % NTHR == 0 || v < NV) *reinterpret_cast<uint4*>(lds + (v / CV) * LD + (v % CV) * VEC) = buf[k];
+    }
+  }
+};
+
+// NV 16-byte pieces copied as they lie
+template <int NV, int NTHR> struct Pieces {
+  static constexpr int IT = (NV + NTHR - 1) / NTHR;
+  uint4 buf[IT];
+  __device__ __forceinline__ void load(const uint4* p) {
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = static_cast<int>(threadIdx.x) + k * NTHR;
+      if (NV % NTHR == 0 || v < NV) buf[k] = p[v];
+    }
+  }
+  __device__ __forceinline__ void store(uint4* lds) const {
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = static_cast<int>(threadIdx.x) + k * NTHR;
+      if (NV % NTHR == 0 || v < NV) lds[v] = buf[k];
+    }
+  }
+};
+
+// The six fragments of a lower (tile t, step ks <= t / 2) triangular 64 x 64 operand, and of an upper one
+// (ks >= t / 2): place of fragment (t, ks)
+__device__ __forceinline__ constexpr int lower_frag(int t, int ks) { return t < 2 ? t : 2 * t - 2 + ks; }
+__device__ __forceinline__ constexpr int upper_frag(int t, int ks) { return t < 2 ? 2 * t + ks : 2 + t; }
+constexpr int NFRAG = 6;
+constexpr int FRAG_PIECES = NFRAG * 2 * 64;   // 16-byte pieces of a split operand: [fragment][piece][lane]
+
+template <typename T> __device__ __forceinline__ typename Fr<T>::S load_frag(const uint4* frags, int f) {
+  const int l = static_cast<int>(threadIdx.x) & 63;
+  uint4 u[2] = {frags[(2 * f) * 64 + l], frags[(2 * f + 1) * 64 + l]};
+  return Fr<T>::from_pieces(u);
+}
+
+}  // namespace delta

@@ -1,0 +1,144 @@
+"""GPU parity of the per-head q/k norm with rotation, and of its gradients, with
+the fp64 oracle.
+
+Tolerances, on the 2-norm of the difference over that of the result: the
+float32 arithmetic of a row (a sum of N squares, the root, at most eight more
+operations; in the backward one more sum of N) is off by at most
+(2 N + 16) 2^-24, the cosine and sine by 2^-22 of one; bf16 outputs add their
+own rounding, 2^-8.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import qk_norm as on
+from state_space_model_mamba_amd import qk_norm
+
+pytestmark = pytest.mark.gpu
+IO = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def make(b, L, Gq, Gk, N, rot, io, seed=0, far=0, weights=True, gain=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(s, generator=gen)  # noqa: E731
+    t = IO[io]
+    d = {"q": (gain * rn(b, L, Gq, N)).to(t), "k": (gain * rn(b, L, Gk, N)).to(t) if Gk else None,
+         "q_weight": 1 + 0.2 * rn(N) if weights else None, "k_weight": 1 + 0.2 * rn(N) if weights and Gk else None,
+         "positions": None, "inv_freq": None}
+    if rot:
+        d["inv_freq"] = (10000.0 ** (-torch.arange(0, rot, 2).double() / rot)).float()
+        d["positions"] = torch.randint(-far, far + 1, (b, L), generator=gen).int()
+    d["dq"], d["dk"] = rn(b, L, Gq, N).to(t), rn(b, L, Gk, N).to(t) if Gk else None
+    return d
+
+
+def names(d):
+    return [d[k] for k in ("q", "k", "q_weight", "k_weight", "positions", "inv_freq")]
+
+
+def near(got, ref, N, label):
+    err = np.linalg.norm(f64(got) - ref) / max(np.linalg.norm(ref), 1e-30)
+    tol = (2 * N + 16) * 2.0 ** -24 + 2.0 ** -22 + (2.0 ** -8 if got.dtype == torch.bfloat16 else 0)
+    print(f"  {label}: {err:.2e} (tolerance {tol:.1e})", flush=True)
+    assert err <= tol, f"{label}: {err:.3e} > {tol:.3e}"
+
+
+def check(d, label, **kw):
+    print(f"[case] qk_norm {label} {kw}", flush=True)
+    c = {k: None if v is None else v.cuda() for k, v in d.items()}
+    y = qk_norm.qk_norm_rope_fwd(*names(c), **kw)
+    g = qk_norm.qk_norm_rope_bwd(*names(c), c["dq"], c["dk"], **kw)
+    torch.cuda.synchronize()
+    N = d["q"].shape[3]
+    for i, x in enumerate("qk"):
+        if d[x] is None:
+            assert y[i] is None and g["d" + x] is None
+            continue
+        rest = (f64(d[x + "_weight"]), f64(d["positions"]), f64(d["inv_freq"]))
+        near(y[i], on.forward(f64(d[x]), *rest, **kw), N, x)
+        dx, dw = on.backward(f64(d[x]), *rest, f64(d["d" + x]), **kw)
+        near(g["d" + x], dx, N, "d" + x)
+        if d[x + "_weight"] is not None:
+            near(g[f"d{x}_weight"], dw, N, f"d{x}_weight")
+        else:
+            assert g[f"d{x}_weight"] is None
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("b,L,Gq,Gk,N,rot", [
+    (1, 1, 1, 1, 8, 8), (2, 3, 3, 1, 16, 0), (1, 5, 4, 2, 40, 20), (2, 7, 8, 8, 64, 32), (1, 33, 5, 3, 96, 96), (3, 50, 2, 2, 128, 128),
+    (1, 9, 1, 0, 256, 128), (1, 20, 6, 6, 200, 6)])
+def test_shapes(b, L, Gq, Gk, N, rot, interleaved, io):
+    check(make(b, L, Gq, Gk, N, rot, io, seed=N + rot, far=5000), f"{io} b={b} L={L} {Gq}+{Gk}x{N} rot={rot}",
+          interleaved=interleaved, norm="l2" if L % 2 else "rms")
+
+
+def test_far_positions_keep_their_angles():
+    check(make(1, 64, 2, 2, 64, 64, "f32", seed=1, far=2 ** 31 - 1), "far")
+
+
+def test_many_positions():
+    check(make(1, 5000, 3, 2, 32, 16, "f32", seed=2, far=100), "5000 positions")
+    check(make(2, 9000, 1, 1, 16, 16, "bf16", seed=3, far=100, weights=False), "18000 positions, no weights")
+
+
+@pytest.mark.parametrize("gain", [1e-20, 1e15])
+def test_values_far_from_one(gain):
+    # squares of 1e-20 vanish against eps (rms of 1e-20 against 1e-3), those of 1e15 stay in range
+    check(make(1, 4, 2, 1, 32, 8, "bf16", seed=4, gain=gain), f"gain {gain}", eps=1e-6)
+
+
+def test_zero_rows_and_no_positions():
+    d = make(1, 6, 2, 1, 16, 8, "f32", seed=5)
+    d["q"][0, 2] = 0
+    d["positions"] = None
+    c = {k: None if v is None else v.cuda() for k, v in d.items()}
+    y = qk_norm.qk_norm_rope_fwd(*names(c))
+    at = torch.arange(6, dtype=torch.int32, device="cuda")[None].contiguous()
+    z = qk_norm.qk_norm_rope_fwd(c["q"], c["k"], c["q_weight"], c["k_weight"], at, c["inv_freq"])
+    torch.cuda.synchronize()
+    assert torch.equal(y[0], z[0]) and torch.equal(y[1], z[1]) and bool((y[0][0, 2] == 0).all())
+
+
+def test_slices_of_wider_rows_and_bits_on_repeat():
+    d = {k: None if v is None else v.cuda() for k, v in make(2, 300, 4, 2, 64, 32, "bf16", seed=6, far=99).items()}
+    row = torch.cat([d["k"].flatten(2), d["q"].flatten(2)], -1)
+    s = dict(d, k=row[..., :128].unflatten(-1, (2, 64)), q=row[..., 128:].unflatten(-1, (4, 64)))
+    first = None
+    for x in (d, s, d):
+        y = qk_norm.qk_norm_rope_fwd(*names(x))
+        g = qk_norm.qk_norm_rope_bwd(*names(x), d["dq"], d["dk"])
+        ws = torch.randint(0, 256, (1 << 20,), dtype=torch.uint8, device="cuda")
+        g = qk_norm.qk_norm_rope_bwd(*names(x), d["dq"], d["dk"], workspace=ws)
+        out = [*y, g["dq"], g["dk"], g["dq_weight"], g["dk_weight"]]
+        first = first or out
+        assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
+def test_autograd_and_a_replayed_graph():
+    d = {k: None if v is None else v.cuda() for k, v in make(1, 40, 4, 2, 32, 32, "bf16", seed=7, far=9).items()}
+    leaves = [d[k].clone().requires_grad_(True) for k in ("q", "k", "q_weight", "k_weight")]
+    y = qk_norm.qk_norm_rope(*leaves, d["positions"], d["inv_freq"])
+    got = torch.autograd.grad(y, leaves, (d["dq"], d["dk"]))
+    g = qk_norm.qk_norm_rope_bwd(*names(d), d["dq"], d["dk"])
+    for a, k in zip(got, ("dq", "dk", "dq_weight", "dk_weight")):
+        assert torch.equal(a, g[k]), k
+    del y, got
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        z = qk_norm.qk_norm_rope_fwd(*names(d))
+        r = qk_norm.qk_norm_rope_bwd(*names(d), d["dq"], d["dk"])
+    ref = qk_norm.qk_norm_rope_fwd(*names(d))
+    for turn in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(z[0], ref[0]) and torch.equal(z[1], ref[1]), turn
+        assert all(torch.equal(r[k], g[k]) for k in ("dq", "dk", "dq_weight", "dk_weight")), turn
+        for t in (*z, *r.values()):
+            t.zero_()

@@ -45,7 +45,7 @@ size_t place(Problem& p, int io, bool backward, char* base) {
     at += (bytes + 255) / 256 * 256;
     return r;
   };
-  const size_t sh = static_cast<size_t>(p.nslots) * p.H, rows = static_cast<size_t>(p.np) * delta::PS;
+  const size_t sh = static_cast<size_t>(p.nslots) * p.H, rows = static_cast<size_t>(p.rows);
   const size_t nd = p.N <= 64 ? 64 : 128, io_size = io == SSD_IO_BF16 ? 2 : 4, frags = sh * delta::FRAG_PIECES * 16;
   p.starts = reinterpret_cast<int32_t*>(take((static_cast<size_t>(p.nseqs) + 1) * 4));
   p.gates = reinterpret_cast<float*>(take(sh * delta::GATES * delta::CH * 4));
@@ -58,10 +58,10 @@ size_t place(Problem& p, int io, bool backward, char* base) {
     p.u = take(sh * rows * delta::CH * io_size);
     p.s = take(sh * rows * nd * 4);
     p.ds = take(sh * rows * nd * io_size);
-    p.oo = reinterpret_cast<float*>(take(sh * p.np * delta::CH * 4));
-    p.dd = reinterpret_cast<float*>(take(sh * p.np * delta::CH * 4));
-    p.be = reinterpret_cast<float*>(take(sh * p.np * delta::CH * 4));
-    p.phi = reinterpret_cast<float*>(take(sh * p.np * 4));
+    p.oo = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));
+    p.vv = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));
+    p.be = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));
+    p.phi = reinterpret_cast<float*>(take(sh * p.nsl * 4));
   }
   return at;
 }
@@ -78,7 +78,8 @@ Problem problem(const delta_shape& s) {
   p.hpg = p.H / p.G;
   p.total = p.B * p.L;
   p.nslots = p.total / delta::CH + p.nseqs;
-  p.np = (p.P + delta::PS - 1) / delta::PS;
+  p.rows = (p.P + delta::PAD - 1) / delta::PAD * delta::PAD;
+  p.nsl = p.rows / delta::SLICE;
   p.scale = s.scale;
   int64_t st[6];
   delta_strides(s, st);
@@ -148,7 +149,8 @@ int delta_bwd(const delta_shape* shape, const void* q, const void* k, const void
   if ((rc = delta::launch_prep(p, io, true, st)) != SSD_OK) return rc;
   if ((rc = delta::launch_walk(p, io, true, st)) != SSD_OK) return rc;
   if ((rc = delta::launch_rwalk(p, io, st)) != SSD_OK) return rc;
-  return delta::launch_grad(p, io, st);
+  if ((rc = delta::launch_grad(p, io, st)) != SSD_OK) return rc;
+  return delta::launch_gates(p, st);
 }
 
 }  // extern "C"

@@ -6,14 +6,16 @@
 
 namespace delta {
 
-constexpr int PS = 64;   // value columns of a walk's block (16 per wave)
+constexpr int SLICE = 16;   // value columns of a state wave
+constexpr int PAD = 32;     // the workspace's value columns are a multiple of this
 
 struct Problem {
   // sizes
   int B, L, H, P, G, N, nseqs, hpg;
   int total;      // B * L rows
   int nslots;     // chunk slots: the chunks of sequence s are slots start(s) / 64 + s, ...
-  int np;         // blocks of PS value columns
+  int rows;       // P rounded up to a multiple of PAD
+  int nsl;        // slices of 16 value columns: rows / SLICE
   float scale;
   int64_t q_sb, q_sl, k_sb, k_sl, v_sb, v_sl;
   // inputs
@@ -26,18 +28,18 @@ struct Problem {
   // workspace
   int32_t* starts;   // (nseqs + 1) first rows (seq_idx given)
   float* gates;      // (slots, H, GATES, 64)
-  uint4* tf;         // (slots, H, FRAG_PIECES): T' = (I + N diag(beta))^-1, rows in pair order
+  uint4* tf;         // (slots, H, FRAG_PIECES): T' - I, T' = (I + N diag(beta))^-1, rows in pair order
   uint4* pf;         // the same of the causal scores, rows in order
-  uint4* ttf;        // transposed (I + diag(beta) N)^-1, rows in pair order (backward)
+  uint4* ttf;        // transposed (I + diag(beta) N)^-1 - I, rows in pair order (backward)
   uint4* ptf;        // transposed scores, rows in pair order (backward)
-  uint4* e;          // (slots, H, np, 4 waves, 4, 64): the residuals, float32, accumulator layout (backward)
-  void* u;           // (slots, H, np * PS, 64) io dtype: beta * e, a column per row (backward)
-  void* s;           // (slots, H, np * PS, ND) 2 bf16 terms or float32: entering states (backward)
-  void* ds;          // (slots, H, np * PS, ND) io dtype: gradient of the state after the chunk (backward)
-  float* oo;         // (slots, H, np, 64): dout . o over the block's columns (backward)
-  float* dd;         // (slots, H, np, 64): dout . o - dv . v
-  float* be;         // (slots, H, np, 64): dbeta
-  float* phi;        // (slots, H, np): <entering state, its gradient>
+  uint4* e;          // (slots, H, nsl, 4, 64): the residuals, float32, accumulator layout (backward)
+  void* u;           // (slots, H, rows, 64) io dtype: beta * e, a column per row (backward)
+  void* s;           // (slots, H, rows, ND) 2 bf16 terms or float32: entering states (backward)
+  void* ds;          // (slots, H, rows, ND) io dtype: gradient of the state after the chunk (backward)
+  float* oo;         // (slots, H, nsl, 64): dout . o over the slice's columns (backward)
+  float* vv;         // (slots, H, nsl, 64): dv . v
+  float* be;         // (slots, H, nsl, 64): Du . e
+  float* phi;        // (slots, H, nsl): <entering state, its gradient>
 };
 
 // per slot and head: exp(c_i), exp(c_last - c_i), beta_i, and c_i in two floats
@@ -48,6 +50,7 @@ int launch_prep(const Problem& p, int io, bool backward, hipStream_t s);
 int launch_walk(const Problem& p, int io, bool backward, hipStream_t s);
 int launch_rwalk(const Problem& p, int io, hipStream_t s);
 int launch_grad(const Problem& p, int io, hipStream_t s);
+int launch_gates(const Problem& p, hipStream_t s);
 
 #ifdef __HIPCC__
 // first row of sequence s (s == nseqs: the end of the last)

@@ -12,11 +12,12 @@
 // the lane (as B: contraction over its rows; as A: its transpose).
 //
 // With bf16 io, float32 values that feed a state or a gate's gradient enter
-// a product as two bf16 terms, x = hi + lo + O(2^-17 |x|): one MFMA more per
+// a product as two bf16 terms, x = hi + lo + O(2^-16 |x|): one MFMA more per
 // product with an exact bf16 operand, two more per product of two such values
-// (lo * lo is dropped).  Single bf16 operands would leave the float32 outputs
-// 3e-3 off; measured error with two terms: 2e-6 .. 4e-6.  With f32 io every
-// product is v_mfma_f32_16x16x4_f32.
+// (lo * lo is dropped).  What is added to a state enters as three terms
+// (2^-24): with two there, states come out 2.6e-6 off, with three 0.8e-6, and
+// with single terms throughout 3e-3.  With f32 io every product is
+// v_mfma_f32_16x16x4_f32.
 #pragma once
 
 #include "ssd_device.h"
@@ -43,9 +44,11 @@ template <typename T> struct Fr;
 template <> struct Fr<bf16_t> {
   typedef bf16x8_t X;
   struct S { bf16x8_t hi, lo; };
-  static constexpr int NX = 1, NS = 2;   // 16-byte pieces of an X and of an S
+  struct S3 { bf16x8_t hi, mid, lo; };
   static __device__ __forceinline__ X zero() { return ssd::Mma<bf16_t>::zero(); }
   static __device__ __forceinline__ X load(const bf16_t* p) { return ssd::Mma<bf16_t>::load_k(p); }
+  // of a row with `left` > 0 values from here on (a multiple of 16 bytes)
+  static __device__ __forceinline__ X load_cols(const bf16_t* p, int) { return load(p); }
   // Rows row0 .. row0 + 3 of one column of a row-major LDS tile: column CS (c / 4) + c % 4 of base
   // (CS 4: 16 columns side by side; CS 8: the columns of a tile in pair order).
   template <int CS> static __device__ __forceinline__ ssd::s16x4_t tr4(const bf16_t* base, int ld, int row0) {
@@ -83,6 +86,18 @@ template <> struct Fr<bf16_t> {
     s.lo = round8(r);
     return s;
   }
+  static __device__ __forceinline__ S3 split3(const float (&v)[8]) {
+    S3 s;
+    s.hi = round8(v);
+    float h[8], r[8];
+    floats(s.hi, h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = v[e] - h[e];
+    const S t = split(r);
+    s.mid = t.hi;
+    s.lo = t.lo;
+    return s;
+  }
   static __device__ __forceinline__ X hi(const S& s) { return s.hi; }
   static __device__ __forceinline__ void pieces(const S& s, uint4 (&u)[2]) {
     u[0] = __builtin_bit_cast(uint4, s.hi);
@@ -113,13 +128,18 @@ template <> struct Fr<bf16_t> {
 template <> struct Fr<float> {
   typedef f32x8_t X;
   typedef f32x8_t S;
-  static constexpr int NX = 2, NS = 2;
+  typedef f32x8_t S3;
   static __device__ __forceinline__ X zero() { return X{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}; }
   static __device__ __forceinline__ X load(const float* p) {
     union { f32x4_t h[2]; X x; } u;
     u.h[0] = *reinterpret_cast<const f32x4_t*>(p);
     u.h[1] = *reinterpret_cast<const f32x4_t*>(p + 4);
     return u.x;
+  }
+  static __device__ __forceinline__ X load_cols(const float* p, int left) {
+    if (left > 4) return load(p);
+    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p);
+    return X{v[0], v[1], v[2], v[3], 0.f, 0.f, 0.f, 0.f};
   }
   template <int CS = 4> static __device__ __forceinline__ X load_tr(const float* base, int ld, int row0) {
     const int c = static_cast<int>(threadIdx.x) & 15;
@@ -140,6 +160,7 @@ template <> struct Fr<float> {
     for (int e = 0; e < 8; ++e) s[e] = v[e];
     return s;
   }
+  static __device__ __forceinline__ S3 split3(const float (&v)[8]) { return split(v); }
   static __device__ __forceinline__ X hi(const S& s) { return s; }
   static __device__ __forceinline__ void pieces(const S& s, uint4 (&u)[2]) {
     u[0] = __builtin_bit_cast(uint4, f32x4_t{s[0], s[1], s[2], s[3]});
@@ -166,6 +187,9 @@ __device__ __forceinline__ f32x4_t mma(bf16x8_t a, const Fr<bf16_t>::S& b, f32x4
 __device__ __forceinline__ f32x4_t mma(const Fr<bf16_t>::S& a, const Fr<bf16_t>::S& b, f32x4_t c) {
   return mma(a.hi, b.hi, mma(a.hi, b.lo, mma(a.lo, b.hi, c)));
 }
+__device__ __forceinline__ f32x4_t mma(bf16x8_t a, const Fr<bf16_t>::S3& b, f32x4_t c) {
+  return mma(a, b.hi, mma(a, b.mid, mma(a, b.lo, c)));
+}
 __device__ __forceinline__ f32x4_t mma(const f32x8_t& a, const f32x8_t& b, f32x4_t c) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) c = ssd::Mma<float>::mma(a[e], b[e], c);
@@ -182,46 +206,36 @@ __device__ __forceinline__ void pair8(f32x4_t a, f32x4_t b, float (&v)[8]) {
 }
 
 // A ROWS x COLS tile of rows `stride` elements apart, held in registers between its loads and its store
-// to LDS; rows >= nrows and columns >= ncols (a multiple of 16 bytes) are zero and not read.
+// to LDS by NTHR threads (tid: 0 .. NTHR - 1); rows >= nrows and columns >= ncols (a multiple of 16 bytes)
+// are zero and not read.  A thread's pieces share their column and lie STEP rows apart, so a whole tile
+// takes one vector offset and a uniform base per piece.
 template <typename T, int ROWS, int COLS, int NTHR> struct Tile {
-  static constexpr int VEC = Vec16<T>::N, CV = COLS / VEC, NV = ROWS * CV, IT = (NV + NTHR - 1) / NTHR;
+  static constexpr int VEC = Vec16<T>::N, CV = COLS / VEC, STEP = NTHR / CV, IT = ROWS / STEP;
+  static_assert(NTHR % CV == 0 && ROWS % STEP == 0, "tile");
   static constexpr int LD = COLS + VEC;   // row pitch in LDS: 16 bytes of padding
   static constexpr int LDS_ELEMS = ROWS * LD;
-  uint4 buf[IT];
-  __device__ __forceinline__ void load(const T* base, int64_t stride, int nrows, int ncols) {
+  f32x4_t buf[IT];
+  // base: uniform; stride * ROWS elements span less than 2^31 bytes
+  __device__ __forceinline__ void load(const T* base, int64_t stride, int nrows, int ncols, int tid) {
+    const int r = tid / CV, cc = (tid % CV) * VEC;
+    const uint32_t off = static_cast<uint32_t>(r * static_cast<uint32_t>(stride) + cc) * static_cast<uint32_t>(sizeof(T));
+    const char* at = reinterpret_cast<const char*>(base);
+    const int64_t step = STEP * stride * static_cast<int64_t>(sizeof(T));
+    if (nrows >= ROWS && ncols >= COLS) {
 #pragma unroll
-    for (int k = 0; k < IT; ++k) {
-      const int v = static_cast<int>(threadIdx.x) + k * NTHR, r = v / CV, cc = (v % CV) * VEC;
-      buf[k] = ssd::zero_u4();
-      if ((NV % NTHR == 0 || v < NV) && r < nrows && cc < ncols) buf[k] = ssd::ld_global16(base + r * stride + cc);
+      for (int k = 0; k < IT; ++k) buf[k] = *reinterpret_cast<const f32x4_t*>(at + k * step + off);
+    } else {
+#pragma unroll
+      for (int k = 0; k < IT; ++k) {
+        buf[k] = zero4();
+        if (r + k * STEP < nrows && cc < ncols) buf[k] = *reinterpret_cast<const f32x4_t*>(at + k * step + off);
+      }
     }
   }
-  __device__ __forceinline__ void store(T* lds) const {
+  __device__ __forceinline__ void store(T* lds, int tid) const {
+    T* d = lds + (tid / CV) * LD + (tid % CV) * VEC;
 #pragma unroll
-    for (int k = 0; k < IT; ++k) {
-      const int v = static_cast<int>(threadIdx.x) + k * NTHR;
-      if (NV % NTHR == 0 || v < NV) *reinterpret_cast<uint4*>(lds + (v / CV) * LD + (v % CV) * VEC) = buf[k];
-    }
-  }
-};
-
-// NV 16-byte pieces copied as they lie
-template <int NV, int NTHR> struct Pieces {
-  static constexpr int IT = (NV + NTHR - 1) / NTHR;
-  uint4 buf[IT];
-  __device__ __forceinline__ void load(const uint4* p) {
-#pragma unroll
-    for (int k = 0; k < IT; ++k) {
-      const int v = static_cast<int>(threadIdx.x) + k * NTHR;
-      if (NV % NTHR == 0 || v < NV) buf[k] = p[v];
-    }
-  }
-  __device__ __forceinline__ void store(uint4* lds) const {
-#pragma unroll
-    for (int k = 0; k < IT; ++k) {
-      const int v = static_cast<int>(threadIdx.x) + k * NTHR;
-      if (NV % NTHR == 0 || v < NV) lds[v] = buf[k];
-    }
+    for (int k = 0; k < IT; ++k) *reinterpret_cast<f32x4_t*>(d + k * STEP * LD) = buf[k];
   }
 };
 
@@ -232,10 +246,40 @@ __device__ __forceinline__ constexpr int upper_frag(int t, int ks) { return t < 
 constexpr int NFRAG = 6;
 constexpr int FRAG_PIECES = NFRAG * 2 * 64;   // 16-byte pieces of a split operand: [fragment][piece][lane]
 
-template <typename T> __device__ __forceinline__ typename Fr<T>::S load_frag(const uint4* frags, int f) {
+// fragment f of a split operand's pieces in memory
+template <typename T> __device__ __forceinline__ typename Fr<T>::S frag_at(const uint4* frags, int f) {
   const int l = static_cast<int>(threadIdx.x) & 63;
-  uint4 u[2] = {frags[(2 * f) * 64 + l], frags[(2 * f + 1) * 64 + l]};
-  return Fr<T>::from_pieces(u);
+  const uint4 v[2] = {frags[2 * f * 64 + l], frags[(2 * f + 1) * 64 + l]};
+  return Fr<T>::from_pieces(v);
 }
+
+// NV 16-byte pieces copied as they lie by NTHR threads
+template <int NV, int NTHR> struct Pieces {
+  static constexpr int IT = NV / NTHR;
+  static_assert(NV % NTHR == 0, "pieces");
+  f32x4_t buf[IT];
+  __device__ __forceinline__ void load(const uint4* p, int tid) {
+#pragma unroll
+    for (int k = 0; k < IT; ++k) buf[k] = reinterpret_cast<const f32x4_t*>(p)[tid + k * NTHR];
+  }
+  __device__ __forceinline__ void store(uint4* lds, int tid) const {
+#pragma unroll
+    for (int k = 0; k < IT; ++k) reinterpret_cast<f32x4_t*>(lds)[tid + k * NTHR] = buf[k];
+  }
+};
+
+// a split operand's fragments in registers, requested from global memory ahead of their use
+struct FragRegs {
+  uint4 u[2 * NFRAG];
+  __device__ __forceinline__ void request(const uint4* frags) {
+    const int l = static_cast<int>(threadIdx.x) & 63;
+#pragma unroll
+    for (int i = 0; i < 2 * NFRAG; ++i) u[i] = frags[i * 64 + l];
+  }
+  template <typename T> __device__ __forceinline__ typename Fr<T>::S get(int f) const {
+    const uint4 v[2] = {u[2 * f], u[2 * f + 1]};
+    return Fr<T>::from_pieces(v);
+  }
+};
 
 }  // namespace delta

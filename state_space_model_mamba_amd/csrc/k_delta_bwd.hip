@@ -27,222 +27,411 @@ namespace delta {
 
 // ---------------------------------------------------------------------------
 // k_delta_rwalk: one sequence's chunks from the last to the first, for one
-// head and 64 of its value columns, 16 per wave, the wave's columns of dS in
-// registers throughout (as the forward walk holds S).
+// head and PS of its value columns, with roles as in the forward walk: a state
+// wave keeps 16 columns of dS in registers and runs the sequential part,
+//     k dS -> du -> Du -> dS,
+// while beside the two of them
+//   * one wave forms ahead what does not need dS, for chunk i - 1: the scores'
+//     part of du, and q^T dout,
+//   * a wave each follows behind with what Du gives, for chunk i + 1: dv, the
+//     row sums for the gates' gradients, and the stores,
+//   * one wave stages the coming chunks' rows in LDS.
 // ---------------------------------------------------------------------------
 template <typename T, int NT> struct RwalkCfg {
-  static constexpr int ND = 32 * NT;
-  using TileN = Tile<T, CH, ND, 256>;
-  using TileP = Tile<T, CH, PS, 256>;
-  static constexpr size_t OFF_Q = sizeof(T) * TileN::LDS_ELEMS;
-  static constexpr size_t OFF_V = 2 * OFF_Q;
-  static constexpr size_t OFF_DO = OFF_V + sizeof(T) * TileP::LDS_ELEMS;
-  static constexpr size_t OFF_T = OFF_DO + sizeof(T) * TileP::LDS_ELEMS;
-  static constexpr size_t OFF_P = OFF_T + 16 * FRAG_PIECES;
-  static constexpr size_t OFF_G = OFF_P + 16 * FRAG_PIECES;
-  static constexpr size_t OFF_R = OFF_G + sizeof(float) * 3 * CH;
-  static constexpr size_t LDS = OFF_R + sizeof(float) * (8 * CH + 4);
+  static constexpr int ND = 32 * NT, NSW = 2, PS = SLICE * NSW, HT = 64, THREADS = 64 * (2 * NSW + 2);
+  using TileN = Tile<T, CH, ND, HT>;
+  using TileP = Tile<T, CH, PS, HT>;
+  static constexpr size_t N_BYTES = sizeof(T) * TileN::LDS_ELEMS, P_BYTES = sizeof(T) * TileP::LDS_ELEMS;
+  // k and q twice, staged while the others work; 512-byte rows once, staged between the chunks
+  static constexpr int KBUF = sizeof(T) * ND <= 256 ? 2 : 1;
+  static constexpr size_t OFF_Q = KBUF * N_BYTES;
+  static constexpr size_t OFF_DO = 2 * OFF_Q;
+  static constexpr size_t OFF_V = OFF_DO + 2 * P_BYTES;
+  static constexpr size_t OFF_D0 = OFF_V + 2 * P_BYTES;      // scores^T dout
+  static constexpr size_t OFF_Q0 = OFF_D0 + 16 * 64 * NSW * 4;
+  static constexpr size_t OFF_DU = OFF_Q0 + 16 * 64 * NSW * 2 * NT;
+  static constexpr size_t OFF_XS = OFF_DU + 16 * 64 * NSW * 4;
+  static constexpr size_t OFF_G = OFF_XS + 16 * 64 * NSW * NT * 2;
+  static constexpr size_t LDS = OFF_G + 4 * sizeof(float) * 3 * CH;   // the gates of four chunks
 };
 
-template <typename T, int NT> __global__ __launch_bounds__(256) void k_delta_rwalk(Problem p) {
+template <typename T, int NT> __global__ __launch_bounds__(64 * 6) void k_delta_rwalk(Problem p) {
   using Cf = RwalkCfg<T, NT>;
   using F = Fr<T>;
   using TileN = typename Cf::TileN;
   using TileP = typename Cf::TileP;
-  constexpr int ND = Cf::ND, LDN = TileN::LD, LDP = TileP::LD;
+  constexpr int ND = Cf::ND, LDN = TileN::LD, LDP = TileP::LD, NSW = Cf::NSW, PS = Cf::PS, KB = Cf::KBUF - 1;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  T* kt = reinterpret_cast<T*>(smem);
-  T* qt = reinterpret_cast<T*>(smem + Cf::OFF_Q);
-  T* vt = reinterpret_cast<T*>(smem + Cf::OFF_V);
-  T* dot = reinterpret_cast<T*>(smem + Cf::OFF_DO);
-  uint4* tfr = reinterpret_cast<uint4*>(smem + Cf::OFF_T);
-  uint4* pfr = reinterpret_cast<uint4*>(smem + Cf::OFF_P);
-  float* gs = reinterpret_cast<float*>(smem + Cf::OFF_G);
-  float* red = reinterpret_cast<float*>(smem + Cf::OFF_R);   // [4 waves][64]: dv . v, then Du . e; then <S, dS>
+  auto kbuf = [&](int i) { return reinterpret_cast<T*>(smem + (i & KB) * Cf::N_BYTES); };
+  auto qbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_Q + (i & KB) * Cf::N_BYTES); };
+  auto dobuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_DO + (i & 1) * Cf::P_BYTES); };
+  auto vbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_V + (i & 1) * Cf::P_BYTES); };
+  auto gbuf = [&](int i) { return reinterpret_cast<float*>(smem + Cf::OFF_G) + (i & 3) * 3 * CH; };
+  f32x4_t* xd0 = reinterpret_cast<f32x4_t*>(smem + Cf::OFF_D0);   // [wave][t][lane]
+  f32x4_t* xq0 = reinterpret_cast<f32x4_t*>(smem + Cf::OFF_Q0);   // [wave][j][lane]
+  f32x4_t* xdu = reinterpret_cast<f32x4_t*>(smem + Cf::OFF_DU);   // [wave][t][lane]
+  uint4* xs = reinterpret_cast<uint4*>(smem + Cf::OFF_XS);        // [wave][q][term][lane]
 
-  const int h = static_cast<int>(blockIdx.x) / p.np, ps = static_cast<int>(blockIdx.x) % p.np;
+  const int np = (p.P + PS - 1) / PS;
+  const int h = static_cast<int>(blockIdx.x) / np, ps = static_cast<int>(blockIdx.x) % np;
   const int seq = static_cast<int>(blockIdx.y), grp = h / p.hpg;
   const int s0 = seq_start(p, seq), s1 = seq_start(p, seq + 1);
-  const int nchunk = (s1 - s0 + CH - 1) / CH, slot0 = slot_base(s0, seq);
+  const int nchunk = (s1 - s0 + CH - 1) / CH, slot0 = slot_base(s0, seq), last = nchunk - 1;
   const int tid = static_cast<int>(threadIdx.x), l = tid & 63, g = l >> 4, c = l & 15, w = ssd::wave_id_s();
-  const int col = PS * ps + 16 * w + c;
-  const int pcols = min(PS, p.P - PS * ps);
-  const int64_t state_at = ((static_cast<int64_t>(seq) * p.H + h) * p.P + col) * p.N;
+  auto slot_head = [&](int i) { return static_cast<int64_t>(slot0 + i) * p.H + h; };
+  auto length = [&](int i) { return min(CH, s1 - s0 - CH * i); };
 
-  f32x4_t S[2 * NT];   // dS
-#pragma unroll
-  for (int j = 0; j < 2 * NT; ++j) {
-    const int n = pair_col(j) + 8 * g;
-    S[j] = zero4();
-    if (p.dfinal && col < p.P && n < p.N) S[j] = *reinterpret_cast<const f32x4_t*>(p.dfinal + state_at + n);
-  }
-
-  const T* kp = static_cast<const T*>(p.k);
-  const T* qp = static_cast<const T*>(p.q);
-  const T* vp = static_cast<const T*>(p.v);
-  if (nchunk) {
-    kp += row_offset(s0, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N;
-    qp += row_offset(s0, p.L, p.q_sb, p.q_sl) + static_cast<int64_t>(grp) * p.N;
-    vp += row_offset(s0, p.L, p.v_sb, p.v_sl) + static_cast<int64_t>(h) * p.P + PS * ps;
-  }
-  const int64_t hp = static_cast<int64_t>(p.H) * p.P;
-  TileN tk, tq;
-  TileP tv, td;
-  Pieces<FRAG_PIECES, 256> tt, tp;
-  uint4 te[4];
-  float tg = 0.f;
-  auto request = [&](int i) {
-    const int len = min(CH, s1 - s0 - CH * i);
-    const int64_t sh = static_cast<int64_t>(slot0 + i) * p.H + h;
-    const int64_t row = static_cast<int64_t>(CH) * i;
-    tk.load(kp + row * p.k_sl, p.k_sl, len, p.N);
-    tq.load(qp + row * p.q_sl, p.q_sl, len, p.N);
-    tv.load(vp + row * p.v_sl, p.v_sl, len, pcols);
-    td.load(static_cast<const T*>(p.dout) + (s0 + row) * hp + static_cast<int64_t>(h) * p.P + PS * ps, hp, len, pcols);
-    tt.load(p.ttf + sh * FRAG_PIECES);
-    tp.load(p.ptf + sh * FRAG_PIECES);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) te[t] = p.e[((((sh * p.np + ps) * 4 + w) * 4) + t) * 64 + l];
-    if (tid < 3 * CH) tg = p.gates[sh * (GATES * CH) + tid];
-  };
-  if (nchunk) request(nchunk - 1);
-
-  for (int i = nchunk - 1; i >= 0; --i) {
-    const int len = min(CH, s1 - s0 - CH * i);
-    const int64_t sh = static_cast<int64_t>(slot0 + i) * p.H + h;
-    const int64_t rows = static_cast<int64_t>(p.np) * PS;
-    tk.store(kt);
-    tq.store(qt);
-    tv.store(vt);
-    td.store(dot);
-    tt.store(tfr);
-    tp.store(pfr);
-    f32x4_t e[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) e[t] = __builtin_bit_cast(f32x4_t, te[t]);
-    if (tid < 3 * CH) gs[tid] = tg;
-    __syncthreads();
-    if (i > 0) request(i - 1);
-
-    typename F::S sf[NT];
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      float v[8];
-      pair8(S[2 * q], S[2 * q + 1], v);
-      sf[q] = F::split(v);
-      F::store(static_cast<T*>(p.ds) + (sh * rows + col) * ND + 32 * q + 8 * g, F::hi(sf[q]));
-    }
-    typename F::X xd[2];   // dout: rows 32 ks + 8 g + e of this lane's column
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) xd[ks] = F::load_tr(dot + 16 * w, LDP, 32 * ks + 8 * g);
-    f32x4_t x[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      f32x4_t acc = zero4();
-#pragma unroll
-      for (int q = 0; q < NT; ++q) acc = mma(F::load(kt + perm_row(t, c) * LDN + 32 * q + 8 * g), sf[q], acc);
-      acc *= *reinterpret_cast<const f32x4_t*>(gs + GATE_OUT * CH + pair_col(t) + 8 * g);
-#pragma unroll
-      for (int ks = (t >> 1); ks < 2; ++ks) acc = mma(load_frag<T>(pfr, upper_frag(t, ks)), xd[ks], acc);
-      x[t] = acc;
-    }
-    typename F::S f2[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      float v[8];
-      pair8(x[2 * q], x[2 * q + 1], v);
-      f2[q] = F::split(v);
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      f32x4_t acc = zero4();
-#pragma unroll
-      for (int ks = (t >> 1); ks < 2; ++ks) acc = mma(load_frag<T>(tfr, upper_frag(t, ks)), f2[ks], acc);
-      const int row = pair_col(t) + 8 * g;
-      x[t] = acc * *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + row);   // dv
-      const f32x4_t v = F::load4_tr(vt + 16 * w, LDP, row);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float dvv = ssd::sum16(x[t][r] * v[r]), due = ssd::sum16(acc[r] * e[t][r]);
-        if (c == 0) {
-          red[w * CH + row + r] = dvv;
-          red[(4 + w) * CH + row + r] = due;
-        }
-        if (row + r < len && col < p.P)
-          static_cast<T*>(p.dv)[(s0 + static_cast<int64_t>(CH) * i + row + r) * hp + static_cast<int64_t>(h) * p.P + col] = ssd::Elem<T>::from_f(x[t][r]);
-      }
-    }
-    // dS <- exp(c_last) dS + q^T (scale exp(c) dout) - k^T (exp(c) dv)
-    typename F::S fd[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const f32x4_t i0 = *reinterpret_cast<const f32x4_t*>(gs + GATE_IN * CH + 32 * q + 8 * g);
-      const f32x4_t i1 = *reinterpret_cast<const f32x4_t*>(gs + GATE_IN * CH + 32 * q + 8 * g + 4);
-      float v[8], d[8];
-      pair8(-i0 * x[2 * q], -i1 * x[2 * q + 1], v);
-      f2[q] = F::split(v);
-      F::floats(xd[q], d);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        d[r] *= p.scale * i0[r];
-        d[4 + r] *= p.scale * i1[r];
-      }
-      fd[q] = F::split(d);
-    }
-    const float last = gs[GATE_IN * CH + CH - 1];
-#pragma unroll
-    for (int j = 0; j < 2 * NT; ++j) {
-      f32x4_t acc = last * S[j];
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        acc = mma(F::template load_tr<8>(qt + pair_col(j), LDN, 32 * ks + 8 * g), fd[ks], acc);
-        acc = mma(F::template load_tr<8>(kt + pair_col(j), LDN, 32 * ks + 8 * g), f2[ks], acc);
-      }
-      S[j] = acc;
-    }
-    // <entering state, its gradient>
-    float phi = 0.f;
-    const char* sb = static_cast<const char*>(p.s) + sh * rows * ND * 4;
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      uint4 u[2];
-      if constexpr (sizeof(T) == 2) {
-        u[0] = *reinterpret_cast<const uint4*>(sb + (static_cast<int64_t>(col) * ND + 32 * q + 8 * g) * 2);
-        u[1] = *reinterpret_cast<const uint4*>(sb + ((rows + col) * ND + 32 * q + 8 * g) * 2);
-      } else {
-        const uint4* d = reinterpret_cast<const uint4*>(sb + (static_cast<int64_t>(col) * ND + 32 * q + 8 * g) * 4);
-        u[0] = d[0];
-        u[1] = d[1];
-      }
-      float v[8];
-      F::floats(F::from_pieces(u), v);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) phi += v[r] * S[2 * q][r] + v[4 + r] * S[2 * q + 1][r];
-    }
-    phi = ssd::wave_sum(phi);
-    if (l == 0) red[8 * CH + w] = phi;
-    __syncthreads();
-    const int64_t at = (sh * p.np + ps) * CH;
-    if (tid < CH) {
-      p.dd[at + tid] = p.oo[at + tid] - (((red[tid] + red[CH + tid]) + red[2 * CH + tid]) + red[3 * CH + tid]);
-      if (tid == 0) p.phi[sh * p.np + ps] = ((red[8 * CH] + red[8 * CH + 1]) + red[8 * CH + 2]) + red[8 * CH + 3];
-    } else if (tid < 2 * CH) {
-      const float* r = red + 4 * CH + tid - CH;
-      p.be[at + tid - CH] = ((r[0] + r[CH]) + r[2 * CH]) + r[3 * CH];
-    }
-  }
-
-  if (p.dinit && col < p.P) {
+  if (w < NSW) {
+    // ---- state waves
+    const int col = PS * ps + SLICE * w + c;
+    const int64_t state_at = ((static_cast<int64_t>(seq) * p.H + h) * p.P + col) * p.N;
+    f32x4_t S[2 * NT];   // dS
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
       const int n = pair_col(j) + 8 * g;
-      if (n < p.N) *reinterpret_cast<f32x4_t*>(p.dinit + state_at + n) = S[j];
+      S[j] = zero4();
+      if (p.dfinal && col < p.P && n < p.N) S[j] = *reinterpret_cast<const f32x4_t*>(p.dfinal + state_at + n);
     }
+    if (nchunk) {
+      typename F::S sf[NT];
+      auto split_state = [&](int q) {
+        float v[8];
+        pair8(S[2 * q], S[2 * q + 1], v);
+        sf[q] = F::split(v);
+      };
+#pragma unroll
+      for (int q = 0; q < NT; ++q) split_state(q);
+      FragRegs tf;
+      tf.request(p.ttf + slot_head(last) * FRAG_PIECES);
+      __syncthreads();
+      __syncthreads();
+      for (int i = last; i >= 0; --i) {
+        const T* kt = kbuf(i);
+        const float* gs = gbuf(i);
+        f32x4_t d0[4], q0[2 * NT];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) d0[t] = xd0[(w * 4 + t) * 64 + l];
+#pragma unroll
+        for (int j = 0; j < 2 * NT; ++j) q0[j] = xq0[(w * 2 * NT + j) * 64 + l];
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          uint4 u[2];
+          F::pieces(sf[q], u);
+          xs[((w * NT + q) * 2 + 0) * 64 + l] = u[0];
+          xs[((w * NT + q) * 2 + 1) * 64 + l] = u[1];
+        }
+        f32x4_t x[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x[t] = zero4();
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) x[t] = mma(F::load(kt + perm_row(t, c) * LDN + 32 * q + 8 * g), sf[q], x[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          x[t] = x[t] * *reinterpret_cast<const f32x4_t*>(gs + GATE_OUT * CH + pair_col(t) + 8 * g) + d0[t];
+        // Du = du + (T^T - I) du
+        typename F::S f2[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float v[8];
+          pair8(x[2 * q], x[2 * q + 1], v);
+          f2[q] = F::split(v);
+        }
+#pragma unroll
+        for (int ks = 1; ks >= 0; --ks) {
+#pragma unroll
+          for (int t = 0; t < 2 * ks + 2; ++t) x[t] = mma(tf.get<T>(upper_frag(t, ks)), f2[ks], x[t]);
+        }
+        if (i > 0) tf.request(p.ttf + slot_head(i - 1) * FRAG_PIECES);
+        // dS <- exp(c_last) dS + q^T (scale exp(c) dout) - k^T (exp(c) beta Du)
+        typename F::S3 f3[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int row = 32 * q + 8 * g;
+          xdu[(w * 4 + 2 * q) * 64 + l] = x[2 * q];
+          xdu[(w * 4 + 2 * q + 1) * 64 + l] = x[2 * q + 1];
+          float v[8];
+          pair8(-x[2 * q] * *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + row) * *reinterpret_cast<const f32x4_t*>(gs + GATE_IN * CH + row),
+                -x[2 * q + 1] * *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + row + 4) *
+                    *reinterpret_cast<const f32x4_t*>(gs + GATE_IN * CH + row + 4), v);
+          f3[q] = F::split3(v);
+        }
+        const float dec = gs[GATE_IN * CH + CH - 1];
+#pragma unroll
+        for (int j = 0; j < 2 * NT; ++j) {
+          S[j] = dec * S[j] + q0[j];
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) S[j] = mma(F::template load_tr<8>(kt + pair_col(j), LDN, 32 * ks + 8 * g), f3[ks], S[j]);
+          if (j & 1) split_state(j >> 1);
+        }
+        __syncthreads();
+      }
+      // the first chunk's <entering state, its gradient>: the entering state is the initial state
+      float phi = 0.f;
+      if (p.h0 && col < p.P) {
+#pragma unroll
+        for (int j = 0; j < 2 * NT; ++j) {
+          const int n = pair_col(j) + 8 * g;
+          if (n < p.N) {
+            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p.h0 + state_at + n) * S[j];
+            phi += (v[0] + v[1]) + (v[2] + v[3]);
+          }
+        }
+      }
+      phi = ssd::wave_sum(phi);
+      if (l == 0) p.phi[slot_head(0) * p.nsl + ps * NSW + w] = phi;
+    }
+    if (p.dinit && col < p.P) {
+#pragma unroll
+      for (int j = 0; j < 2 * NT; ++j) {
+        const int n = pair_col(j) + 8 * g;
+        if (n < p.N) *reinterpret_cast<f32x4_t*>(p.dinit + state_at + n) = S[j];
+      }
+    }
+    return;
+  }
+  if (nchunk == 0) return;
+  const int64_t hp = static_cast<int64_t>(p.H) * p.P;
+
+  if (w == NSW) {
+    // ---- the wave ahead
+    FragRegs pf;
+    auto ahead = [&](int i) {
+      const T *dot = dobuf(i), *qt = qbuf(i);
+      const float* gs = gbuf(i);
+      typename F::X xd[NSW][2];   // dout: rows 32 ks + 8 g + e of column c of each slice
+      typename F::S3 fd[NSW][2];
+#pragma unroll
+      for (int z = 0; z < NSW; ++z) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) xd[z][ks] = F::load_tr(dot + SLICE * z, LDP, 32 * ks + 8 * g);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        f32x4_t acc[NSW];
+#pragma unroll
+        for (int z = 0; z < NSW; ++z) acc[z] = zero4();
+#pragma unroll
+        for (int ks = (t >> 1); ks < 2; ++ks) {
+#pragma unroll
+          for (int z = 0; z < NSW; ++z) acc[z] = mma(pf.get<T>(upper_frag(t, ks)), xd[z][ks], acc[z]);
+        }
+#pragma unroll
+        for (int z = 0; z < NSW; ++z) xd0[(z * 4 + t) * 64 + l] = acc[z];
+      }
+      if (i > 0) pf.request(p.ptf + slot_head(i - 1) * FRAG_PIECES);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const f32x4_t i0 = p.scale * *reinterpret_cast<const f32x4_t*>(gs + GATE_IN * CH + 32 * ks + 8 * g);
+        const f32x4_t i1 = p.scale * *reinterpret_cast<const f32x4_t*>(gs + GATE_IN * CH + 32 * ks + 8 * g + 4);
+#pragma unroll
+        for (int z = 0; z < NSW; ++z) {
+          float d[8];
+          F::floats(xd[z][ks], d);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            d[r] *= i0[r];
+            d[4 + r] *= i1[r];
+          }
+          fd[z][ks] = F::split3(d);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * NT; ++j) {
+        f32x4_t acc[NSW];
+#pragma unroll
+        for (int z = 0; z < NSW; ++z) acc[z] = zero4();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const typename F::X xq = F::template load_tr<8>(qt + pair_col(j), LDN, 32 * ks + 8 * g);
+#pragma unroll
+          for (int z = 0; z < NSW; ++z) acc[z] = mma(xq, fd[z][ks], acc[z]);
+        }
+#pragma unroll
+        for (int z = 0; z < NSW; ++z) xq0[(z * 2 * NT + j) * 64 + l] = acc[z];
+      }
+    };
+    pf.request(p.ptf + slot_head(last) * FRAG_PIECES);
+    __syncthreads();
+    ahead(last);
+    __syncthreads();
+    for (int i = last; i >= 0; --i) {
+      __syncthreads();
+      if (i > 0) ahead(i - 1);
+      __syncthreads();
+    }
+    return;
+  }
+
+  if (w < 2 * NSW + 1) {
+    // ---- the waves behind, one for each state wave: with the residuals, and the entering state of the chunk after
+    // (for its inner product)
+    const int z = w - NSW - 1, slice = ps * NSW + z, col = PS * ps + SLICE * z + c;
+    uint4 te[4], ss[NT][2], us[NT][2];
+    f32x4_t du[4];
+    const int64_t state_row = static_cast<int64_t>(col) * ND + 8 * g;   // of S and dS
+    auto request = [&](int i) {
+      const uint4* e = p.e + (slot_head(i) * p.nsl + slice) * 4 * 64 + l;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) te[t] = e[t * 64];
+      if (i < last) {
+        const char* base = static_cast<const char*>(p.s) + slot_head(i + 1) * p.rows * ND * 4 + state_row * static_cast<int>(sizeof(T));
+        const int64_t lo = sizeof(T) == 2 ? static_cast<int64_t>(p.rows) * ND * 2 : 16;   // from the first term to the second
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          ss[q][0] = *reinterpret_cast<const uint4*>(base + 32 * q * sizeof(T));
+          ss[q][1] = *reinterpret_cast<const uint4*>(base + lo + 32 * q * sizeof(T));
+        }
+      }
+    };
+    auto take = [&]() {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) du[t] = xdu[(z * 4 + t) * 64 + l];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) us[q][t] = xs[((z * NT + q) * 2 + t) * 64 + l];
+      }
+    };
+    auto behind = [&](int i) {
+      const int len = length(i);
+      const float* gs = gbuf(i);
+      const T* vt = vbuf(i);
+      const int64_t at = (slot_head(i) * p.nsl + slice) * CH;
+      if (i < last) {
+        float phi = 0.f;
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          float a[8], b[8];
+          F::floats(F::from_pieces(us[q]), a);
+          F::floats(F::from_pieces(ss[q]), b);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) phi += a[r] * b[r];
+        }
+        phi = ssd::wave_sum(phi);
+        if (l == 0) p.phi[slot_head(i + 1) * p.nsl + slice] = phi;
+      }
+      f32x4_t be[4], vv[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        be[t] = du[t] * __builtin_bit_cast(f32x4_t, te[t]);
+        const int row = pair_col(t) + 8 * g;
+        du[t] *= *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + row);   // dv
+        vv[t] = du[t] * F::load4_tr(vt + SLICE * z, LDP, row);
+      }
+      if (i > 0) request(i - 1);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          be[t][r] = ssd::sum16(be[t][r]);
+          vv[t][r] = ssd::sum16(vv[t][r]);
+        }
+      }
+      if (c == 0) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          *reinterpret_cast<f32x4_t*>(p.be + at + pair_col(t) + 8 * g) = be[t];
+          *reinterpret_cast<f32x4_t*>(p.vv + at + pair_col(t) + 8 * g) = vv[t];
+        }
+      }
+      T* ds = static_cast<T*>(p.ds) + slot_head(i) * p.rows * ND + state_row;
+#pragma unroll
+      for (int q = 0; q < NT; ++q) F::store(ds + 32 * q, F::hi(F::from_pieces(us[q])));
+      // dv, a 16-column stretch of every row: rows at a uniform distance from the wave's first
+      char* dv = reinterpret_cast<char*>(static_cast<T*>(p.dv) + (s0 + static_cast<int64_t>(CH) * i) * hp + static_cast<int64_t>(h) * p.P + PS * ps + SLICE * z);
+      const uint32_t off = static_cast<uint32_t>(8 * g * static_cast<uint32_t>(hp) + c) * static_cast<uint32_t>(sizeof(T));
+      if (col < p.P) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (len == CH || pair_col(t) + 8 * g + r < len)
+              *reinterpret_cast<T*>(dv + (pair_col(t) + r) * hp * static_cast<int>(sizeof(T)) + off) = ssd::Elem<T>::from_f(du[t][r]);
+          }
+        }
+      }
+    };
+    __syncthreads();
+    request(last);
+    __syncthreads();
+    for (int i = last; i >= 0; --i) {
+      if (i < last) take();
+      __syncthreads();
+      if (i < last) behind(i + 1);
+      __syncthreads();
+    }
+    take();
+    behind(0);
+    return;
+  }
+
+  // ---- the staging wave
+  const int pcols = min(PS, p.P - PS * ps);
+  const T* kp = static_cast<const T*>(p.k) + row_offset(s0, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N;
+  const T* qp = static_cast<const T*>(p.q) + row_offset(s0, p.L, p.q_sb, p.q_sl) + static_cast<int64_t>(grp) * p.N;
+  const T* vp = static_cast<const T*>(p.v) + row_offset(s0, p.L, p.v_sb, p.v_sl) + static_cast<int64_t>(h) * p.P + PS * ps;
+  TileN tk, tq;
+  TileP td, tv;
+  float tg[3];
+  auto request_k = [&](int i) { tk.load(kp + static_cast<int64_t>(CH) * i * p.k_sl, p.k_sl, length(i), p.N, l); };
+  auto request_v = [&](int i) { tv.load(vp + static_cast<int64_t>(CH) * i * p.v_sl, p.v_sl, length(i), pcols, l); };
+  // for the wave ahead: q, dout and the gates
+  auto request_q = [&](int i) {
+    const int64_t row = static_cast<int64_t>(CH) * i;
+    tq.load(qp + row * p.q_sl, p.q_sl, length(i), p.N, l);
+    td.load(static_cast<const T*>(p.dout) + (s0 + row) * hp + static_cast<int64_t>(h) * p.P + PS * ps, hp, length(i), pcols, l);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) tg[k] = p.gates[slot_head(i) * (GATES * CH) + k * CH + l];
+  };
+  auto stage_q = [&](int i) {
+    tq.store(qbuf(i), l);
+    td.store(dobuf(i), l);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) gbuf(i)[k * CH + l] = tg[k];
+  };
+  request_k(last);
+  request_q(last);
+  tk.store(kbuf(last), l);
+  stage_q(last);
+  if (last > 0) request_q(last - 1);
+  if (KB && last > 0) request_k(last - 1);
+  request_v(last);
+  __syncthreads();
+  if (KB && last > 0) {
+    stage_q(last - 1);
+    if (last > 1) request_q(last - 2);
+  }
+  __syncthreads();
+  for (int i = last; i >= 0; --i) {
+    if (!KB) {
+      if (i < last) tk.store(kbuf(i), l);
+      if (i > 0) {
+        stage_q(i - 1);
+        request_k(i - 1);
+      }
+      if (i > 1) request_q(i - 2);
+    }
+    __syncthreads();
+    if (KB) {
+      if (i > 0) tk.store(kbuf(i - 1), l);
+      if (i > 1) {
+        stage_q(i - 2);
+        request_k(i - 2);
+      }
+      if (i > 2) request_q(i - 3);
+    }
+    tv.store(vbuf(i), l);
+    if (i > 0) request_v(i - 1);
+    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
-// k_delta_grad: dq, dk, dg and dbeta of one chunk and group, its heads one
+// k_delta_grad: dq and dk of one chunk and group, its heads one
 // after the other (dq and dk are sums over them, taken in registers in head
 // order).  Eight waves: 16 rows of the chunk times half of the N columns each.
 // All products end in the io type, so every operand is a single term.
@@ -292,13 +481,13 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
   if (ch.len == 0) return;
   const int tid = static_cast<int>(threadIdx.x), l = tid & 63, g = l >> 4, c = l & 15, w = ssd::wave_id_s();
   const int rt = w & 3, half = w >> 2, row = 16 * rt + c;
-  const int64_t hp = static_cast<int64_t>(p.H) * p.P, rows = static_cast<int64_t>(p.np) * PS;
+  const int64_t hp = static_cast<int64_t>(p.H) * p.P, rows = p.rows;
   {
     typename Cf::TileN tk, tq;
-    tk.load(static_cast<const T*>(p.k) + row_offset(ch.row, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N, p.k_sl, ch.len, p.N);
-    tq.load(static_cast<const T*>(p.q) + row_offset(ch.row, p.L, p.q_sb, p.q_sl) + static_cast<int64_t>(grp) * p.N, p.q_sl, ch.len, p.N);
-    tk.store(kt);
-    tq.store(qt);
+    tk.load(static_cast<const T*>(p.k) + row_offset(ch.row, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N, p.k_sl, ch.len, p.N, tid);
+    tq.load(static_cast<const T*>(p.q) + row_offset(ch.row, p.L, p.q_sb, p.q_sl) + static_cast<int64_t>(grp) * p.N, p.q_sl, ch.len, p.N, tid);
+    tk.store(kt, tid);
+    tq.store(qt, tid);
   }
   f32x4_t dqa[NT], dka[NT];
 #pragma unroll
@@ -312,23 +501,23 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
     for (int t = 0; t < NT; ++t) x1[t] = x2[t] = x3[t] = zero4();
     m1[0] = m1[1] = m2[0] = m2[1] = zero4();
     for (int p0 = 0; p0 < p.P; p0 += PSL) {
-      const int pcols = min(PSL, p.P - p0);
+      const int pcols = min(PSL, p.P - p0), prows = min(PSL, static_cast<int>(rows) - p0);
       typename Cf::TileP td, tv;
       typename Cf::TileU tu;
       typename Cf::TileS ts, tds;
       const int64_t at = static_cast<int64_t>(ch.row) * hp + static_cast<int64_t>(h) * p.P + p0;
-      td.load(static_cast<const T*>(p.dout) + at, hp, ch.len, pcols);
-      tv.load(static_cast<const T*>(p.dv) + at, hp, ch.len, pcols);
-      tu.load(static_cast<const T*>(p.u) + (sh * rows + p0) * CH, CH, PSL, CH);
-      ts.load(reinterpret_cast<const T*>(static_cast<const char*>(p.s) + sh * rows * ND * 4) + static_cast<int64_t>(p0) * ND, ND, PSL, ND);
-      tds.load(static_cast<const T*>(p.ds) + (sh * rows + p0) * ND, ND, PSL, ND);
+      td.load(static_cast<const T*>(p.dout) + at, hp, ch.len, pcols, tid);
+      tv.load(static_cast<const T*>(p.dv) + at, hp, ch.len, pcols, tid);
+      tu.load(static_cast<const T*>(p.u) + (sh * rows + p0) * CH, CH, prows, CH, tid);
+      ts.load(reinterpret_cast<const T*>(static_cast<const char*>(p.s) + sh * rows * ND * 4) + static_cast<int64_t>(p0) * ND, ND, prows, ND, tid);
+      tds.load(static_cast<const T*>(p.ds) + (sh * rows + p0) * ND, ND, prows, ND, tid);
       const float tg = tid < GATES * CH ? p.gates[sh * (GATES * CH) + tid] : 0.f;
       __syncthreads();   // the previous head's last products are done
-      td.store(dot);
-      tv.store(dvt);
-      tu.store(ut);
-      ts.store(st);
-      tds.store(dst);
+      td.store(dot, tid);
+      tv.store(dvt, tid);
+      tu.store(ut, tid);
+      ts.store(st, tid);
+      tds.store(dst, tid);
       if (tid < GATES * CH) gs[tid] = tg;
       __syncthreads();
 #pragma unroll
@@ -397,26 +586,6 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
         dka[t] = mma(xk, xf, dka[t]);
       }
     }
-    // the gates' gradients: sums over the blocks of value columns in order, dg by a scan over the rows
-    if (w == 0) {
-      float d = 0.f, b = 0.f, phi = 0.f;
-      for (int s = 0; s < p.np; ++s) {
-        d += p.dd[(sh * p.np + s) * CH + l];
-        b += p.be[(sh * p.np + s) * CH + l];
-        phi += p.phi[sh * p.np + s];
-      }
-      float run = d;
-#pragma unroll
-      for (int k = 1; k < 64; k <<= 1) {
-        const float o = __shfl_up(run, k);
-        if (l >= k) run += o;
-      }
-      if (l < ch.len) {
-        const int64_t at = (static_cast<int64_t>(ch.row) + l) * p.H + h;
-        p.dg[at] = phi - (run - d);
-        p.dbeta[at] = b;
-      }
-    }
   }
   if (row < ch.len) {
     const int64_t at = ((static_cast<int64_t>(ch.row) + row) * p.G + grp) * p.N;
@@ -432,6 +601,35 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
 }
 
 // ---------------------------------------------------------------------------
+// k_delta_gates: dg and dbeta of one chunk, a wave per head: the slices' row
+// sums added in slice order, dg by a scan over the rows.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void k_delta_gates(Problem p) {
+  const int slot = static_cast<int>(blockIdx.x), h = static_cast<int>(blockIdx.y) * 4 + ssd::wave_id_s(), l = ssd::lane_id();
+  const Chunk ch = chunk_of(p, slot);
+  if (ch.len == 0 || h >= p.H) return;
+  const int64_t sh = static_cast<int64_t>(slot) * p.H + h;
+  float d = 0.f, b = 0.f, phi = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.nsl; ++s) {
+    d += p.oo[(sh * p.nsl + s) * CH + l] - p.vv[(sh * p.nsl + s) * CH + l];
+    b += p.be[(sh * p.nsl + s) * CH + l];
+    phi += p.phi[sh * p.nsl + s];
+  }
+  float run = d;
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) {
+    const float o = __shfl_up(run, k);
+    if (l >= k) run += o;
+  }
+  if (l < ch.len) {
+    const int64_t at = (static_cast<int64_t>(ch.row) + l) * p.H + h;
+    p.dg[at] = phi - (run - d);
+    p.dbeta[at] = b;
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
 template <typename K> int go(K kernel, dim3 grid, int threads, size_t lds, hipStream_t s, const Problem& p) {
@@ -442,7 +640,8 @@ template <typename K> int go(K kernel, dim3 grid, int threads, size_t lds, hipSt
 
 template <typename T, int NT> int rwalk(const Problem& p, hipStream_t s) {
   static_assert(RwalkCfg<T, NT>::LDS <= 160 * 1024, "LDS");
-  return go(k_delta_rwalk<T, NT>, dim3(p.H * p.np, p.nseqs), 256, RwalkCfg<T, NT>::LDS, s, p);
+  using Cf = RwalkCfg<T, NT>;
+  return go(k_delta_rwalk<T, NT>, dim3(p.H * ((p.P + Cf::PS - 1) / Cf::PS), p.nseqs), Cf::THREADS, Cf::LDS, s, p);
 }
 template <typename T, int NT> int grad(const Problem& p, hipStream_t s) {
   static_assert(GradCfg<T, NT>::LDS <= 160 * 1024, "LDS");
@@ -457,5 +656,6 @@ int launch_grad(const Problem& p, int io, hipStream_t s) {
   if (io == SSD_IO_BF16) return p.N <= 64 ? grad<bf16_t, 2>(p, s) : grad<bf16_t, 4>(p, s);
   return p.N <= 64 ? grad<float, 2>(p, s) : grad<float, 4>(p, s);
 }
+int launch_gates(const Problem& p, hipStream_t s) { return go(k_delta_gates, dim3(p.nslots, (p.H + 3) / 4), 256, 0, s, p); }
 
 }  // namespace delta

@@ -146,7 +146,7 @@ def test_gates_at_their_ends(io):
 
 def test_one_key_for_all_rows():
     # the same key at every row, beta near one: N is dense, T' alternates, and dv undoes most of what later rows say:
-    # dg is a tenth of the terms whose difference it is
+    # dg is some four hundred times smaller than the terms whose difference it is
     d = make(1, 130, 2, 32, 1, 32, "f32", seed=8)
     d["k"][:] = d["k"][:, :1]
     d["beta"][:] = 0.9

@@ -14,6 +14,7 @@ struct Problem {
   int B, L, H, P, G, N, nseqs, hpg;
   int total;      // B * L rows
   int nslots;     // chunk slots: the chunks of sequence s are slots start(s) / 64 + s, ...
+  int hb;         // heads of a group that one block of k_delta_prep takes
   int rows;       // P rounded up to a multiple of PAD
   int nsl;        // slices of 16 value columns: rows / SLICE
   float scale;
@@ -29,7 +30,7 @@ struct Problem {
   int32_t* starts;   // (nseqs + 1) first rows (seq_idx given)
   float* gates;      // (slots, H, GATES, 64)
   uint4* tf;         // (slots, H, FRAG_PIECES): T' - I, T' = (I + N diag(beta))^-1, rows in pair order
-  uint4* pf;         // the same of the causal scores, rows in order
+  uint4* pf;         // the same of the causal scores, rows in order (bf16 forward: the first terms alone)
   uint4* ttf;        // transposed (I + diag(beta) N)^-1 - I, rows in pair order (backward)
   uint4* ptf;        // transposed scores, rows in pair order (backward)
   uint4* e;          // (slots, H, nsl, 4, 64): the residuals, float32, accumulator layout (backward)
@@ -42,8 +43,10 @@ struct Problem {
   float* phi;        // (slots, H, nsl): <entering state, its gradient>
 };
 
-// per slot and head: exp(c_i), exp(c_last - c_i), beta_i, and c_i in two floats
-enum { GATE_IN = 0, GATE_OUT = 1, GATE_BETA = 2, GATE_C = 3, GATE_CLO = 4, GATES = 5 };
+// Per slot and head, 64 values each: exp(c_i); beta_i exp(c_last - c_i); beta_i; exp(c_last - c_i); -beta_i exp(c_i);
+// and c_i in two floats.  The forward walk reads the first WALK_GATES, the backward's the first RWALK_GATES.
+enum { GATE_IN = 0, GATE_BO = 1, GATE_BETA = 2, GATE_OUT = 3, GATE_BI = 4, GATE_C = 5, GATE_CLO = 6, GATES = 7 };
+constexpr int WALK_GATES = 3, RWALK_GATES = 5;
 
 int launch_starts(const Problem& p, hipStream_t s);
 int launch_prep(const Problem& p, int io, bool backward, hipStream_t s);

@@ -62,8 +62,10 @@ template <> struct Fr<bf16_t> {
     u.h[1] = tr4<CS>(base, ld, row0 + 4);
     return u.x;
   }
-  static __device__ __forceinline__ f32x4_t load4_tr(const bf16_t* base, int ld, int row0) {
-    const ssd::s16x4_t v = tr4<4>(base, ld, row0);
+  typedef ssd::s16x4_t X4;   // 4 rows of one column as they lie
+  static __device__ __forceinline__ X4 load4_raw(const bf16_t* base, int ld, int row0) { return tr4<4>(base, ld, row0); }
+  static __device__ __forceinline__ f32x4_t load4_tr(const bf16_t* base, int ld, int row0) { return floats4(tr4<4>(base, ld, row0)); }
+  static __device__ __forceinline__ f32x4_t floats4(X4 v) {
     f32x4_t f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) f[r] = ssd::bf16_to_f32(static_cast<bf16_t>(v[r]));
@@ -149,6 +151,9 @@ template <> struct Fr<float> {
     for (int e = 0; e < 8; ++e) x[e] = p[e * ld];
     return x;
   }
+  typedef f32x4_t X4;
+  static __device__ __forceinline__ X4 load4_raw(const float* base, int ld, int row0) { return load4_tr(base, ld, row0); }
+  static __device__ __forceinline__ f32x4_t floats4(X4 v) { return v; }
   static __device__ __forceinline__ f32x4_t load4_tr(const float* base, int ld, int row0) {
     const float* p = base + row0 * ld + (static_cast<int>(threadIdx.x) & 15);
     return f32x4_t{p[0], p[ld], p[2 * ld], p[3 * ld]};
@@ -195,6 +200,19 @@ __device__ __forceinline__ f32x4_t mma(const f32x8_t& a, const f32x8_t& b, f32x4
   for (int e = 0; e < 8; ++e) c = ssd::Mma<float>::mma(a[e], b[e], c);
   return c;
 }
+
+// One term of a split operand's product at a time, smallest first, so that callers can run over independent tiles
+// between the terms (a tile's own MFMAs depend on each other).
+// exact A times split B: terms lo, hi
+__device__ __forceinline__ f32x4_t mma_term(bf16x8_t a, const Fr<bf16_t>::S& b, f32x4_t c, int term) { return mma(a, term ? b.hi : b.lo, c); }
+__device__ __forceinline__ f32x4_t mma_term(bf16x8_t a, const Fr<bf16_t>::S3& b, f32x4_t c, int term) {
+  return mma(a, term == 0 ? b.lo : term == 1 ? b.mid : b.hi, c);
+}
+__device__ __forceinline__ f32x4_t mma_term(const Fr<bf16_t>::S& a, const Fr<bf16_t>::S& b, f32x4_t c, int term) {
+  return term == 0 ? mma(a.lo, b.hi, c) : term == 1 ? mma(a.hi, b.lo, c) : mma(a.hi, b.hi, c);
+}
+// float32: the whole product, taken with the first term
+__device__ __forceinline__ f32x4_t mma_term(const f32x8_t& a, const f32x8_t& b, f32x4_t c, int term) { return term ? c : mma(a, b, c); }
 
 // first column of tile t among columns in pair order, for load_tr<8>
 __device__ __forceinline__ constexpr int pair_col(int t) { return 32 * (t >> 1) + 4 * (t & 1); }

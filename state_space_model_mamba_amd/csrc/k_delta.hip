@@ -80,26 +80,25 @@ __global__ __launch_bounds__(ST_THR) void k_delta_starts(Problem p) {
 
 // ---------------------------------------------------------------------------
 // k_delta_prep: T' (and for the backward the transposed (I + diag(beta) N)^-1
-// and the transposed scores) and the scores of one chunk and head, as the
-// walks' operand fragments.
+// and the transposed scores) and the scores of one chunk, as the walks'
+// operand fragments, for up to HB heads of one group.
+//
+// q k^T and k k^T are the group's: they are taken once, from operands loaded
+// straight into registers, and every head scales its copies by its decays.
+// With the rows of the first operand in pair order a pair of score tiles is
+// the walk's fragment already; only the matrices to invert go through LDS.
 //
 // The inverse of a unit lower triangular 64 x 64 matrix in float32: the four
-// 16 x 16 diagonal blocks by substitution (a lane per column, one wave), then
-// 32 x 32 and 64 x 64 by the block formula T21 = -T22 A21 T11 with float32
-// MFMA tiles, in place in LDS.
+// 16 x 16 diagonal blocks by substitution (a lane per column, one wave, while
+// others scale the scores), then 32 x 32 and 64 x 64 by the block formula
+// T21 = -T22 A21 T11 with float32 MFMA tiles, in place in LDS.
 // ---------------------------------------------------------------------------
 constexpr int LDM = 68;   // pitch of the float32 64 x 64 matrices
 
-template <typename T, int NT, bool BWD> struct PrepCfg {
-  static constexpr int ND = 32 * NT;
-  using TileT = Tile<T, CH, ND, 256>;
+template <bool BWD> struct PrepCfg {
   static constexpr int NM = BWD ? 2 : 1;
-  static constexpr size_t OFF_Q = sizeof(T) * TileT::LDS_ELEMS;
-  static constexpr size_t OFF_M = 2 * OFF_Q;
-  static constexpr size_t OFF_P = OFF_M + sizeof(float) * NM * CH * LDM;
-  static constexpr size_t OFF_C = OFF_P + sizeof(float) * CH * LDM;
-  static constexpr size_t OFF_B = OFF_C + sizeof(double) * CH;
-  static constexpr size_t LDS = OFF_B + sizeof(float) * CH;
+  static constexpr size_t OFF_C = sizeof(float) * NM * CH * LDM;
+  static size_t lds(int heads) { return OFF_C + sizeof(float) * 3 * CH * heads; }
 };
 
 // acc += A B of 16 x 16 float32 blocks in LDS
@@ -114,153 +113,235 @@ __device__ __forceinline__ void block_store(float* m, f32x4_t v) {
   for (int r = 0; r < 4; ++r) m[(4 * (l >> 4) + r) * LDM + (l & 15)] = v[r];
 }
 
-template <int NM> __device__ __forceinline__ void invert64(float* m) {
-  const int l = ssd::lane_id(), g = l >> 4, c = l & 15, w = ssd::wave_id_s();
-  auto blk = [&](int mat, int i, int j) { return m + mat * CH * LDM + 16 * i * LDM + 16 * j; };
-  if (w < NM) {
-    float* d = blk(w, g, g);
-    float x[16];
+// the inverses of the four 16 x 16 diagonal blocks, in place, by one wave: a lane per block and column
+__device__ __forceinline__ void invert_diagonal(float* m) {
+  const int l = ssd::lane_id(), g = l >> 4, c = l & 15;
+  float* d = m + 16 * g * LDM + 16 * g;
+  float x[16];
+  x[0] = c == 0 ? 1.f : 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.f : 0.f;
+  for (int i = 1; i < 16; ++i) {
+    f32x4_t row[4];
 #pragma unroll
-    for (int k = 0; k < 15; ++k) {
+    for (int q = 0; q <= (i - 1) / 4; ++q) row[q] = *reinterpret_cast<const f32x4_t*>(d + i * LDM + 4 * q);
+    float s0 = i == c ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-      for (int i = k + 1; i < 16; ++i) x[i] -= d[i * LDM + k] * x[k];
+    for (int k = 0; k < i; ++k) {
+      if ((i - 1 - k) & 1) s1 -= row[k / 4][k % 4] * x[k]; else s0 -= row[k / 4][k % 4] * x[k];
     }
+    x[i] = s0 + s1;
+  }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) d[i * LDM + c] = x[i];
+  for (int i = 0; i < 16; ++i) d[i * LDM + c] = x[i];
+}
+
+// the rest of the inverse: blocks (1, 0) and (3, 2), then the lower left quarter column by column (a wave each,
+// the products between in registers)
+template <int NM> __device__ __forceinline__ void invert_rest(float* m) {
+  const int l = ssd::lane_id(), g = l >> 4, c = l & 15, w = ssd::wave_id_s();
+  float* base = m + (w >> 1) * CH * LDM;
+  auto blk = [&](int i, int j) { return base + 16 * i * LDM + 16 * j; };
+  auto mma_left = [&](const float* t, f32x4_t y, f32x4_t acc) {   // acc + T y, y a tile in registers
+    return ssd::Mma<float>::mma_rd(*reinterpret_cast<const f32x4_t*>(t + c * LDM + 4 * g), y, acc);
+  };
+  if (w < 2 * NM) {
+    const int q = 2 * (w & 1);
+    const f32x4_t y = block_mma(blk(q + 1, q), blk(q, q), zero4());
+    block_store(blk(q + 1, q), -mma_left(blk(q + 1, q + 1), y, zero4()));
   }
   __syncthreads();
   if (w < 2 * NM) {
-    const int mat = w >> 1, q = 2 * (w & 1);
-    const f32x4_t y = block_mma(blk(mat, q + 1, q), blk(mat, q, q), zero4());
-    const float* t = blk(mat, q + 1, q + 1);
-    const f32x4_t x = ssd::Mma<float>::mma_rd(*reinterpret_cast<const f32x4_t*>(t + c * LDM + 4 * g), y, zero4());
-    block_store(blk(mat, q + 1, q), -x);
+    const int j = w & 1;
+    f32x4_t y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      y[i] = block_mma(blk(2 + i, 1), blk(1, j), zero4());   // T_01 is zero
+      if (j == 0) y[i] = block_mma(blk(2 + i, 0), blk(0, 0), y[i]);
+    }
+    const f32x4_t t2 = mma_left(blk(2, 2), y[0], zero4());
+    const f32x4_t t3 = mma_left(blk(3, 3), y[1], mma_left(blk(3, 2), y[0], zero4()));
+    block_store(blk(2, j), -t2);
+    block_store(blk(3, j), -t3);
   }
-  __syncthreads();
-  const int i = 2 + (w >> 1), j = w & 1;
-  f32x4_t y[NM];
-#pragma unroll
-  for (int mat = 0; mat < NM; ++mat) {
-    y[mat] = block_mma(blk(mat, i, 1), blk(mat, 1, j), zero4());   // T_01 is zero
-    if (j == 0) y[mat] = block_mma(blk(mat, i, 0), blk(mat, 0, 0), y[mat]);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int mat = 0; mat < NM; ++mat) block_store(blk(mat, i, j), y[mat]);
-  __syncthreads();
-#pragma unroll
-  for (int mat = 0; mat < NM; ++mat) {
-    y[mat] = block_mma(blk(mat, i, 2), blk(mat, 2, j), zero4());
-    if (i == 3) y[mat] = block_mma(blk(mat, 3, 3), blk(mat, 3, j), y[mat]);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int mat = 0; mat < NM; ++mat) block_store(blk(mat, i, j), -y[mat]);
   __syncthreads();
 }
 
-template <typename T, int NT, bool BWD> __global__ __launch_bounds__(256) void k_delta_prep(Problem p) {
-  using Cf = PrepCfg<T, NT, BWD>;
+template <typename T, int NT, bool BWD> __global__ __launch_bounds__(256, BWD ? 2 : 3) void k_delta_prep(Problem p) {
+  using Cf = PrepCfg<BWD>;
   using F = Fr<T>;
-  using TileT = typename Cf::TileT;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  T* kt = reinterpret_cast<T*>(smem);
-  T* qt = reinterpret_cast<T*>(smem + Cf::OFF_Q);
-  float* mm = reinterpret_cast<float*>(smem + Cf::OFF_M);
-  float* pm = reinterpret_cast<float*>(smem + Cf::OFF_P);
-  double* cs = reinterpret_cast<double*>(smem + Cf::OFF_C);
-  float* bs = reinterpret_cast<float*>(smem + Cf::OFF_B);
+  float* mm = reinterpret_cast<float*>(smem);
+  float* cb = reinterpret_cast<float*>(smem + Cf::OFF_C);   // per head: the sums of g in two floats, and beta
 
-  const int slot = static_cast<int>(blockIdx.x), h = static_cast<int>(blockIdx.y), grp = h / p.hpg;
+  const int slot = static_cast<int>(blockIdx.x);
+  const int parts = (p.hpg + p.hb - 1) / p.hb, grp = static_cast<int>(blockIdx.y) / parts;
+  const int h0 = grp * p.hpg + static_cast<int>(blockIdx.y) % parts * p.hb, h1 = min(h0 + p.hb, (grp + 1) * p.hpg);
   const Chunk ch = chunk_of(p, slot);
   if (ch.len == 0) return;
-  const int64_t sh = static_cast<int64_t>(slot) * p.H + h;
   const int tid = static_cast<int>(threadIdx.x), l = tid & 63, g = l >> 4, c = l & 15, w = ssd::wave_id_s();
 
-  TileT tk, tq;
-  tk.load(static_cast<const T*>(p.k) + row_offset(ch.row, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N, p.k_sl, ch.len, p.N, tid);
-  tq.load(static_cast<const T*>(p.q) + row_offset(ch.row, p.L, p.q_sb, p.q_sl) + static_cast<int64_t>(grp) * p.N, p.q_sl, ch.len, p.N, tid);
-  if (tid < CH) {
-    const int64_t at = static_cast<int64_t>(ch.row + tid) * p.H + h;
-    float gv = tid < ch.len ? p.g[at] : 0.f;
+  // the heads' gates, a wave each
+  for (int h = h0 + w; h < h1; h += 4) {
+    const int64_t at = static_cast<int64_t>(ch.row + l) * p.H + h;
+    float gv = l < ch.len ? p.g[at] : 0.f;
     gv = gv < -104.f ? -104.f : gv;
-    const float b = tid < ch.len ? p.beta[at] : 0.f;
+    const float b = l < ch.len ? p.beta[at] : 0.f;
     double s = gv;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const double o = __shfl_up(s, d);
-      if (tid >= d) s += o;
+      if (l >= d) s += o;
     }
-    cs[tid] = s;
-    bs[tid] = b;
     const double last = __shfl(s, 63);
-    float* gt = p.gates + sh * (GATES * CH) + tid;
-    gt[GATE_IN * CH] = expf(static_cast<float>(s));
-    gt[GATE_OUT * CH] = expf(static_cast<float>(last - s));
+    const float hi = static_cast<float>(s), lo = static_cast<float>(s - hi);
+    float* cs = cb + (h - h0) * 3 * CH;
+    cs[l] = hi;
+    cs[CH + l] = lo;
+    cs[2 * CH + l] = b;
+    float* gt = p.gates + (static_cast<int64_t>(slot) * p.H + h) * (GATES * CH) + l;
+    const float in = expf(hi), out = expf(static_cast<float>(last - s));
+    gt[GATE_IN * CH] = in;
+    gt[GATE_BO * CH] = b * out;
     gt[GATE_BETA * CH] = b;
-    const float hi = static_cast<float>(s);
+    gt[GATE_OUT * CH] = out;
+    gt[GATE_BI * CH] = -b * in;
     gt[GATE_C * CH] = hi;
-    gt[GATE_CLO * CH] = static_cast<float>(s - hi);
+    gt[GATE_CLO * CH] = lo;
   }
-  tk.store(kt, tid);
-  tq.store(qt, tid);
-  __syncthreads();
 
-  // rows 16 w .. 16 w + 15 of N and of the scores; zero above the diagonal
-  for (int ct = 0; ct < 4; ++ct) {
-    f32x4_t kk = zero4(), qk = zero4();
-    if (ct <= w) {
+  const T* kp = static_cast<const T*>(p.k) + row_offset(ch.row, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N;
+  const T* qp = static_cast<const T*>(p.q) + row_offset(ch.row, p.L, p.q_sb, p.q_sl) + static_cast<int64_t>(grp) * p.N;
+  // Rows past the chunk's last stand in as its first: what they give stays in rows past the last (and beta is 0
+  // there).  Columns past N have to be zero.
+  auto operand = [&](const T* base, int64_t stride, int row, int ks, auto whole) {
+    const int n = 32 * ks + 8 * g;
+    const T* at = base + (row < ch.len ? row : 0) * stride + n;
+    if constexpr (decltype(whole)::value) return F::load(at);
+    else return n < p.N ? F::load_cols(at, p.N - n) : F::zero();
+  };
+  // Row tile w of k k^T (tiles ct <= w, rows 4 g + r and column c), and of the scores the fragments sw, sw + SW, ..
+  // (rows i = 16 t + c, values j; transposed: rows j in pair order, values i), sw = w - NM: the first NM waves
+  // invert the diagonal blocks meanwhile.
+  // lower: (0,0) (1,0) (2,0) (2,1) (3,0) (3,1); upper: (0,0) (0,1) (1,0) (1,1) (2,1) (3,1)
+  constexpr int SW = 4 - Cf::NM, SF = NFRAG / SW;
+  const int sw = w - Cf::NM;
+  auto lower_t = [](int f) { return f < 2 ? f : 2 + ((f - 2) >> 1); };
+  auto lower_k = [](int f) { return f < 2 ? 0 : (f - 2) & 1; };
+  auto upper_t = [](int f) { return f < 4 ? f >> 1 : f - 2; };
+  auto upper_k = [](int f) { return f < 4 ? f & 1 : 1; };
+  f32x4_t kk[4], qk[SF][2], kq[BWD ? SF : 1][2];
+  auto products = [&](auto whole) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) kk[t] = zero4();
+#pragma unroll
+    for (int ks = 0; ks < NT; ++ks) {
+      const typename F::X a = operand(kp, p.k_sl, 16 * w + c, ks, whole);
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct)
+        if (ct <= w) kk[ct] = mma(a, operand(kp, p.k_sl, 16 * ct + c, ks, whole), kk[ct]);
+    }
+    if (sw < 0) return;
+#pragma unroll
+    for (int z = 0; z < SF; ++z) {
+      const int f = sw + SW * z;
+      qk[z][0] = qk[z][1] = zero4();
+      if constexpr (BWD) kq[z][0] = kq[z][1] = zero4();
 #pragma unroll
       for (int ks = 0; ks < NT; ++ks) {
-        const typename F::X b = F::load(kt + (16 * ct + c) * TileT::LD + 32 * ks + 8 * g);
-        kk = mma(F::load(kt + (16 * w + c) * TileT::LD + 32 * ks + 8 * g), b, kk);
-        qk = mma(F::load(qt + (16 * w + c) * TileT::LD + 32 * ks + 8 * g), b, qk);
+        const typename F::X x = operand(qp, p.q_sl, 16 * lower_t(f) + c, ks, whole);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) qk[z][y] = mma(operand(kp, p.k_sl, perm_row(2 * lower_k(f) + y, c), ks, whole), x, qk[z][y]);
+        if constexpr (BWD) {
+          const typename F::X u = operand(kp, p.k_sl, perm_row(upper_t(f), c), ks, whole);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) kq[z][y] = mma(operand(qp, p.q_sl, perm_row(2 * upper_k(f) + y, c), ks, whole), u, kq[z][y]);
+        }
       }
     }
-    const int j = 16 * ct + c;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 16 * w + 4 * g + r;
-      const float dec = j <= i ? expf(static_cast<float>(cs[i] - cs[j])) : 0.f;
-      const float n = j < i ? kk[r] * dec : 0.f;
-      mm[i * LDM + j] = n * bs[j];
-      if constexpr (BWD) mm[CH * LDM + i * LDM + j] = n * bs[i];
-      pm[i * LDM + j] = j <= i ? p.scale * (qk[r] * dec) : 0.f;
-    }
-  }
-  __syncthreads();
-  invert64<Cf::NM>(mm);
-
-  auto put = [&](uint4* to, int f, const float (&v)[8]) {
-    uint4 u[2];
-    F::pieces(F::split(v), u);
-    uint4* d = to + sh * FRAG_PIECES + 2 * f * 64 + l;
-    d[0] = u[0];
-    d[64] = u[1];
   };
-  for (int f = w; f < NFRAG; f += 4) {
-    // lower: (0,0) (1,0) (2,0) (2,1) (3,0) (3,1); upper: (0,0) (0,1) (1,0) (1,1) (2,1) (3,1)
-    const int lt = f < 2 ? f : 2 + ((f - 2) >> 1), lk = f < 2 ? 0 : (f - 2) & 1;
-    const int row = perm_row(lt, c);
-    float v[8];
+  if (p.N == 32 * NT) products(std::true_type{}); else products(std::false_type{});
+  __syncthreads();
+
+  for (int h = h0; h < h1; ++h) {
+    const int64_t sh = static_cast<int64_t>(slot) * p.H + h;
+    const float *chi = cb + (h - h0) * 3 * CH, *clo = chi + CH, *bs = chi + 2 * CH;
+    // exp(c_i - c_j) where `low` (j <= i), and 0
+    auto decay = [](float hi_i, float lo_i, float hi_j, float lo_j, bool low) {
+      const float d = __expf(low ? (hi_i - hi_j) + (lo_i - lo_j) : 0.f);
+      return low ? d : 0.f;
+    };
+    auto load4 = [](const float* x) { return *reinterpret_cast<const f32x4_t*>(x); };
+    auto put = [&](uint4* to, int f, const float (&v)[8]) {
+      uint4 u[2];
+      F::pieces(F::split(v), u);
+      uint4* d = to + sh * FRAG_PIECES + 2 * f * 64 + l;
+      d[0] = u[0];
+      d[64] = u[1];
+    };
+    // rows 16 w .. 16 w + 15 of N, scaled; zero on and above the diagonal
+    {
+      const int i0 = 16 * w + 4 * g;
+      const f32x4_t hi = load4(chi + i0), lo = load4(clo + i0), bi = load4(bs + i0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = mm[row * LDM + 32 * lk + 8 * g + e] - (row == 32 * lk + 8 * g + e ? 1.f : 0.f);
-    put(p.tf, f, v);
+      for (int ct = 0; ct < 4; ++ct) {
+        const int j = 16 * ct + c;
+        const float hj = chi[j], lj = clo[j], bj = bs[j];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = pm[(16 * lt + c) * LDM + 32 * lk + 8 * g + e];
-    put(p.pf, f, v);
-    if constexpr (BWD) {
-      const int ut = f < 4 ? f >> 1 : f - 2, uk = f < 4 ? f & 1 : 1;
-      const int col = perm_row(ut, c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = mm[CH * LDM + (32 * uk + 8 * g + e) * LDM + col] - (col == 32 * uk + 8 * g + e ? 1.f : 0.f);
-      put(p.ttf, f, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = pm[(32 * uk + 8 * g + e) * LDM + col];
-      put(p.ptf, f, v);
+        for (int r = 0; r < 4; ++r) {
+          const float n = ct <= w ? kk[ct][r] * decay(hi[r], lo[r], hj, lj, j < i0 + r) : 0.f;
+          mm[(i0 + r) * LDM + j] = n * bj;
+          if constexpr (BWD) mm[CH * LDM + (i0 + r) * LDM + j] = n * bi[r];
+        }
+      }
     }
+    __syncthreads();
+    if (sw < 0) {
+      invert_diagonal(mm + w * CH * LDM);
+    } else {
+#pragma unroll
+      for (int z = 0; z < SF; ++z) {
+        const int f = sw + SW * z;
+        float v[8];
+        const int i = 16 * lower_t(f) + c, j0 = 32 * lower_k(f) + 8 * g;
+        const float hi = chi[i], li = clo[i];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const f32x4_t hj = load4(chi + j0 + 4 * y), lj = load4(clo + j0 + 4 * y);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[4 * y + r] = p.scale * (qk[z][y][r] * decay(hi, li, hj[r], lj[r], j0 + 4 * y + r <= i));
+        }
+        if constexpr (BWD || sizeof(T) == 4) put(p.pf, f, v);
+        else F::store(reinterpret_cast<T*>(p.pf + sh * (FRAG_PIECES / 2) + f * 64 + l), F::round8(v));
+        if constexpr (BWD) {
+          const int j = perm_row(upper_t(f), c), i0 = 32 * upper_k(f) + 8 * g;
+          const float hj = chi[j], lj = clo[j];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const f32x4_t ih = load4(chi + i0 + 4 * y), il = load4(clo + i0 + 4 * y);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[4 * y + r] = p.scale * (kq[z][y][r] * decay(ih[r], il[r], hj, lj, j <= i0 + 4 * y + r));
+          }
+          put(p.ptf, f, v);
+        }
+      }
+    }
+    __syncthreads();
+    invert_rest<Cf::NM>(mm);
+    for (int f = w; f < NFRAG; f += 4) {
+      const int row = perm_row(lower_t(f), c), k0 = 32 * lower_k(f) + 8 * g;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = mm[row * LDM + k0 + e] - (row == k0 + e ? 1.f : 0.f);
+      put(p.tf, f, v);
+      if constexpr (BWD) {
+        const int ff = NFRAG - 1 - f;   // a wave with two of the one has one of the other
+        const int col = perm_row(upper_t(ff), c), r0 = 32 * upper_k(ff) + 8 * g;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = mm[CH * LDM + (r0 + e) * LDM + col] - (col == r0 + e ? 1.f : 0.f);
+        put(p.ttf, ff, v);
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -270,51 +351,56 @@ template <typename T, int NT, bool BWD> __global__ __launch_bounds__(256) void k
 // state waves keeps 16 columns (N x 16) in registers as accumulator tiles for
 // the whole sequence and runs the sequential part alone:
 //     k S -> r -> T' r -> S   (three products a chunk, nothing else).
-// Beside them, on the other SIMDs, NSW / 2 output waves form the previous
-// chunk's o from the entering state and the corrections that two state waves
-// each leave in LDS (in the backward dout . o, and the stores of states and
-// corrections), and NSW / 2 staging waves bring the coming chunks' rows in:
+// Beside them output waves form the previous chunk's o from the entering
+// state and the residuals that the state waves leave in LDS (in the backward dout . o, and the stores of states and
+// corrections), and two staging waves bring the coming chunks' rows in:
 // their loads are in flight for a whole chunk, which no wave waits for.
 //
-// Per chunk two barriers: between the first and the second the state waves
-// work on chunk i, the output waves on chunk i - 1 and the staging waves on
-// k, v of chunk i + 1 and q, scores of chunk i; between the second and the
-// next first the output waves take what the state waves left for them.
+// Between two barriers the state waves work on chunk i, the output waves on
+// chunk i - 1 and the staging waves on k, v of chunk i + 1 and q, scores of
+// chunk i.  Where LDS holds what the state waves leave only once, a second
+// barrier a chunk lets the output waves take it first.
 // ---------------------------------------------------------------------------
 template <typename T, int NT, bool BWD, int NSW> struct WalkCfg {
-  static constexpr int ND = 32 * NT, PS = SLICE * NSW, NOUT = NSW / 2, HT = 64 * (NSW / 2), THREADS = 128 * NSW;
+  static constexpr int ND = 32 * NT, PS = SLICE * NSW, NOUT = BWD && NSW == 2 ? 2 : NSW / 2, NZ = NSW / NOUT, NST = 2, HT = 64 * NST, THREADS = 64 * (NSW + NOUT + NST);
   using TileN = Tile<T, CH, ND, HT>;
   using TileP = Tile<T, CH, PS, HT>;
   // q and the scores through LDS, or (512-byte rows: no room) straight into the output waves' registers
   static constexpr bool QLDS = sizeof(T) * ND <= 256;
-  // terms of the entering states and corrections in o: one where o ends in bf16 (its error then is 2.4e-3, the
-  // output's own rounding 1.7e-3 of it), two for the float32 dout . o
+  // terms of the entering states and the scores in o: one where o ends in bf16 (its error then is 2.4e-3, the
+  // output's own rounding 1.7e-3 of it), two for the float32 dout . o; the corrections always enter as two
   static constexpr int XP = BWD || sizeof(T) == 4 ? 2 : 1;
+  static constexpr int PIECES = FRAG_PIECES / 2 * XP;   // of the scores
   static constexpr size_t N_BYTES = sizeof(T) * TileN::LDS_ELEMS, V_BYTES = sizeof(T) * TileP::LDS_ELEMS;
   static constexpr size_t OFF_V = 2 * N_BYTES;
   static constexpr size_t OFF_Q = OFF_V + 2 * V_BYTES;
   static constexpr size_t OFF_P = OFF_Q + (QLDS ? 2 * N_BYTES : 0);
-  static constexpr size_t OFF_XS = OFF_P + (QLDS ? 2 * 16 * FRAG_PIECES : 0);
-  static constexpr size_t OFF_XU = OFF_XS + 16 * 64 * NSW * NT * XP;
-  static constexpr size_t OFF_G = OFF_XU + 16 * 64 * NSW * 4;
-  static constexpr size_t LDS = OFF_G + 2 * sizeof(float) * 3 * CH;
+  static constexpr size_t OFF_XS = OFF_P + (QLDS ? 2 * 16 * PIECES : 0);
+  // what the state waves leave, twice where there is room: then nobody waits for the output waves to take it
+  static constexpr int XBUF = QLDS && NSW == 2 ? 2 : 1;
+  static constexpr size_t OFF_XE = OFF_XS + XBUF * 16 * 64 * NSW * NT * XP;
+  static constexpr size_t OFF_G = OFF_XE + XBUF * 16 * 64 * NSW * 4;
+  // gates of the chunks in work: the staged one, the state waves' and (with one barrier) the output waves'
+  static constexpr int GBUF = 2 * XBUF;
+  static constexpr size_t LDS = OFF_G + GBUF * sizeof(float) * WALK_GATES * CH;
 };
 
 template <typename T, int NT, bool BWD, int NSW>
-__global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
+__global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_delta_walk(Problem p) {
   using Cf = WalkCfg<T, NT, BWD, NSW>;
   using F = Fr<T>;
   using TileN = typename Cf::TileN;
   using TileP = typename Cf::TileP;
-  constexpr int ND = Cf::ND, LDN = TileN::LD, LDP = TileP::LD, XP = Cf::XP, PS = Cf::PS;
+  constexpr int ND = Cf::ND, LDN = TileN::LD, LDP = TileP::LD, XP = Cf::XP, PS = Cf::PS, XB = Cf::XBUF - 1;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   auto kbuf = [&](int i) { return reinterpret_cast<T*>(smem + (i & 1) * Cf::N_BYTES); };
   auto vbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_V + (i & 1) * Cf::V_BYTES); };
   auto qbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_Q + (i & 1) * Cf::N_BYTES); };
-  auto pbuf = [&](int i) { return reinterpret_cast<uint4*>(smem + Cf::OFF_P) + (i & 1) * FRAG_PIECES; };
-  auto gbuf = [&](int i) { return reinterpret_cast<float*>(smem + Cf::OFF_G) + (i & 1) * 3 * CH; };
-  uint4* xs = reinterpret_cast<uint4*>(smem + Cf::OFF_XS);      // [wave][q][term][lane]
-  f32x4_t* xu = reinterpret_cast<f32x4_t*>(smem + Cf::OFF_XU);  // [wave][t][lane]
+  auto pbuf = [&](int i) { return reinterpret_cast<uint4*>(smem + Cf::OFF_P) + (i & 1) * Cf::PIECES; };
+  auto gbuf = [&](int i) { return reinterpret_cast<float*>(smem + Cf::OFF_G) + (i & (Cf::GBUF - 1)) * WALK_GATES * CH; };
+  // from the state waves: the entering state's terms [wave][q][term][lane], and the residuals [wave][t][lane]
+  auto xs = [&](int i) { return reinterpret_cast<uint4*>(smem + Cf::OFF_XS) + (i & XB) * 64 * NSW * NT * XP; };
+  auto xe = [&](int i) { return reinterpret_cast<f32x4_t*>(smem + Cf::OFF_XE) + (i & XB) * 64 * NSW * 4; };
 
   const int np = (p.P + PS - 1) / PS;
   const int h = static_cast<int>(blockIdx.x) / np, ps = static_cast<int>(blockIdx.x) % np;
@@ -328,7 +414,6 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
   if (w < NSW) {
     // ---- state waves
     const int col = PS * ps + SLICE * w + c;   // this lane's value column
-    const int slice = ps * NSW + w;
     const int64_t state_at = ((static_cast<int64_t>(seq) * p.H + h) * p.P + col) * p.N;
     f32x4_t S[2 * NT];
 #pragma unroll
@@ -350,29 +435,56 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
     for (int i = 0; i < nchunk; ++i) {
       const T *kt = kbuf(i), *vt = vbuf(i);
       const float* gs = gbuf(i);
-      __syncthreads();
+      auto gate = [&](int which, int row) { return *reinterpret_cast<const f32x4_t*>(gs + which * CH + row); };
+      __syncthreads();   // the second barrier of the chunk before (at first: the first chunk is staged)
+      typename F::X kf[4][NT];
+      typename F::X4 vf[4];
+      f32x4_t in[4];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) kf[t][q] = F::load(kt + perm_row(t, c) * LDN + 32 * q + 8 * g);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        vf[t] = F::load4_raw(vt + SLICE * w, LDP, pair_col(t) + 8 * g);
+        in[t] = gate(GATE_IN, pair_col(t) + 8 * g);
+      }
+      const float last = gs[GATE_IN * CH + CH - 1];
+      if constexpr (XB == 0) __syncthreads();   // the output waves have taken what is overwritten now
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
         uint4 u[2];
         F::pieces(sf[q], u);
 #pragma unroll
-        for (int t = 0; t < XP; ++t) xs[((w * NT + q) * XP + t) * 64 + l] = u[t];
+        for (int t = 0; t < XP; ++t) xs(i)[((w * NT + q) * XP + t) * 64 + l] = u[t];
       }
-      // r = v - exp(c) k S, rows in pair order
+      // r = v - exp(c) k S, rows in pair order; beside it the decay of S, and k's columns for the last product
       f32x4_t x[4];
+      typename F::X kc[2 * NT][2];
 #pragma unroll
       for (int t = 0; t < 4; ++t) x[t] = zero4();
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) x[t] = mma(F::load(kt + perm_row(t, c) * LDN + 32 * q + 8 * g), sf[q], x[t]);
+        for (int term = 0; term < 2; ++term) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) x[t] = mma_term(kf[t][q], sf[q], x[t], term);
+        }
+#pragma unroll
+        for (int j = 2 * q; j < 2 * q + 2; ++j) {
+          S[j] *= last;
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) kc[j][ks] = F::template load_tr<8>(kt + pair_col(j), LDN, 32 * ks + 8 * g);
+        }
       }
+      f32x4_t bo[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int row = pair_col(t) + 8 * g;
-        x[t] = F::load4_tr(vt + SLICE * w, LDP, row) - *reinterpret_cast<const f32x4_t*>(gs + GATE_IN * CH + row) * x[t];
+        x[t] = F::floats4(vf[t]) - in[t] * x[t];
+        bo[t] = gate(GATE_BO, pair_col(t) + 8 * g);
       }
-      // e = r + (T' - I) r, u = beta e
+      // e = r + (T' - I) r
       typename F::S f2[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -383,40 +495,38 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
-        for (int t = 2 * ks; t < 4; ++t) x[t] = mma(tf.get<T>(lower_frag(t, ks)), f2[ks], x[t]);
+        for (int term = 0; term < 3; ++term) {
+#pragma unroll
+          for (int t = 2 * ks; t < 4; ++t) x[t] = mma_term(tf.get<T>(lower_frag(t, ks)), f2[ks], x[t], term);
+        }
       }
-      if (i + 1 < nchunk) tf.request(p.tf + slot_head(i + 1) * FRAG_PIECES);
       typename F::S3 f3[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const int row = 32 * q + 8 * g;
-        if constexpr (BWD) {
-          if (slice < p.nsl) {
-            uint4* e = p.e + ((slot_head(i) * p.nsl + slice) * 4 + 2 * q) * 64 + l;
-            e[0] = __builtin_bit_cast(uint4, x[2 * q]);
-            e[64] = __builtin_bit_cast(uint4, x[2 * q + 1]);
-          }
-        }
-        const f32x4_t u0 = x[2 * q] * *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + row);
-        const f32x4_t u1 = x[2 * q + 1] * *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + row + 4);
-        xu[(w * 4 + 2 * q) * 64 + l] = u0;
-        xu[(w * 4 + 2 * q + 1) * 64 + l] = u1;
+        xe(i)[(w * 4 + 2 * q) * 64 + l] = x[2 * q];
+        xe(i)[(w * 4 + 2 * q + 1) * 64 + l] = x[2 * q + 1];
         float v[8];
-        pair8(u0 * *reinterpret_cast<const f32x4_t*>(gs + GATE_OUT * CH + row),
-              u1 * *reinterpret_cast<const f32x4_t*>(gs + GATE_OUT * CH + row + 4), v);
+        pair8(x[2 * q] * bo[2 * q], x[2 * q + 1] * bo[2 * q + 1], v);
         f3[q] = F::split3(v);
       }
-      // S <- exp(c_last) S + k^T (exp(c_last - c) u)
-      const float last = gs[GATE_IN * CH + CH - 1];
+      if (i + 1 < nchunk) tf.request(p.tf + slot_head(i + 1) * FRAG_PIECES);
+      // S <- exp(c_last) S + k^T (beta exp(c_last - c) e), four tiles at a time: the first four are split for the
+      // next chunk while the others' products run
 #pragma unroll
-      for (int j = 0; j < 2 * NT; ++j) {
-        S[j] *= last;
+      for (int j0 = 0; j0 < 2 * NT; j0 += 4) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) S[j] = mma(F::template load_tr<8>(kt + pair_col(j), LDN, 32 * ks + 8 * g), f3[ks], S[j]);
-        if (j & 1) split_state(j >> 1);
+        for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+#pragma unroll
+            for (int j = j0; j < j0 + 4; ++j) S[j] = mma_term(kc[j][ks], f3[ks], S[j], term);
+          }
+        }
+        split_state(j0 / 2);
+        split_state(j0 / 2 + 1);
       }
-      __syncthreads();
     }
+    if (nchunk) __syncthreads();
     if constexpr (!BWD) {
       if (p.final && col < p.P) {
 #pragma unroll
@@ -433,13 +543,14 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
   const int64_t hp = static_cast<int64_t>(p.H) * p.P;
 
   if (w < NSW + Cf::NOUT) {
-    // ---- output waves: the columns of state waves 2 ow and 2 ow + 1
+    // ---- output waves: the columns of NZ state waves each
+    constexpr int NZ = Cf::NZ;
     const int ow = w - NSW;
-    const int col0 = PS * ps + 2 * SLICE * ow, slice0 = ps * NSW + 2 * ow;
+    const int col0 = PS * ps + NZ * SLICE * ow, slice0 = ps * NSW + NZ * ow;
     typename F::X xq[Cf::QLDS ? 1 : 4][NT];
     FragRegs pf;
     typedef typename std::conditional<sizeof(T) == 2, uint2, uint4>::type Raw4;   // four values as they lie
-    Raw4 dox[2][4];
+    Raw4 dox[NZ][4];
     auto request_out = [&](int i) {
       const int len = length(i);
       const int64_t row0 = static_cast<int64_t>(CH) * i;
@@ -457,7 +568,7 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
       }
       if constexpr (BWD) {
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
+        for (int z = 0; z < NZ; ++z) {
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const int row = 16 * t + c, cc = col0 + SLICE * z + 4 * g;
@@ -468,40 +579,43 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
         }
       }
     };
-    uint4 us[2][NT][XP];
-    f32x4_t uu[2][4];
+    uint4 us[NZ][NT][XP];
+    f32x4_t ee[NZ][4], be[4];
     float in[4];
     auto take = [&](int i) {
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
+      for (int z = 0; z < NZ; ++z) {
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
 #pragma unroll
-          for (int t = 0; t < XP; ++t) us[z][q][t] = xs[(((2 * ow + z) * NT + q) * XP + t) * 64 + l];
+          for (int t = 0; t < XP; ++t) us[z][q][t] = xs(i)[(((NZ * ow + z) * NT + q) * XP + t) * 64 + l];
         }
 #pragma unroll
-        for (int t = 0; t < 4; ++t) uu[z][t] = xu[((2 * ow + z) * 4 + t) * 64 + l];
+        for (int t = 0; t < 4; ++t) ee[z][t] = xe(i)[((NZ * ow + z) * 4 + t) * 64 + l];
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) in[t] = p.scale * gbuf(i)[GATE_IN * CH + 16 * t + c];
+      for (int t = 0; t < 4; ++t) {
+        in[t] = p.scale * gbuf(i)[GATE_IN * CH + 16 * t + c];
+        be[t] = *reinterpret_cast<const f32x4_t*>(gbuf(i) + GATE_BETA * CH + pair_col(t) + 8 * g);
+      }
     };
     auto out = [&](int i) {
       const int len = length(i);
       const int64_t sh = slot_head(i);
-      typename F::S uf[2][2];
+      typename F::S uf[NZ][2];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
+      for (int z = 0; z < NZ; ++z) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           float v[8];
-          pair8(uu[z][2 * q], uu[z][2 * q + 1], v);
+          pair8(ee[z][2 * q] * be[2 * q], ee[z][2 * q + 1] * be[2 * q + 1], v);
           uf[z][q] = F::split(v);
         }
       }
       if constexpr (BWD) {
         char* base = static_cast<char*>(p.s) + sh * p.rows * ND * 4;
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
+        for (int z = 0; z < NZ; ++z) {
           const int64_t r = col0 + SLICE * z + c;
           if (slice0 + z < p.nsl) {
 #pragma unroll
@@ -515,6 +629,8 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
               }
             }
 #pragma unroll
+            for (int t = 0; t < 4; ++t) p.e[((sh * p.nsl + slice0 + z) * 4 + t) * 64 + l] = __builtin_bit_cast(uint4, ee[z][t]);
+#pragma unroll
             for (int q = 0; q < 2; ++q) F::store(static_cast<T*>(p.u) + (sh * p.rows + r) * CH + 32 * q + 8 * g, F::hi(uf[z][q]));
           }
         }
@@ -524,33 +640,38 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
       // o, transposed: rows are value columns 4 g + r, columns are chunk rows 16 t + c
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        f32x4_t acc[2] = {zero4(), zero4()};
+        f32x4_t acc[NZ];
+#pragma unroll
+        for (int z = 0; z < NZ; ++z) acc[z] = zero4();
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
           typename F::X x;
           if constexpr (Cf::QLDS) x = F::load(qt + (16 * t + c) * LDN + 32 * q + 8 * g);
           else x = xq[t][q];
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
+          for (int z = 0; z < NZ; ++z) {
             if constexpr (XP == 2) acc[z] = mma(F::from_pieces(us[z][q]), x, acc[z]);
             else acc[z] = mma(__builtin_bit_cast(typename F::X, us[z][q][0]), x, acc[z]);
           }
         }
-        acc[0] *= in[t];
-        acc[1] *= in[t];
+#pragma unroll
+        for (int z = 0; z < NZ; ++z) acc[z] *= in[t];
 #pragma unroll
         for (int ks = 0; ks <= (t >> 1); ++ks) {
-          typename F::S sc;
-          if constexpr (Cf::QLDS) sc = frag_at<T>(pt, lower_frag(t, ks));
-          else sc = pf.get<T>(lower_frag(t, ks));
+          if constexpr (XP == 2) {
+            typename F::S sc;
+            if constexpr (Cf::QLDS) sc = frag_at<T>(pt, lower_frag(t, ks));
+            else sc = pf.get<T>(lower_frag(t, ks));
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            if constexpr (XP == 2) acc[z] = mma(uf[z][ks], sc, acc[z]);
-            else acc[z] = mma(F::hi(uf[z][ks]), sc, acc[z]);
+            for (int z = 0; z < NZ; ++z) acc[z] = mma(uf[z][ks], sc, acc[z]);
+          } else {
+            const typename F::X sc = F::load(reinterpret_cast<const T*>(pt + lower_frag(t, ks) * 64 + l));
+#pragma unroll
+            for (int z = 0; z < NZ; ++z) acc[z] = mma(uf[z][ks], sc, acc[z]);
           }
         }
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
+        for (int z = 0; z < NZ; ++z) {
           if constexpr (BWD) {
             const f32x4_t d = acc[z] * ssd::load4f<T>(reinterpret_cast<const T*>(&dox[z][t]));
             const float s = ssd::sum_kgroups((d[0] + d[1]) + (d[2] + d[3]));
@@ -564,9 +685,10 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
       }
     };
     request_out(0);
+    __syncthreads();
     for (int i = 0; i < nchunk; ++i) {
       if (i > 0) take(i - 1);
-      __syncthreads();
+      if constexpr (XB == 0) __syncthreads();
       if (i > 0) {
         out(i - 1);
         request_out(i);
@@ -583,29 +705,29 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
   const int pcols = min(PS, p.P - PS * ps);
   const T* kp = static_cast<const T*>(p.k) + row_offset(s0, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N;
   const T* vp = static_cast<const T*>(p.v) + row_offset(s0, p.L, p.v_sb, p.v_sl) + static_cast<int64_t>(h) * p.P + PS * ps;
-  constexpr int GI = (3 * CH + Cf::HT - 1) / Cf::HT;
+  constexpr int GI = (WALK_GATES * CH + Cf::HT - 1) / Cf::HT;
   TileN tk, tq;
   TileP tv;
-  Pieces<FRAG_PIECES, Cf::HT> tp;
+  Pieces<Cf::PIECES, Cf::HT> tp;
   float tg[GI];
   auto request_state = [&](int i) {
     const int64_t row = static_cast<int64_t>(CH) * i;
     tk.load(kp + row * p.k_sl, p.k_sl, length(i), p.N, ht);
     tv.load(vp + row * p.v_sl, p.v_sl, length(i), pcols, ht);
 #pragma unroll
-    for (int k = 0; k < GI; ++k) tg[k] = ht + k * Cf::HT < 3 * CH ? p.gates[slot_head(i) * (GATES * CH) + ht + k * Cf::HT] : 0.f;
+    for (int k = 0; k < GI; ++k) tg[k] = ht + k * Cf::HT < WALK_GATES * CH ? p.gates[slot_head(i) * (GATES * CH) + ht + k * Cf::HT] : 0.f;
   };
   auto stage_state = [&](int i) {
     tk.store(kbuf(i), ht);
     tv.store(vbuf(i), ht);
 #pragma unroll
     for (int k = 0; k < GI; ++k)
-      if (ht + k * Cf::HT < 3 * CH) gbuf(i)[ht + k * Cf::HT] = tg[k];
+      if (ht + k * Cf::HT < WALK_GATES * CH) gbuf(i)[ht + k * Cf::HT] = tg[k];
   };
   auto request_scores = [&](int i) {
     if constexpr (Cf::QLDS) {
       tq.load(qp + static_cast<int64_t>(CH) * i * p.q_sl, p.q_sl, length(i), p.N, ht);
-      tp.load(p.pf + slot_head(i) * FRAG_PIECES, ht);
+      tp.load(p.pf + slot_head(i) * Cf::PIECES, ht);
     }
   };
   auto stage_scores = [&](int i) {
@@ -618,8 +740,9 @@ __global__ __launch_bounds__(128 * NSW) void k_delta_walk(Problem p) {
   request_scores(0);
   stage_state(0);
   if (nchunk > 1) request_state(1);
+  __syncthreads();
   for (int i = 0; i < nchunk; ++i) {
-    __syncthreads();
+    if constexpr (XB == 0) __syncthreads();
     stage_scores(i);
     if (i + 1 < nchunk) {
       request_scores(i + 1);
@@ -642,7 +765,7 @@ template <typename K> int go(K kernel, dim3 grid, int threads, size_t lds, hipSt
 int launch_starts(const Problem& p, hipStream_t s) { return go(k_delta_starts, dim3(1), ST_THR, 0, s, p); }
 
 template <typename T, int NT, bool BWD> int prep(const Problem& p, hipStream_t s) {
-  return go(k_delta_prep<T, NT, BWD>, dim3(p.nslots, p.H), 256, PrepCfg<T, NT, BWD>::LDS, s, p);
+  return go(k_delta_prep<T, NT, BWD>, dim3(p.nslots, p.G * ((p.hpg + p.hb - 1) / p.hb)), 256, PrepCfg<BWD>::lds(p.hb), s, p);
 }
 template <typename T, int NT, bool BWD, int NSW> int walk_of(const Problem& p, hipStream_t s) {
   using Cf = WalkCfg<T, NT, BWD, NSW>;

@@ -49,13 +49,13 @@ template <typename T, int NT> struct RwalkCfg {
   static constexpr size_t OFF_V = OFF_DO + 2 * P_BYTES;
   static constexpr size_t OFF_D0 = OFF_V + 2 * P_BYTES;      // scores^T dout
   static constexpr size_t OFF_Q0 = OFF_D0 + 16 * 64 * NSW * 4;
-  static constexpr size_t OFF_DU = OFF_Q0 + 16 * 64 * NSW * 2 * NT;
+  static constexpr size_t OFF_DU = OFF_Q0 + KBUF * 16 * 64 * NSW * 2 * NT;   // q^T dout, twice as k
   static constexpr size_t OFF_XS = OFF_DU + 16 * 64 * NSW * 4;
   static constexpr size_t OFF_G = OFF_XS + 16 * 64 * NSW * NT * 2;
-  static constexpr size_t LDS = OFF_G + 4 * sizeof(float) * 3 * CH;   // the gates of four chunks
+  static constexpr size_t LDS = OFF_G + 4 * sizeof(float) * RWALK_GATES * CH;   // the gates of four chunks
 };
 
-template <typename T, int NT> __global__ __launch_bounds__(64 * 6) void k_delta_rwalk(Problem p) {
+template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_delta_rwalk(Problem p) {
   using Cf = RwalkCfg<T, NT>;
   using F = Fr<T>;
   using TileN = typename Cf::TileN;
@@ -66,9 +66,9 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) void k_delta_
   auto qbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_Q + (i & KB) * Cf::N_BYTES); };
   auto dobuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_DO + (i & 1) * Cf::P_BYTES); };
   auto vbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_V + (i & 1) * Cf::P_BYTES); };
-  auto gbuf = [&](int i) { return reinterpret_cast<float*>(smem + Cf::OFF_G) + (i & 3) * 3 * CH; };
+  auto gbuf = [&](int i) { return reinterpret_cast<float*>(smem + Cf::OFF_G) + (i & 3) * RWALK_GATES * CH; };
   f32x4_t* xd0 = reinterpret_cast<f32x4_t*>(smem + Cf::OFF_D0);   // [wave][t][lane]
-  f32x4_t* xq0 = reinterpret_cast<f32x4_t*>(smem + Cf::OFF_Q0);   // [wave][j][lane]
+  auto xq0 = [&](int i) { return reinterpret_cast<f32x4_t*>(smem + Cf::OFF_Q0) + (i & KB) * 64 * NSW * 2 * NT; };   // [wave][j][lane]
   f32x4_t* xdu = reinterpret_cast<f32x4_t*>(smem + Cf::OFF_DU);   // [wave][t][lane]
   uint4* xs = reinterpret_cast<uint4*>(smem + Cf::OFF_XS);        // [wave][q][term][lane]
 
@@ -104,16 +104,38 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) void k_delta_
       FragRegs tf;
       tf.request(p.ttf + slot_head(last) * FRAG_PIECES);
       __syncthreads();
-      __syncthreads();
       for (int i = last; i >= 0; --i) {
         const T* kt = kbuf(i);
         const float* gs = gbuf(i);
-        f32x4_t d0[4], q0[2 * NT];
+        auto gate = [&](int which, int row) { return *reinterpret_cast<const f32x4_t*>(gs + which * CH + row); };
+        __syncthreads();   // second barrier of the chunk before (the first time: of what came ahead)
+        f32x4_t d0[4], q0[2 * NT], out[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) d0[t] = xd0[(w * 4 + t) * 64 + l];
+        for (int t = 0; t < 4; ++t) {
+          d0[t] = xd0[(w * 4 + t) * 64 + l];
+          out[t] = gate(GATE_OUT, pair_col(t) + 8 * g);
+        }
+        const float dec = gs[GATE_IN * CH + CH - 1];
+        if constexpr (KB == 0) {
 #pragma unroll
-        for (int j = 0; j < 2 * NT; ++j) q0[j] = xq0[(w * 2 * NT + j) * 64 + l];
+          for (int j = 0; j < 2 * NT; ++j) q0[j] = xq0(i)[(w * 2 * NT + j) * 64 + l];
+        }
+        typename F::X kf[4][NT];
+        if constexpr (KB != 0) {   // k's rows are staged: on their way while the others take what they need
+#pragma unroll
+          for (int q = 0; q < NT; ++q) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) kf[t][q] = F::load(kt + perm_row(t, c) * LDN + 32 * q + 8 * g);
+          }
+        }
         __syncthreads();
+        if constexpr (KB == 0) {
+#pragma unroll
+          for (int q = 0; q < NT; ++q) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) kf[t][q] = F::load(kt + perm_row(t, c) * LDN + 32 * q + 8 * g);
+          }
+        }
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
           uint4 u[2];
@@ -122,16 +144,31 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) void k_delta_
           xs[((w * NT + q) * 2 + 1) * 64 + l] = u[1];
         }
         f32x4_t x[4];
+        typename F::X kc[2 * NT][2];
 #pragma unroll
         for (int t = 0; t < 4; ++t) x[t] = zero4();
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t) x[t] = mma(F::load(kt + perm_row(t, c) * LDN + 32 * q + 8 * g), sf[q], x[t]);
-        }
+          for (int term = 0; term < 2; ++term) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          x[t] = x[t] * *reinterpret_cast<const f32x4_t*>(gs + GATE_OUT * CH + pair_col(t) + 8 * g) + d0[t];
+            for (int t = 0; t < 4; ++t) x[t] = mma_term(kf[t][q], sf[q], x[t], term);
+          }
+          // beside it the first part of the next dS, and k's columns for the last product
+#pragma unroll
+          for (int j = 2 * q; j < 2 * q + 2; ++j) {
+            if constexpr (KB != 0) q0[j] = xq0(i)[(w * 2 * NT + j) * 64 + l];
+            S[j] = dec * S[j] + q0[j];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) kc[j][ks] = F::template load_tr<8>(kt + pair_col(j), LDN, 32 * ks + 8 * g);
+          }
+        }
+        f32x4_t bi[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          x[t] = x[t] * out[t] + d0[t];
+          bi[t] = gate(GATE_BI, pair_col(t) + 8 * g);
+        }
         // Du = du + (T^T - I) du
         typename F::S f2[2];
 #pragma unroll
@@ -143,32 +180,37 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) void k_delta_
 #pragma unroll
         for (int ks = 1; ks >= 0; --ks) {
 #pragma unroll
-          for (int t = 0; t < 2 * ks + 2; ++t) x[t] = mma(tf.get<T>(upper_frag(t, ks)), f2[ks], x[t]);
+          for (int term = 0; term < 3; ++term) {
+#pragma unroll
+            for (int t = 0; t < 2 * ks + 2; ++t) x[t] = mma_term(tf.get<T>(upper_frag(t, ks)), f2[ks], x[t], term);
+          }
         }
-        if (i > 0) tf.request(p.ttf + slot_head(i - 1) * FRAG_PIECES);
         // dS <- exp(c_last) dS + q^T (scale exp(c) dout) - k^T (exp(c) beta Du)
         typename F::S3 f3[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int row = 32 * q + 8 * g;
           xdu[(w * 4 + 2 * q) * 64 + l] = x[2 * q];
           xdu[(w * 4 + 2 * q + 1) * 64 + l] = x[2 * q + 1];
           float v[8];
-          pair8(-x[2 * q] * *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + row) * *reinterpret_cast<const f32x4_t*>(gs + GATE_IN * CH + row),
-                -x[2 * q + 1] * *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + row + 4) *
-                    *reinterpret_cast<const f32x4_t*>(gs + GATE_IN * CH + row + 4), v);
+          pair8(x[2 * q] * bi[2 * q], x[2 * q + 1] * bi[2 * q + 1], v);
           f3[q] = F::split3(v);
         }
-        const float dec = gs[GATE_IN * CH + CH - 1];
+        if (i > 0) tf.request(p.ttf + slot_head(i - 1) * FRAG_PIECES);
 #pragma unroll
-        for (int j = 0; j < 2 * NT; ++j) {
-          S[j] = dec * S[j] + q0[j];
+        for (int j0 = 0; j0 < 2 * NT; j0 += 4) {
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) S[j] = mma(F::template load_tr<8>(kt + pair_col(j), LDN, 32 * ks + 8 * g), f3[ks], S[j]);
-          if (j & 1) split_state(j >> 1);
+          for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+#pragma unroll
+              for (int j = j0; j < j0 + 4; ++j) S[j] = mma_term(kc[j][ks], f3[ks], S[j], term);
+            }
+          }
+          split_state(j0 / 2);
+          split_state(j0 / 2 + 1);
         }
-        __syncthreads();
       }
+      __syncthreads();
       // the first chunk's <entering state, its gradient>: the entering state is the initial state
       float phi = 0.f;
       if (p.h0 && col < p.P) {
@@ -251,7 +293,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) void k_delta_
           for (int z = 0; z < NSW; ++z) acc[z] = mma(xq, fd[z][ks], acc[z]);
         }
 #pragma unroll
-        for (int z = 0; z < NSW; ++z) xq0[(z * 2 * NT + j) * 64 + l] = acc[z];
+        for (int z = 0; z < NSW; ++z) xq0(i)[(z * 2 * NT + j) * 64 + l] = acc[z];
       }
     };
     pf.request(p.ptf + slot_head(last) * FRAG_PIECES);
@@ -376,7 +418,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) void k_delta_
   const T* vp = static_cast<const T*>(p.v) + row_offset(s0, p.L, p.v_sb, p.v_sl) + static_cast<int64_t>(h) * p.P + PS * ps;
   TileN tk, tq;
   TileP td, tv;
-  float tg[3];
+  float tg[RWALK_GATES];
   auto request_k = [&](int i) { tk.load(kp + static_cast<int64_t>(CH) * i * p.k_sl, p.k_sl, length(i), p.N, l); };
   auto request_v = [&](int i) { tv.load(vp + static_cast<int64_t>(CH) * i * p.v_sl, p.v_sl, length(i), pcols, l); };
   // for the wave ahead: q, dout and the gates
@@ -385,13 +427,13 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) void k_delta_
     tq.load(qp + row * p.q_sl, p.q_sl, length(i), p.N, l);
     td.load(static_cast<const T*>(p.dout) + (s0 + row) * hp + static_cast<int64_t>(h) * p.P + PS * ps, hp, length(i), pcols, l);
 #pragma unroll
-    for (int k = 0; k < 3; ++k) tg[k] = p.gates[slot_head(i) * (GATES * CH) + k * CH + l];
+    for (int k = 0; k < RWALK_GATES; ++k) tg[k] = p.gates[slot_head(i) * (GATES * CH) + k * CH + l];
   };
   auto stage_q = [&](int i) {
     tq.store(qbuf(i), l);
     td.store(dobuf(i), l);
 #pragma unroll
-    for (int k = 0; k < 3; ++k) gbuf(i)[k * CH + l] = tg[k];
+    for (int k = 0; k < RWALK_GATES; ++k) gbuf(i)[k * CH + l] = tg[k];
   };
   request_k(last);
   request_q(last);

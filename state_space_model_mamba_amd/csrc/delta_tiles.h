@@ -214,6 +214,36 @@ __device__ __forceinline__ f32x4_t mma_term(const Fr<bf16_t>::S& a, const Fr<bf1
 // float32: the whole product, taken with the first term
 __device__ __forceinline__ f32x4_t mma_term(const f32x8_t& a, const f32x8_t& b, f32x4_t c, int term) { return term ? c : mma(a, b, c); }
 
+// What the backward keeps per slice of 16 value columns (states, their gradients, corrections) lies in memory as the
+// lanes hold it, 16-byte pieces [half][q][lane]: piece (half, q) of lane (g, c) is column c's values 32 q + 8 g .. + 7
+// (bf16; half: the term) or 32 q + 8 g + 4 half .. + 3 (float32).  A wave then stores and loads whole kilobytes;
+// column by column they took 4 times as long in the memory pipeline.
+//
+// SLICES slices of such pieces as an LDS tile with a row for every value column and NQ * 32 values in it, by NTHR
+// threads; slices >= nslices are zero and not read.
+template <typename T, int SLICES, int NQ, int NTHR> struct SliceTile {
+  static constexpr int HALVES = sizeof(T) / 2, PER = HALVES * NQ * 64, NV = SLICES * PER, IT = (NV + NTHR - 1) / NTHR;
+  static constexpr int VEC = Vec16<T>::N, LD = NQ * 32 + VEC, LDS_ELEMS = SLICES * 16 * LD;
+  f32x4_t buf[IT];
+  // base: the first slice; pitch: pieces from one slice to the next
+  __device__ __forceinline__ void load(const uint4* base, int pitch, int nslices, int tid) {
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = tid + k * NTHR, s = v / PER;
+      buf[k] = zero4();
+      if ((NV % NTHR == 0 || v < NV) && s < nslices) buf[k] = reinterpret_cast<const f32x4_t*>(base)[s * pitch + v % PER];
+    }
+  }
+  __device__ __forceinline__ void store(T* lds, int tid) const {
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = tid + k * NTHR, r = v % PER, l = r & 63, q = (r >> 6) % NQ, half = (r >> 6) / NQ;
+      if (NV % NTHR == 0 || v < NV)
+        *reinterpret_cast<f32x4_t*>(lds + (v / PER * 16 + (l & 15)) * LD + 32 * q + 8 * (l >> 4) + 4 * half) = buf[k];
+    }
+  }
+};
+
 // first column of tile t among columns in pair order, for load_tr<8>
 __device__ __forceinline__ constexpr int pair_col(int t) { return 32 * (t >> 1) + 4 * (t & 1); }
 

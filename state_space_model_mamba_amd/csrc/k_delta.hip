@@ -391,7 +391,8 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
   using F = Fr<T>;
   using TileN = typename Cf::TileN;
   using TileP = typename Cf::TileP;
-  constexpr int ND = Cf::ND, LDN = TileN::LD, LDP = TileP::LD, XP = Cf::XP, PS = Cf::PS, XB = Cf::XBUF - 1;
+  constexpr int LDN = TileN::LD, LDP = TileP::LD, XP = Cf::XP, PS = Cf::PS, XB = Cf::XBUF - 1;
+  constexpr int HALVES = sizeof(T) / 2;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   auto kbuf = [&](int i) { return reinterpret_cast<T*>(smem + (i & 1) * Cf::N_BYTES); };
   auto vbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_V + (i & 1) * Cf::V_BYTES); };
@@ -500,26 +501,35 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
           for (int t = 2 * ks; t < 4; ++t) x[t] = mma_term(tf.get<T>(lower_frag(t, ks)), f2[ks], x[t], term);
         }
       }
-      typename F::S3 f3[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      // S <- exp(c_last) S + k^T (beta exp(c_last - c) e), by halves of the chunk's rows: the first half's products run
+      // while the second half is split, and of the second half's the last four tiles' while the first four are split
+      // for the next chunk.  The next T' is requested piece by piece between them.
+      const uint4* tnext = p.tf + slot_head(i + 1 < nchunk ? i + 1 : i) * FRAG_PIECES + l;
+      auto correction = [&](int q) {
         xe(i)[(w * 4 + 2 * q) * 64 + l] = x[2 * q];
         xe(i)[(w * 4 + 2 * q + 1) * 64 + l] = x[2 * q + 1];
         float v[8];
         pair8(x[2 * q] * bo[2 * q], x[2 * q + 1] * bo[2 * q + 1], v);
-        f3[q] = F::split3(v);
+        return F::split3(v);
+      };
+      const typename F::S3 fa = correction(0);
+#pragma unroll
+      for (int term = 0; term < 3; ++term) {
+#pragma unroll
+        for (int j = 0; j < 2 * NT; ++j) S[j] = mma_term(kc[j][0], fa, S[j], term);
+        tf.u[2 * term] = tnext[2 * term * 64];
+        tf.u[2 * term + 1] = tnext[(2 * term + 1) * 64];
       }
-      if (i + 1 < nchunk) tf.request(p.tf + slot_head(i + 1) * FRAG_PIECES);
-      // S <- exp(c_last) S + k^T (beta exp(c_last - c) e), four tiles at a time: the first four are split for the
-      // next chunk while the others' products run
+      const typename F::S3 fb = correction(1);
 #pragma unroll
       for (int j0 = 0; j0 < 2 * NT; j0 += 4) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+        for (int term = 0; term < 3; ++term) {
 #pragma unroll
-          for (int term = 0; term < 3; ++term) {
-#pragma unroll
-            for (int j = j0; j < j0 + 4; ++j) S[j] = mma_term(kc[j][ks], f3[ks], S[j], term);
+          for (int j = j0; j < j0 + 4; ++j) S[j] = mma_term(kc[j][1], fb, S[j], term);
+          if (j0 == 0) {
+            tf.u[6 + 2 * term] = tnext[(6 + 2 * term) * 64];
+            tf.u[7 + 2 * term] = tnext[(7 + 2 * term) * 64];
           }
         }
         split_state(j0 / 2);
@@ -613,25 +623,24 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
         }
       }
       if constexpr (BWD) {
-        char* base = static_cast<char*>(p.s) + sh * p.rows * ND * 4;
 #pragma unroll
         for (int z = 0; z < NZ; ++z) {
-          const int64_t r = col0 + SLICE * z + c;
           if (slice0 + z < p.nsl) {
+            const int64_t at = sh * p.nsl + slice0 + z;
 #pragma unroll
-            for (int q = 0; q < NT; ++q) {
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                if constexpr (sizeof(T) == 2)
-                  *reinterpret_cast<uint4*>(base + ((static_cast<int64_t>(t) * p.rows + r) * ND + 32 * q + 8 * g) * 2) = us[z][q][t];
-                else
-                  *reinterpret_cast<uint4*>(base + (r * ND + 32 * q + 8 * g + 4 * t) * 4) = us[z][q][t];
-              }
+              for (int q = 0; q < NT; ++q) p.s[((at * 2 + t) * NT + q) * 64 + l] = us[z][q][t];
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) p.e[((sh * p.nsl + slice0 + z) * 4 + t) * 64 + l] = __builtin_bit_cast(uint4, ee[z][t]);
+            for (int t = 0; t < 4; ++t) p.e[(at * 4 + t) * 64 + l] = __builtin_bit_cast(uint4, ee[z][t]);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) F::store(static_cast<T*>(p.u) + (sh * p.rows + r) * CH + 32 * q + 8 * g, F::hi(uf[z][q]));
+            for (int q = 0; q < 2; ++q) {
+              uint4 u[2];
+              F::pieces(uf[z][q], u);
+#pragma unroll
+              for (int t = 0; t < HALVES; ++t) p.u[((at * HALVES + t) * 2 + q) * 64 + l] = u[t];
+            }
           }
         }
       }

@@ -60,7 +60,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__
   using F = Fr<T>;
   using TileN = typename Cf::TileN;
   using TileP = typename Cf::TileP;
-  constexpr int ND = Cf::ND, LDN = TileN::LD, LDP = TileP::LD, NSW = Cf::NSW, PS = Cf::PS, KB = Cf::KBUF - 1;
+  constexpr int LDN = TileN::LD, LDP = TileP::LD, NSW = Cf::NSW, PS = Cf::PS, KB = Cf::KBUF - 1;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   auto kbuf = [&](int i) { return reinterpret_cast<T*>(smem + (i & KB) * Cf::N_BYTES); };
   auto qbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_Q + (i & KB) * Cf::N_BYTES); };
@@ -186,24 +186,33 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__
           }
         }
         // dS <- exp(c_last) dS + q^T (scale exp(c) dout) - k^T (exp(c) beta Du)
-        typename F::S3 f3[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        // (in the forward walk's order)
+        const uint4* tnext = p.ttf + slot_head(i > 0 ? i - 1 : i) * FRAG_PIECES + l;
+        auto correction = [&](int q) {
           xdu[(w * 4 + 2 * q) * 64 + l] = x[2 * q];
           xdu[(w * 4 + 2 * q + 1) * 64 + l] = x[2 * q + 1];
           float v[8];
           pair8(x[2 * q] * bi[2 * q], x[2 * q + 1] * bi[2 * q + 1], v);
-          f3[q] = F::split3(v);
+          return F::split3(v);
+        };
+        const typename F::S3 fa = correction(0);
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+#pragma unroll
+          for (int j = 0; j < 2 * NT; ++j) S[j] = mma_term(kc[j][0], fa, S[j], term);
+          tf.u[2 * term] = tnext[2 * term * 64];
+          tf.u[2 * term + 1] = tnext[(2 * term + 1) * 64];
         }
-        if (i > 0) tf.request(p.ttf + slot_head(i - 1) * FRAG_PIECES);
+        const typename F::S3 fb = correction(1);
 #pragma unroll
         for (int j0 = 0; j0 < 2 * NT; j0 += 4) {
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
+          for (int term = 0; term < 3; ++term) {
 #pragma unroll
-            for (int term = 0; term < 3; ++term) {
-#pragma unroll
-              for (int j = j0; j < j0 + 4; ++j) S[j] = mma_term(kc[j][ks], f3[ks], S[j], term);
+            for (int j = j0; j < j0 + 4; ++j) S[j] = mma_term(kc[j][1], fb, S[j], term);
+            if (j0 == 0) {
+              tf.u[6 + 2 * term] = tnext[(6 + 2 * term) * 64];
+              tf.u[7 + 2 * term] = tnext[(7 + 2 * term) * 64];
             }
           }
           split_state(j0 / 2);
@@ -311,21 +320,20 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__
   if (w < 2 * NSW + 1) {
     // ---- the waves behind, one for each state wave: with the residuals, and the entering state of the chunk after
     // (for its inner product)
-    const int z = w - NSW - 1, slice = ps * NSW + z, col = PS * ps + SLICE * z + c;
+    const int z = w - NSW - 1, slice = ps * NSW + z;
+    constexpr int HALVES = sizeof(T) / 2;
     uint4 te[4], ss[NT][2], us[NT][2];
     f32x4_t du[4];
-    const int64_t state_row = static_cast<int64_t>(col) * ND + 8 * g;   // of S and dS
     auto request = [&](int i) {
       const uint4* e = p.e + (slot_head(i) * p.nsl + slice) * 4 * 64 + l;
 #pragma unroll
       for (int t = 0; t < 4; ++t) te[t] = e[t * 64];
       if (i < last) {
-        const char* base = static_cast<const char*>(p.s) + slot_head(i + 1) * p.rows * ND * 4 + state_row * static_cast<int>(sizeof(T));
-        const int64_t lo = sizeof(T) == 2 ? static_cast<int64_t>(p.rows) * ND * 2 : 16;   // from the first term to the second
+        const uint4* at = p.s + (slot_head(i + 1) * p.nsl + slice) * 2 * NT * 64 + l;
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
-          ss[q][0] = *reinterpret_cast<const uint4*>(base + 32 * q * sizeof(T));
-          ss[q][1] = *reinterpret_cast<const uint4*>(base + lo + 32 * q * sizeof(T));
+          ss[q][0] = at[q * 64];
+          ss[q][1] = at[(NT + q) * 64];
         }
       }
     };
@@ -341,7 +349,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__
     auto behind = [&](int i) {
       const int len = length(i);
       const float* gs = gbuf(i);
-      const T* vt = vbuf(i);
+      T* vt = vbuf(i) + SLICE * z;   // this wave's columns of v, and then of dv
       const int64_t at = (slot_head(i) * p.nsl + slice) * CH;
       if (i < last) {
         float phi = 0.f;
@@ -362,7 +370,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__
         be[t] = du[t] * __builtin_bit_cast(f32x4_t, te[t]);
         const int row = pair_col(t) + 8 * g;
         du[t] *= *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + row);   // dv
-        vv[t] = du[t] * F::load4_tr(vt + SLICE * z, LDP, row);
+        vv[t] = du[t] * F::load4_tr(vt, LDP, row);
       }
       if (i > 0) request(i - 1);
 #pragma unroll
@@ -380,21 +388,25 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__
           *reinterpret_cast<f32x4_t*>(p.vv + at + pair_col(t) + 8 * g) = vv[t];
         }
       }
-      T* ds = static_cast<T*>(p.ds) + slot_head(i) * p.rows * ND + state_row;
+      uint4* ds = p.ds + (slot_head(i) * p.nsl + slice) * HALVES * NT * 64 + l;
 #pragma unroll
-      for (int q = 0; q < NT; ++q) F::store(ds + 32 * q, F::hi(F::from_pieces(us[q])));
-      // dv, a 16-column stretch of every row: rows at a uniform distance from the wave's first
-      char* dv = reinterpret_cast<char*>(static_cast<T*>(p.dv) + (s0 + static_cast<int64_t>(CH) * i) * hp + static_cast<int64_t>(h) * p.P + PS * ps + SLICE * z);
-      const uint32_t off = static_cast<uint32_t>(8 * g * static_cast<uint32_t>(hp) + c) * static_cast<uint32_t>(sizeof(T));
-      if (col < p.P) {
+      for (int q = 0; q < NT; ++q) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < HALVES; ++t) ds[(t * NT + q) * 64] = us[q][t];
+      }
+      // dv by rows, through v's place in LDS: 16 two-byte stores of four 32-byte stretches each would hold up the
+      // memory pipeline
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if (len == CH || pair_col(t) + 8 * g + r < len)
-              *reinterpret_cast<T*>(dv + (pair_col(t) + r) * hp * static_cast<int>(sizeof(T)) + off) = ssd::Elem<T>::from_f(du[t][r]);
-          }
-        }
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) vt[(pair_col(t) + 8 * g + r) * LDP + c] = ssd::Elem<T>::from_f(du[t][r]);
+      }
+      T* dv = static_cast<T*>(p.dv) + (s0 + static_cast<int64_t>(CH) * i + l) * hp + static_cast<int64_t>(h) * p.P + PS * ps + SLICE * z;
+      constexpr int VEC = Vec16<T>::N;
+      if (l < len) {
+#pragma unroll
+        for (int k = 0; k < SLICE; k += VEC)
+          if (PS * ps + SLICE * z + k < p.P) *reinterpret_cast<uint4*>(dv + k) = *reinterpret_cast<const uint4*>(vt + l * LDP + k);
       }
     };
     __syncthreads();
@@ -485,8 +497,8 @@ template <typename T, int NT> struct GradCfg {
   static constexpr int PSL = sizeof(T) == 2 ? 64 : 32;   // value columns staged at once
   using TileN = Tile<T, CH, ND, GTHR>;
   using TileP = Tile<T, CH, PSL, GTHR>;    // dout, dv
-  using TileU = Tile<T, PSL, CH, GTHR>;    // u, a value column per row
-  using TileS = Tile<T, PSL, ND, GTHR>;    // S, dS, a value column per row
+  using TileU = SliceTile<T, PSL / SLICE, 2, GTHR>;    // u, a value column per row
+  using TileS = SliceTile<T, PSL / SLICE, NT, GTHR>;   // S, dS, a value column per row
   using TileM = Tile<T, CH, CH, GTHR>;     // dP, F + F^T (over the tiles above)
   static constexpr size_t OFF_Q = sizeof(T) * TileN::LDS_ELEMS;
   static constexpr size_t OFF_DO = 2 * OFF_Q;
@@ -504,7 +516,7 @@ template <typename T, int NT> struct GradCfg {
 template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_grad(Problem p) {
   using Cf = GradCfg<T, NT>;
   using F = Fr<T>;
-  constexpr int ND = Cf::ND, LDN = Cf::TileN::LD, LDP = Cf::TileP::LD, LDU = Cf::TileU::LD, LDS_ = Cf::TileS::LD, LDMT = Cf::TileM::LD;
+  constexpr int LDN = Cf::TileN::LD, LDP = Cf::TileP::LD, LDU = Cf::TileU::LD, LDS_ = Cf::TileS::LD, LDMT = Cf::TileM::LD;
   constexpr int PSL = Cf::PSL;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   T* kt = reinterpret_cast<T*>(smem);
@@ -523,7 +535,7 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
   if (ch.len == 0) return;
   const int tid = static_cast<int>(threadIdx.x), l = tid & 63, g = l >> 4, c = l & 15, w = ssd::wave_id_s();
   const int rt = w & 3, half = w >> 2, row = 16 * rt + c;
-  const int64_t hp = static_cast<int64_t>(p.H) * p.P, rows = p.rows;
+  const int64_t hp = static_cast<int64_t>(p.H) * p.P;
   {
     typename Cf::TileN tk, tq;
     tk.load(static_cast<const T*>(p.k) + row_offset(ch.row, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N, p.k_sl, ch.len, p.N, tid);
@@ -543,16 +555,19 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
     for (int t = 0; t < NT; ++t) x1[t] = x2[t] = x3[t] = zero4();
     m1[0] = m1[1] = m2[0] = m2[1] = zero4();
     for (int p0 = 0; p0 < p.P; p0 += PSL) {
-      const int pcols = min(PSL, p.P - p0), prows = min(PSL, static_cast<int>(rows) - p0);
+      const int pcols = min(PSL, p.P - p0);
       typename Cf::TileP td, tv;
       typename Cf::TileU tu;
       typename Cf::TileS ts, tds;
       const int64_t at = static_cast<int64_t>(ch.row) * hp + static_cast<int64_t>(h) * p.P + p0;
       td.load(static_cast<const T*>(p.dout) + at, hp, ch.len, pcols, tid);
       tv.load(static_cast<const T*>(p.dv) + at, hp, ch.len, pcols, tid);
-      tu.load(static_cast<const T*>(p.u) + (sh * rows + p0) * CH, CH, prows, CH, tid);
-      ts.load(reinterpret_cast<const T*>(static_cast<const char*>(p.s) + sh * rows * ND * 4) + static_cast<int64_t>(p0) * ND, ND, prows, ND, tid);
-      tds.load(static_cast<const T*>(p.ds) + (sh * rows + p0) * ND, ND, prows, ND, tid);
+      const int64_t first = sh * p.nsl + p0 / SLICE;
+      const int nslices = min(PSL / SLICE, p.nsl - p0 / SLICE);
+      constexpr int HALVES = sizeof(T) / 2;
+      tu.load(p.u + first * HALVES * 2 * 64, HALVES * 2 * 64, nslices, tid);
+      ts.load(p.s + first * 2 * NT * 64, 2 * NT * 64, nslices, tid);   // bf16: the first terms
+      tds.load(p.ds + first * HALVES * NT * 64, HALVES * NT * 64, nslices, tid);
       const float tg = tid < GATES * CH ? p.gates[sh * (GATES * CH) + tid] : 0.f;
       __syncthreads();   // the previous head's last products are done
       td.store(dot, tid);

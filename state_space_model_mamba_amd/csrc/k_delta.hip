@@ -150,14 +150,17 @@ template <int NM> __device__ __forceinline__ void invert_rest(float* m) {
     block_store(blk(q + 1, q), -mma_left(blk(q + 1, q + 1), y, zero4()));
   }
   __syncthreads();
+  const int j = w & 1;
+  f32x4_t y[2];
   if (w < 2 * NM) {
-    const int j = w & 1;
-    f32x4_t y[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       y[i] = block_mma(blk(2 + i, 1), blk(1, j), zero4());   // T_01 is zero
       if (j == 0) y[i] = block_mma(blk(2 + i, 0), blk(0, 0), y[i]);
     }
+  }
+  __syncthreads();   // column 0 reads blocks (2, 1) and (3, 1), which column 1 overwrites
+  if (w < 2 * NM) {
     const f32x4_t t2 = mma_left(blk(2, 2), y[0], zero4());
     const f32x4_t t3 = mma_left(blk(3, 3), y[1], mma_left(blk(3, 2), y[0], zero4()));
     block_store(blk(2, j), -t2);

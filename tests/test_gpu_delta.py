@@ -199,6 +199,18 @@ def test_bitwise_repeatable_with_garbage_workspace():
         assert all(torch.equal(a, b) for a, b in zip(first, bits))
 
 
+@pytest.mark.parametrize("H,P,G,N", [(128, 64, 8, 128), (64, 128, 64, 128), (160, 32, 4, 64)])
+def test_bits_on_repeat_of_many_chunks(H, P, G, N):
+    """Thousands of chunk and head blocks, each the same bits every time (waves of a block share LDS throughout)."""
+    d = cuda(make(1, 2048, H, P, G, N, "bf16", seed=20))
+    first = None
+    for _ in range(6):
+        r, g = delta.delta_fwd(*args(d), want_final_states=True), delta.delta_bwd(*args(d), d["do"])
+        out = [r["o"], r["final_states"]] + [g[k] for k in GRADS]
+        first = first or out
+        assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
 def test_rows_past_the_last_sequence_stay_as_they_were():
     d = cuda(make(1, 100, 2, 16, 1, 16, "f32", seed=13, lengths=[40, 60]))
     s = delta.make_shape(1, 100, 2, 16, 1, 16, 1, ssd.SSD_IO_F32)   # one sequence of the two

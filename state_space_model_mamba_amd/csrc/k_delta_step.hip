@@ -90,27 +90,39 @@ template <typename T, int NV, int RG> __global__ __launch_bounds__(64 * STEP_WAV
     const T* qp = static_cast<const T*>(a.q) + b * a.q_sb + static_cast<int64_t>(grp) * a.N;
     const T* kp = static_cast<const T*>(a.k) + b * a.k_sb + static_cast<int64_t>(grp) * a.N;
     const T* vp = static_cast<const T*>(a.v) + b * a.v_sb + static_cast<int64_t>(h) * a.P;
-    for (int t = 0; t < a.T; ++t) {
-      const int64_t at = static_cast<int64_t>(b) * a.T + t;
+    // a token's operands are requested while the one before is worked on
+    struct Token {
       f32x4_t q[NV], k[NV];
-      float v[RG];
+      float v[RG], g, beta;
+    };
+    auto request = [&](int t) {
+      Token x;
+      const int64_t at = static_cast<int64_t>(b) * a.T + t;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int n = 4 * (l8 + 8 * j);
-        q[j] = k[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        x.q[j] = x.k[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         if (n < a.N) {
-          q[j] = ssd::load4f<T>(qp + t * a.q_sl + n);
-          k[j] = ssd::load4f<T>(kp + t * a.k_sl + n);
+          x.q[j] = ssd::load4f<T>(qp + t * a.q_sl + n);
+          x.k[j] = ssd::load4f<T>(kp + t * a.k_sl + n);
         }
       }
 #pragma unroll
-      for (int i = 0; i < RG; ++i) v[i] = row0 + 8 * i < a.P ? ssd::Elem<T>::to_f(vp[t * a.v_sl + row0 + 8 * i]) : 0.f;
-      const float dec = expf(a.g[at * a.H + h]), beta = a.beta[at * a.H + h];
+      for (int i = 0; i < RG; ++i) x.v[i] = row0 + 8 * i < a.P ? ssd::Elem<T>::to_f(vp[t * a.v_sl + row0 + 8 * i]) : 0.f;
+      x.g = a.g[at * a.H + h];
+      x.beta = a.beta[at * a.H + h];
+      return x;
+    };
+    Token x = request(0);
+    for (int t = 0; t < a.T; ++t) {
+      const int64_t at = static_cast<int64_t>(b) * a.T + t;
+      const Token y = request(t + 1 < a.T ? t + 1 : t);
+      const float dec = expf(x.g);
       float kq = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) kq += k[j][r] * q[j][r];
+        for (int r = 0; r < 4; ++r) kq += x.k[j][r] * x.q[j][r];
       }
       kq = sum8(kq);
 #pragma unroll
@@ -121,18 +133,19 @@ template <typename T, int NV, int RG> __global__ __launch_bounds__(64 * STEP_WAV
           S[i][j] *= dec;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            sk += S[i][j][r] * k[j][r];
-            sq += S[i][j][r] * q[j][r];
+            sk += S[i][j][r] * x.k[j][r];
+            sq += S[i][j][r] * x.q[j][r];
           }
         }
         sk = sum8(sk);
         sq = sum8(sq);
-        const float u = beta * (v[i] - sk);
+        const float u = x.beta * (x.v[i] - sk);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) S[i][j] += u * k[j];
+        for (int j = 0; j < NV; ++j) S[i][j] += u * x.k[j];
         const int p = row0 + 8 * i;
         if (l8 == 0 && p < a.P) static_cast<T*>(a.o)[(at * a.H + h) * a.P + p] = ssd::Elem<T>::from_f(a.scale * (sq + u * kq));
       }
+      x = y;
     }
     if (next >= a.B) break;
     b = next;
@@ -158,8 +171,12 @@ template <typename T, int NV, int RG> int go(StepArgs a, hipStream_t s) {
   hipLaunchKernelGGL((k_delta_step<T, NV, RG>), dim3(a.H * a.nblk, a.B), dim3(64 * STEP_WAVES), 0, s, a);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
+// Two rows a lane where that still gives every CU eight waves, else one (one sequence of 128 heads of 64 x 128: STEP1;
+// 64 of them: STEP2).
 template <typename T> int by_size(const StepArgs& a, hipStream_t s) {
-  return a.N <= 32 ? go<T, 1, 2>(a, s) : a.N <= 64 ? go<T, 2, 2>(a, s) : go<T, 4, 2>(a, s);
+  if (static_cast<int64_t>(a.B) * a.H * ((a.P + 15) / 16) >= 8 * 256)
+    return a.N <= 32 ? go<T, 1, 2>(a, s) : a.N <= 64 ? go<T, 2, 2>(a, s) : go<T, 4, 2>(a, s);
+  return a.N <= 32 ? go<T, 1, 1>(a, s) : a.N <= 64 ? go<T, 2, 1>(a, s) : go<T, 4, 1>(a, s);
 }
 }  // namespace
 

@@ -33,6 +33,7 @@ struct Args {
   float* slots;       // (blocks, 2, N) partial weight gradients
   int64_t q_sb, q_sl, k_sb, k_sl;
   int tokens, L, Gq, Gk, N, half, interleaved, l2, tt;
+  uint32_t magic;     // row / (Gq + Gk) = mulhi(row, magic) for the rows of tt > 1 positions of several heads
   float eps;
 };
 
@@ -104,7 +105,8 @@ __device__ __forceinline__ void rotate(float (&f)[V], int n, int half, const flo
 template <typename T, int LPR, int PAIR, bool BWD> __global__ __launch_bounds__(THR) void k_qk_norm(Args a) {
   constexpr int V = Vec<T>::V, ROWS = THR / LPR;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  float2* table = reinterpret_cast<float2*>(smem);   // [tt][half]
+  int64_t* place = reinterpret_cast<int64_t*>(smem);                // [tt][2]: where a position's q and k rows begin
+  float2* table = reinterpret_cast<float2*>(place + 2 * a.tt);      // [tt][half]: cosines and sines
   const int tid = static_cast<int>(threadIdx.x), rl = tid / LPR, n = (tid % LPR) * V;
   const int heads = a.Gq + a.Gk;
   const bool live = n < a.N;
@@ -118,28 +120,31 @@ template <typename T, int LPR, int PAIR, bool BWD> __global__ __launch_bounds__(
   const float inv_m = a.l2 ? 1.f : 1.f / static_cast<float>(a.N);
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tt; t0 < a.tokens; t0 += static_cast<int64_t>(gridDim.x) * a.tt) {
     const int nt = static_cast<int>(a.tokens - t0 < a.tt ? a.tokens - t0 : a.tt);
-    if (a.half) {
-      __syncthreads();
-      for (int i = tid; i < nt * a.half; i += THR) {
-        const int64_t t = t0 + i / a.half;
-        const double at = a.pos ? static_cast<double>(a.pos[t]) : static_cast<double>(t % a.L);
-        const double turns = at * static_cast<double>(a.inv_freq[i % a.half]) * 0.15915494309189533577;   // 1 / (2 pi)
-        const float part = static_cast<float>(2.0 * (turns - rint(turns)));
-        table[i] = float2{cospif(part), sinpif(part)};
-      }
-      __syncthreads();
+    __syncthreads();
+    for (int i = tid; i < nt; i += THR) {
+      const int t = static_cast<int>(t0) + i, bt = t / a.L;
+      place[2 * i] = bt * a.q_sb + static_cast<int64_t>(t - bt * a.L) * a.q_sl;
+      place[2 * i + 1] = bt * a.k_sb + static_cast<int64_t>(t - bt * a.L) * a.k_sl;
     }
+    for (int i = tid; i < nt * a.half; i += THR) {
+      const int t = static_cast<int>(t0) + i / a.half;
+      const double at = a.pos ? static_cast<double>(a.pos[t]) : static_cast<double>(t % a.L);
+      const double turns = at * static_cast<double>(a.inv_freq[i % a.half]) * 0.15915494309189533577;   // 1 / (2 pi)
+      const float part = static_cast<float>(2.0 * (turns - rint(turns)));
+      table[i] = float2{cospif(part), sinpif(part)};
+    }
+    __syncthreads();
     const int nrows = nt * heads;
     // every lane runs every turn: lanes past the last row take part in the exchanges with zeros
     for (int r0 = 0; r0 < nrows; r0 += ROWS) {
       const int row = r0 + rl;
       const bool ok = live && row < nrows;
-      const int tl = row < nrows ? row / heads : 0, hd = row < nrows ? row - tl * heads : 0;
+      const int tl = row >= nrows || a.tt == 1 ? 0 : heads == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), a.magic));
+      const int hd = row < nrows ? row - tl * heads : 0;
       const bool isq = hd < a.Gq;
       const int hl = isq ? hd : hd - a.Gq, nh = isq ? a.Gq : a.Gk;
-      const int64_t t = t0 + tl, bt = t / a.L;
-      const T* x = static_cast<const T*>(isq ? a.q : a.k) + bt * (isq ? a.q_sb : a.k_sb) + (t - bt * a.L) * (isq ? a.q_sl : a.k_sl) +
-                   static_cast<int64_t>(hl) * a.N;
+      const int64_t t = t0 + tl;
+      const T* x = static_cast<const T*>(isq ? a.q : a.k) + place[2 * tl + (isq ? 0 : 1)] + static_cast<int64_t>(hl) * a.N;
       const int64_t packed = (t * nh + hl) * static_cast<int64_t>(a.N);
       const float2* cs = table + tl * a.half;
       const float* w = isq ? a.wq : a.wk;
@@ -198,18 +203,22 @@ template <typename T, int LPR, int PAIR, bool BWD> __global__ __launch_bounds__(
   }
 }
 
-// The slots' sum, a column per 16 threads: each adds every 16th slot in order, then the 16 in order.
-__global__ __launch_bounds__(THR) void k_qk_norm_reduce(const float* slots, int nslots, int N, float* dwq, float* dwk) {
-  __shared__ double part[16][17];
-  const int lc = static_cast<int>(threadIdx.x) & 15, lr = static_cast<int>(threadIdx.x) >> 4;
-  const int col = static_cast<int>(blockIdx.x) * 16 + lc;
+// The slots' sum, a column per 64 threads: each adds every 64th slot in order, then the 64 in order.
+constexpr int RED_COLS = 16, RED_ROWS = 64;
+__global__ __launch_bounds__(RED_COLS * RED_ROWS) void k_qk_norm_reduce(const float* slots, int nslots, int N, float* dwq, float* dwk) {
+  __shared__ double part[RED_ROWS][RED_COLS + 1];
+  const int lc = static_cast<int>(threadIdx.x) % RED_COLS, lr = static_cast<int>(threadIdx.x) / RED_COLS;
+  const int col = static_cast<int>(blockIdx.x) * RED_COLS + lc;
   double s = 0.0;
-  if (col < 2 * N)
-    for (int i = lr; i < nslots; i += 16) s += static_cast<double>(slots[static_cast<int64_t>(i) * 2 * N + col]);
+  if (col < 2 * N) {
+#pragma unroll 8
+    for (int i = lr; i < nslots; i += RED_ROWS) s += static_cast<double>(slots[static_cast<int64_t>(i) * 2 * N + col]);
+  }
   part[lr][lc] = s;
   __syncthreads();
   if (lr == 0 && col < 2 * N) {
-    for (int i = 1; i < 16; ++i) s += part[i][lc];
+#pragma unroll 16
+    for (int i = 1; i < RED_ROWS; ++i) s += part[i][lc];
     if (col < N) {
       if (dwq) dwq[col] = static_cast<float>(s);
     } else if (dwk) {
@@ -249,7 +258,7 @@ int positions_per_block(const qk_norm_shape& s) {
   const int64_t tokens = s.batch * s.seqlen, heads = s.qheads + s.kheads, places = THR / lanes_per_row(s);
   int64_t tt = (places + heads - 1) / heads;
   if (tt > tokens) tt = tokens;
-  while (tt < 4 && tokens / (2 * tt) >= 2048) tt *= 2;
+  while (heads <= THR && tt < 4 && tokens / (2 * tt) >= 2048) tt *= 2;
   return static_cast<int>(tt < 1 ? 1 : tt);
 }
 
@@ -259,7 +268,7 @@ int64_t blocks(const qk_norm_shape& s, bool bwd) {
 }
 
 template <typename T, int LPR, int PAIR, bool BWD> int go(const Args& a, int64_t grid, hipStream_t st) {
-  size_t lds = sizeof(float2) * static_cast<size_t>(a.tt) * a.half;
+  size_t lds = (sizeof(float2) * a.half + 2 * sizeof(int64_t)) * static_cast<size_t>(a.tt);
   constexpr size_t red = sizeof(float) * (THR / LPR) * 2 * LPR * Vec<T>::V;   // at most 16 KB
   if (BWD && lds < red) lds = red;
   if (lds > 65536) return SSD_ERR_UNSUPPORTED_SHAPE;   // tt <= 256 places, half <= 128 where a place is 64 lanes
@@ -301,7 +310,9 @@ Args args(const qk_norm_shape& s, const void* q, const void* k, const float* wq,
   a.half = s.rot_dim / 2;
   a.interleaved = s.interleaved;
   a.l2 = s.norm == QK_NORM_L2;
-  a.tt = positions_per_block(s);
+  a.tt = positions_per_block(s);   // tt > 1: fewer than 4 * 256 rows, for which the rounded up reciprocal of 2 .. 256 heads is exact (that of 1 does
+  // not fit 32 bits)
+  a.magic = a.Gq + a.Gk > 1 ? static_cast<uint32_t>((uint64_t{1} << 32) / static_cast<uint64_t>(a.Gq + a.Gk) + 1) : 0;
   a.eps = s.eps;
   return a;
 }
@@ -356,7 +367,8 @@ int qk_norm_bwd(const qk_norm_shape* shape, const void* q, const void* k, const 
   const int r = shape->io_dtype == SSD_IO_BF16 ? qkn::by_lanes<ssd::bf16_t, true>(*shape, a, grid, st)
                                                : qkn::by_lanes<float, true>(*shape, a, grid, st);
   if (r != SSD_OK || (!dq_weight && !dk_weight)) return r;
-  hipLaunchKernelGGL(qkn::k_qk_norm_reduce, dim3(static_cast<unsigned>((2 * shape->dstate + 15) / 16)), dim3(qkn::THR), 0, st,
+  hipLaunchKernelGGL(qkn::k_qk_norm_reduce, dim3(static_cast<unsigned>((2 * shape->dstate + qkn::RED_COLS - 1) / qkn::RED_COLS)),
+                     dim3(qkn::RED_COLS * qkn::RED_ROWS), 0, st,
                      a.slots, static_cast<int>(grid), a.N, dq_weight, dk_weight);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }

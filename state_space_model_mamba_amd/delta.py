@@ -13,6 +13,7 @@ states kept in memory (the states that ``delta_fwd`` returns have its layout).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -60,6 +61,7 @@ def make_shape(batch, seqlen, nheads, headdim, ngroups, dstate, nseqs, io_dtype=
 
 
 def workspace_size(shape: DeltaShape, backward: bool = False) -> int:
+    """Bytes of workspace delta_fwd, or with ``backward`` delta_bwd, needs."""
     n = ctypes.c_size_t(0)
     rc = load_library().delta_workspace_size(ctypes.byref(shape), int(bool(backward)), ctypes.byref(n))
     if rc:
@@ -67,8 +69,16 @@ def workspace_size(shape: DeltaShape, backward: bool = False) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=256)
+def _sized(batch, seqlen, nheads, headdim, ngroups, dstate, nseqs, io_dtype, scale, strides) -> DeltaShape:
+    """make_shape, kept per sizes (callers read it only)."""
+    return make_shape(batch, seqlen, nheads, headdim, ngroups, dstate, nseqs, io_dtype, scale, strides)
+
+
 def row_strides(t, name):
     """(batch, row) strides of a (batch, rows, heads, width) tensor whose last two axes are contiguous."""
+    if t.is_contiguous():
+        return 0, 0
     b, L, n, w = t.shape
     sb, sl, sn, sw = t.stride()
     if (sw != 1 and w > 1) or (sn != w and n > 1):
@@ -87,9 +97,13 @@ def _check_strided(t, name, dtype, shape, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return row_strides(t, name)
+
+
+def _stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class _on:
@@ -123,7 +137,7 @@ def _inputs(what, q, k, v, g, beta, nseqs, scale) -> DeltaShape:
                *_check_strided(v, "v", io, (b, L, H, P), dev))
     ssd._check(g, "g", torch.float32, (b, L, H), dev)
     ssd._check(beta, "beta", torch.float32, (b, L, H), dev)
-    return make_shape(b, L, H, P, G, N, nseqs, ssd.SSD_IO_BF16 if io == torch.bfloat16 else ssd.SSD_IO_F32, scale, strides)
+    return _sized(b, L, H, P, G, N, nseqs, ssd.SSD_IO_BF16 if io == torch.bfloat16 else ssd.SSD_IO_F32, scale, strides)
 
 
 def _nseqs(q, initial_states, seq_idx, nseqs) -> int:
@@ -173,7 +187,7 @@ def delta_fwd(q, k, v, g, beta, initial_states=None, seq_idx=None, scale: Option
         rc = lib.delta_fwd(ctypes.byref(shape), ssd._ptr(q), ssd._ptr(k), ssd._ptr(v), ssd._ptr(g), ssd._ptr(beta),
                            ssd._ptr(initial_states), ssd._ptr(seq_idx), ssd._ptr(o), ssd._ptr(final),
                            ssd._ptr(workspace), workspace.numel() * workspace.element_size(),
-                           torch.cuda.current_stream(dev).cuda_stream)
+                           _stream(dev))
     if rc:
         raise ssd.SsdError(rc, "delta_fwd")
     return {"o": o, "final_states": final, "workspace": workspace, "shape": shape}
@@ -209,7 +223,7 @@ def delta_bwd(q, k, v, g, beta, do, initial_states=None, seq_idx=None, d_final_s
                            ssd._ptr(initial_states), ssd._ptr(seq_idx), ssd._ptr(do), ssd._ptr(d_final_states),
                            ssd._ptr(out["dq"]), ssd._ptr(out["dk"]), ssd._ptr(out["dv"]), ssd._ptr(out["dg"]),
                            ssd._ptr(out["dbeta"]), ssd._ptr(out["d_initial_states"]), ssd._ptr(workspace),
-                           workspace.numel() * workspace.element_size(), torch.cuda.current_stream(dev).cuda_stream)
+                           workspace.numel() * workspace.element_size(), _stream(dev))
     if rc:
         raise ssd.SsdError(rc, "delta_bwd")
     out["workspace"] = workspace
@@ -280,7 +294,7 @@ def delta_step(q, k, v, g, beta, states, state_indices=None, scale: Optional[flo
         rc = lib.delta_step(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                             beta.data_ptr(), states.data_ptr(), states.shape[0],
                             None if state_indices is None else state_indices.data_ptr(), out.data_ptr(),
-                            torch.cuda.current_stream(dev).cuda_stream)
+                            _stream(dev))
     if rc:
         raise ssd.SsdError(rc, "delta_step")
     return out

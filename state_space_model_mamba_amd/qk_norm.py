@@ -13,7 +13,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from state_space_model_mamba_amd import ssd
-from state_space_model_mamba_amd.delta import _check_strided, _on
+from state_space_model_mamba_amd.delta import _check_strided, _on, _stream
 
 QK_NORM_RMS, QK_NORM_L2 = 0, 1
 NORMS = {"rms": QK_NORM_RMS, "l2": QK_NORM_L2}
@@ -108,7 +108,7 @@ def qk_norm_rope_fwd(q, k=None, q_weight=None, k_weight=None, positions=None, in
     with _on(dev):
         rc = lib.qk_norm_fwd(ctypes.byref(shape), ssd._ptr(q), ssd._ptr(k), ssd._ptr(q_weight), ssd._ptr(k_weight),
                              ssd._ptr(positions), ssd._ptr(inv_freq), ssd._ptr(q_out), ssd._ptr(k_out),
-                             torch.cuda.current_stream(dev).cuda_stream)
+                             _stream(dev))
     if rc:
         raise ssd.SsdError(rc, "qk_norm_fwd")
     return q_out, k_out
@@ -139,7 +139,7 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_o
                              ssd._ptr(positions), ssd._ptr(inv_freq), ssd._ptr(dq_out), ssd._ptr(dk_out),
                              ssd._ptr(out["dq"]), ssd._ptr(out["dk"]), ssd._ptr(out["dq_weight"]),
                              ssd._ptr(out["dk_weight"]), ssd._ptr(workspace),
-                             workspace.numel() * workspace.element_size(), torch.cuda.current_stream(dev).cuda_stream)
+                             workspace.numel() * workspace.element_size(), _stream(dev))
     if rc:
         raise ssd.SsdError(rc, "qk_norm_bwd")
     return out

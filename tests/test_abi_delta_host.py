@@ -158,6 +158,7 @@ def test_bindings_refuse_the_cpu_and_bad_arguments():
 def test_row_strides_of_slices():
     x = torch.zeros(3, 7, 4 * 16 + 2 * 8)
     s = x[..., 64:].unflatten(-1, (2, 8))
+    assert delta.row_strides(x.unflatten(-1, (10, 8)), "x") == (0, 0)   # contiguous
     assert delta.row_strides(s, "s") == (7 * 80, 80)
     assert delta.row_strides(s[:1], "s") == (7 * 80, 80)
     assert delta.row_strides(s[:, :1], "s") == (7 * 80, 16)

@@ -72,7 +72,8 @@ def check(d, label, **kw):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("b,L,Gq,Gk,N,rot", [
     (1, 1, 1, 1, 8, 8), (2, 3, 3, 1, 16, 0), (1, 5, 4, 2, 40, 20), (2, 7, 8, 8, 64, 32), (1, 33, 5, 3, 96, 96), (3, 50, 2, 2, 128, 128),
-    (1, 9, 1, 0, 256, 128), (1, 20, 6, 6, 200, 6)])
+    (1, 9, 1, 0, 256, 128), (1, 20, 6, 6, 200, 6), (2, 37, 1, 0, 16, 8),
+    (1, 11, 1, 1, 8, 8)])
 def test_shapes(b, L, Gq, Gk, N, rot, interleaved, io):
     check(make(b, L, Gq, Gk, N, rot, io, seed=N + rot, far=5000), f"{io} b={b} L={L} {Gq}+{Gk}x{N} rot={rot}",
           interleaved=interleaved, norm="l2" if L % 2 else "rms")

@@ -23,6 +23,7 @@ using ssd::bf16_t;
 
 constexpr int THR = 256;
 constexpr int MAXN = 256;
+constexpr int UNROLL = 2;         // rows of a lane in flight
 constexpr int MAX_SLOTS = 1024;   // blocks of the backward, and its workspace slots
 
 struct Args {
@@ -33,6 +34,7 @@ struct Args {
   float* slots;       // (blocks, 2, N) partial weight gradients
   int64_t q_sb, q_sl, k_sb, k_sl;
   int tokens, L, Gq, Gk, N, half, interleaved, l2, tt;
+  int flat;           // batch rows follow each other at the row stride
   uint32_t magic;     // row / (Gq + Gk) = mulhi(row, magic) for the rows of tt > 1 positions of several heads
   float eps;
 };
@@ -103,10 +105,9 @@ __device__ __forceinline__ void rotate(float (&f)[V], int n, int half, const flo
 
 // BWD: the gradients; else the forward.  Rows of a position: its q heads, then its k heads.
 template <typename T, int LPR, int PAIR, bool BWD> __global__ __launch_bounds__(THR) void k_qk_norm(Args a) {
-  constexpr int V = Vec<T>::V, ROWS = THR / LPR;
+  constexpr int V = Vec<T>::V, ROWS = THR / LPR, UN = PAIR == PAIR_ANY ? 1 : UNROLL;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  int64_t* place = reinterpret_cast<int64_t*>(smem);                // [tt][2]: where a position's q and k rows begin
-  float2* table = reinterpret_cast<float2*>(place + 2 * a.tt);      // [tt][half]: cosines and sines
+  float2* table = reinterpret_cast<float2*>(smem);   // [tt][half]: cosines and sines
   const int tid = static_cast<int>(threadIdx.x), rl = tid / LPR, n = (tid % LPR) * V;
   const int heads = a.Gq + a.Gk;
   const bool live = n < a.N;
@@ -120,67 +121,92 @@ template <typename T, int LPR, int PAIR, bool BWD> __global__ __launch_bounds__(
   const float inv_m = a.l2 ? 1.f : 1.f / static_cast<float>(a.N);
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tt; t0 < a.tokens; t0 += static_cast<int64_t>(gridDim.x) * a.tt) {
     const int nt = static_cast<int>(a.tokens - t0 < a.tt ? a.tokens - t0 : a.tt);
-    __syncthreads();
-    for (int i = tid; i < nt; i += THR) {
-      const int t = static_cast<int>(t0) + i, bt = t / a.L;
-      place[2 * i] = bt * a.q_sb + static_cast<int64_t>(t - bt * a.L) * a.q_sl;
-      place[2 * i + 1] = bt * a.k_sb + static_cast<int64_t>(t - bt * a.L) * a.k_sl;
-    }
-    for (int i = tid; i < nt * a.half; i += THR) {
-      const int t = static_cast<int>(t0) + i / a.half;
-      const double at = a.pos ? static_cast<double>(a.pos[t]) : static_cast<double>(t % a.L);
-      const double turns = at * static_cast<double>(a.inv_freq[i % a.half]) * 0.15915494309189533577;   // 1 / (2 pi)
-      const float part = static_cast<float>(2.0 * (turns - rint(turns)));
-      table[i] = float2{cospif(part), sinpif(part)};
-    }
-    __syncthreads();
     const int nrows = nt * heads;
-    // every lane runs every turn: lanes past the last row take part in the exchanges with zeros
-    for (int r0 = 0; r0 < nrows; r0 += ROWS) {
-      const int row = r0 + rl;
-      const bool ok = live && row < nrows;
-      const int tl = row >= nrows || a.tt == 1 ? 0 : heads == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), a.magic));
-      const int hd = row < nrows ? row - tl * heads : 0;
-      const bool isq = hd < a.Gq;
-      const int hl = isq ? hd : hd - a.Gq, nh = isq ? a.Gq : a.Gk;
-      const int64_t t = t0 + tl;
-      const T* x = static_cast<const T*>(isq ? a.q : a.k) + place[2 * tl + (isq ? 0 : 1)] + static_cast<int64_t>(hl) * a.N;
-      const int64_t packed = (t * nh + hl) * static_cast<int64_t>(a.N);
-      const float2* cs = table + tl * a.half;
-      const float* w = isq ? a.wq : a.wk;
-      float f[V], y[V];
+    // Every lane runs every turn: lanes past the last row take part in the exchanges with zeros.  The rows of UN turns
+    // are requested before the angles are formed.
+    for (int r0 = 0; r0 < nrows; r0 += UN * ROWS) {
+      struct {
+        const T *x, *dy;
+        T* out;
+        int tl;
+        bool ok, isq;
+        uint4 xr, yr;
+      } rows[UN];
 #pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = y[e] = 0.f;
-      if (ok) Vec<T>::load(x + n, f);
-      const T* dy = BWD ? static_cast<const T*>(isq ? a.dyq : a.dyk) + packed : nullptr;
-      if (BWD && ok) Vec<T>::load(dy + n, y);
-      float ss = 0.f;
+      for (int u = 0; u < UN; ++u) {
+        const int row = r0 + u * ROWS + rl;
+        auto& w = rows[u];
+        w.ok = live && row < nrows;
+        w.tl = row >= nrows || a.tt == 1 ? 0 : heads == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), a.magic));
+        const int hd = row < nrows ? row - w.tl * heads : 0;
+        w.isq = hd < a.Gq;
+        const int hl = w.isq ? hd : hd - a.Gq, nh = w.isq ? a.Gq : a.Gk;
+        const int t = static_cast<int>(t0) + w.tl;
+        const int64_t sl = w.isq ? a.q_sl : a.k_sl;
+        int64_t at = t * sl;
+        if (!a.flat) {
+          const int bt = t / a.L;
+          at = bt * (w.isq ? a.q_sb : a.k_sb) + (t - bt * a.L) * sl;
+        }
+        const int64_t packed = (static_cast<int64_t>(t) * nh + hl) * static_cast<int64_t>(a.N);
+        w.x = static_cast<const T*>(w.isq ? a.q : a.k) + at + static_cast<int64_t>(hl) * a.N;
+        w.out = static_cast<T*>(w.isq ? a.oq : a.ok) + packed + n;
+        w.dy = BWD ? static_cast<const T*>(w.isq ? a.dyq : a.dyk) + packed : nullptr;
+        w.xr = w.yr = ssd::zero_u4();
+        if (w.ok) {
+          w.xr = ssd::ld_global16(w.x + n);
+          if (BWD) w.yr = ssd::ld_global16(w.dy + n);
+        }
+      }
+      if (r0 == 0 && a.half) {
+        __syncthreads();
+        for (int i = tid; i < nt * a.half; i += THR) {
+          const int t = static_cast<int>(t0) + i / a.half;
+          const double at = a.pos ? static_cast<double>(a.pos[t]) : static_cast<double>(t % a.L);
+          const double turns = at * static_cast<double>(a.inv_freq[i % a.half]) * 0.15915494309189533577;   // 1 / (2 pi)
+          const float part = static_cast<float>(2.0 * (turns - rint(turns)));
+          table[i] = float2{cospif(part), sinpif(part)};
+        }
+        __syncthreads();
+      }
 #pragma unroll
-      for (int e = 0; e < V; ++e) ss += f[e] * f[e];
-      const float r = 1.f / sqrtf(row_sum<LPR>(ss) * inv_m + a.eps);
-      T* out = static_cast<T*>(isq ? a.oq : a.ok) + packed + n;
-      if constexpr (!BWD) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) y[e] = f[e] * r * (isq ? wq[e] : wk[e]);
-        rotate<V, PAIR, LPR>(y, n, a.half, cs, 1.f, [&](int i) {
-          return ok ? ssd::Elem<T>::to_f(x[i]) * r * (w ? w[i] : 1.f) : 0.f; });
-        if (ok) Vec<T>::store(out, y);
-      } else {
-        rotate<V, PAIR, LPR>(y, n, a.half, cs, -1.f, [&](int i) { return ok ? ssd::Elem<T>::to_f(dy[i]) : 0.f; });
-        float dot = 0.f;
+      for (int u = 0; u < UN; ++u) {
+        const auto& row = rows[u];
+        const bool ok = row.ok, isq = row.isq;
+        const float2* cs = table + row.tl * a.half;
+        const float* w = isq ? a.wq : a.wk;
+        float f[V], y[V];
+        float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float gw = y[e] * f[e] * r;
-          if (ok) {
-            if (isq) gq[e] += gw; else gk[e] += gw;
-          }
-          y[e] *= isq ? wq[e] : wk[e];
-          dot += y[e] * f[e];
+          f[e] = ssd::vget<T>(row.xr, e);
+          y[e] = ssd::vget<T>(row.yr, e);
+          ss += f[e] * f[e];
         }
-        const float m = row_sum<LPR>(dot) * inv_m * r * r;
+        const float r = 1.f / sqrtf(row_sum<LPR>(ss) * inv_m + a.eps);
+        if constexpr (!BWD) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) y[e] = r * (y[e] - f[e] * m);
-        if (ok) Vec<T>::store(out, y);
+          for (int e = 0; e < V; ++e) y[e] = f[e] * r * (isq ? wq[e] : wk[e]);
+          rotate<V, PAIR, LPR>(y, n, a.half, cs, 1.f, [&](int i) {
+            return ok ? ssd::Elem<T>::to_f(row.x[i]) * r * (w ? w[i] : 1.f) : 0.f; });
+          if (ok) Vec<T>::store(row.out, y);
+        } else {
+          rotate<V, PAIR, LPR>(y, n, a.half, cs, -1.f, [&](int i) { return ok ? ssd::Elem<T>::to_f(row.dy[i]) : 0.f; });
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float gw = y[e] * f[e] * r;
+            if (ok) {
+              if (isq) gq[e] += gw; else gk[e] += gw;
+            }
+            y[e] *= isq ? wq[e] : wk[e];
+            dot += y[e] * f[e];
+          }
+          const float m = row_sum<LPR>(dot) * inv_m * r * r;
+#pragma unroll
+          for (int e = 0; e < V; ++e) y[e] = r * (y[e] - f[e] * m);
+          if (ok) Vec<T>::store(row.out, y);
+        }
       }
     }
   }
@@ -258,7 +284,7 @@ int positions_per_block(const qk_norm_shape& s) {
   const int64_t tokens = s.batch * s.seqlen, heads = s.qheads + s.kheads, places = THR / lanes_per_row(s);
   int64_t tt = (places + heads - 1) / heads;
   if (tt > tokens) tt = tokens;
-  while (heads <= THR && tt < 4 && tokens / (2 * tt) >= 2048) tt *= 2;
+  while (heads <= THR && tt < 8 && tokens / (2 * tt) >= 1024) tt *= 2;
   return static_cast<int>(tt < 1 ? 1 : tt);
 }
 
@@ -268,7 +294,7 @@ int64_t blocks(const qk_norm_shape& s, bool bwd) {
 }
 
 template <typename T, int LPR, int PAIR, bool BWD> int go(const Args& a, int64_t grid, hipStream_t st) {
-  size_t lds = (sizeof(float2) * a.half + 2 * sizeof(int64_t)) * static_cast<size_t>(a.tt);
+  size_t lds = sizeof(float2) * a.half * static_cast<size_t>(a.tt);
   constexpr size_t red = sizeof(float) * (THR / LPR) * 2 * LPR * Vec<T>::V;   // at most 16 KB
   if (BWD && lds < red) lds = red;
   if (lds > 65536) return SSD_ERR_UNSUPPORTED_SHAPE;   // tt <= 256 places, half <= 128 where a place is 64 lanes
@@ -303,6 +329,7 @@ Args args(const qk_norm_shape& s, const void* q, const void* k, const float* wq,
   a.k_sl = kc ? s.kheads * s.dstate : s.k_row_stride;
   a.k_sb = kc ? s.seqlen * a.k_sl : s.k_batch_stride;
   a.tokens = static_cast<int>(s.batch * s.seqlen);
+  a.flat = a.q_sb == s.seqlen * a.q_sl && (s.kheads == 0 || a.k_sb == s.seqlen * a.k_sl);
   a.L = static_cast<int>(s.seqlen);
   a.Gq = static_cast<int>(s.qheads);
   a.Gk = static_cast<int>(s.kheads);
@@ -310,7 +337,7 @@ Args args(const qk_norm_shape& s, const void* q, const void* k, const float* wq,
   a.half = s.rot_dim / 2;
   a.interleaved = s.interleaved;
   a.l2 = s.norm == QK_NORM_L2;
-  a.tt = positions_per_block(s);   // tt > 1: fewer than 4 * 256 rows, for which the rounded up reciprocal of 2 .. 256 heads is exact (that of 1 does
+  a.tt = positions_per_block(s);   // tt > 1: fewer than 8 * 256 rows, for which the rounded up reciprocal of 2 .. 256 heads is exact (that of 1 does
   // not fit 32 bits)
   a.magic = a.Gq + a.Gk > 1 ? static_cast<uint32_t>((uint64_t{1} << 32) / static_cast<uint64_t>(a.Gq + a.Gk) + 1) : 0;
   a.eps = s.eps;

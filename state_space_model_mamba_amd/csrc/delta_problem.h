@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "ssd_device.h"
+
 namespace delta {
 
 constexpr int SLICE = 16;   // value columns of a state wave
@@ -64,6 +66,18 @@ __device__ __forceinline__ int slot_base(int start, int s) { return (start >> 6)
 struct Chunk {
   int seq, row, len;   // sequence, first row (flat), rows of the chunk (0: the slot holds none)
 };
+// Sequence, head and value column block of a walk's block.  Consecutive ones run on the same XCD, whose L2 then serves
+// a head's chunk matrices to its column blocks and a group's q and k to its heads.
+struct Place {
+  int seq, h, ps;
+};
+__device__ __forceinline__ Place place_of(int np) {
+  const int64_t across = gridDim.x;
+  const int64_t id = ssd::xcd_logical_block(static_cast<int64_t>(blockIdx.y) * across + blockIdx.x, across * gridDim.y);
+  const int x = static_cast<int>(id % across);
+  return Place{static_cast<int>(id / across), x / np, x % np};
+}
+
 // which chunk a slot holds
 __device__ __forceinline__ Chunk chunk_of(const Problem& p, int slot) {
   int lo = 0, hi = p.nseqs;   // the last sequence whose slots begin at or before this one

@@ -407,8 +407,8 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
   auto xe = [&](int i) { return reinterpret_cast<f32x4_t*>(smem + Cf::OFF_XE) + (i & XB) * 64 * NSW * 4; };
 
   const int np = (p.P + PS - 1) / PS;
-  const int h = static_cast<int>(blockIdx.x) / np, ps = static_cast<int>(blockIdx.x) % np;
-  const int seq = static_cast<int>(blockIdx.y), grp = h / p.hpg;
+  const Place at_block = place_of(np);
+  const int h = at_block.h, ps = at_block.ps, seq = at_block.seq, grp = h / p.hpg;
   const int s0 = seq_start(p, seq), s1 = seq_start(p, seq + 1);
   const int nchunk = (s1 - s0 + CH - 1) / CH, slot0 = slot_base(s0, seq);
   const int tid = static_cast<int>(threadIdx.x), l = tid & 63, g = l >> 4, c = l & 15, w = ssd::wave_id_s();

@@ -36,10 +36,10 @@ namespace delta {
 //     part of du, and q^T dout,
 //   * a wave each follows behind with what Du gives, for chunk i + 1: dv, the
 //     row sums for the gates' gradients, and the stores,
-//   * one wave stages the coming chunks' rows in LDS.
+//   * two waves stage the coming chunks' rows in LDS.
 // ---------------------------------------------------------------------------
 template <typename T, int NT> struct RwalkCfg {
-  static constexpr int ND = 32 * NT, NSW = 2, PS = SLICE * NSW, HT = 64, THREADS = 64 * (2 * NSW + 2);
+  static constexpr int ND = 32 * NT, NSW = 2, PS = SLICE * NSW, NST = 2, HT = 64 * NST, THREADS = 64 * (2 * NSW + 1 + NST);
   using TileN = Tile<T, CH, ND, HT>;
   using TileP = Tile<T, CH, PS, HT>;
   static constexpr size_t N_BYTES = sizeof(T) * TileN::LDS_ELEMS, P_BYTES = sizeof(T) * TileP::LDS_ELEMS;
@@ -56,7 +56,7 @@ template <typename T, int NT> struct RwalkCfg {
   static constexpr size_t LDS = OFF_G + 4 * sizeof(float) * RWALK_GATES * CH;   // the gates of four chunks
 };
 
-template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_delta_rwalk(Problem p) {
+template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_delta_rwalk(Problem p) {
   using Cf = RwalkCfg<T, NT>;
   using F = Fr<T>;
   using TileN = typename Cf::TileN;
@@ -74,8 +74,8 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__
   uint4* xs = reinterpret_cast<uint4*>(smem + Cf::OFF_XS);        // [wave][q][term][lane]
 
   const int np = (p.P + PS - 1) / PS;
-  const int h = static_cast<int>(blockIdx.x) / np, ps = static_cast<int>(blockIdx.x) % np;
-  const int seq = static_cast<int>(blockIdx.y), grp = h / p.hpg;
+  const Place at_block = place_of(np);
+  const int h = at_block.h, ps = at_block.ps, seq = at_block.seq, grp = h / p.hpg;
   const int s0 = seq_start(p, seq), s1 = seq_start(p, seq + 1);
   const int nchunk = (s1 - s0 + CH - 1) / CH, slot0 = slot_base(s0, seq), last = nchunk - 1;
   const int tid = static_cast<int>(threadIdx.x), l = tid & 63, g = l >> 4, c = l & 15, w = ssd::wave_id_s();
@@ -424,33 +424,36 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__
     return;
   }
 
-  // ---- the staging wave
+  // ---- the staging waves
+  const int ht = tid - 64 * (2 * NSW + 1);
+  constexpr int GI = (RWALK_GATES * CH + Cf::HT - 1) / Cf::HT;
   const int pcols = min(PS, p.P - PS * ps);
   const T* kp = static_cast<const T*>(p.k) + row_offset(s0, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N;
   const T* qp = static_cast<const T*>(p.q) + row_offset(s0, p.L, p.q_sb, p.q_sl) + static_cast<int64_t>(grp) * p.N;
   const T* vp = static_cast<const T*>(p.v) + row_offset(s0, p.L, p.v_sb, p.v_sl) + static_cast<int64_t>(h) * p.P + PS * ps;
   TileN tk, tq;
   TileP td, tv;
-  float tg[RWALK_GATES];
-  auto request_k = [&](int i) { tk.load(kp + static_cast<int64_t>(CH) * i * p.k_sl, p.k_sl, length(i), p.N, l); };
-  auto request_v = [&](int i) { tv.load(vp + static_cast<int64_t>(CH) * i * p.v_sl, p.v_sl, length(i), pcols, l); };
+  float tg[GI];
+  auto request_k = [&](int i) { tk.load(kp + static_cast<int64_t>(CH) * i * p.k_sl, p.k_sl, length(i), p.N, ht); };
+  auto request_v = [&](int i) { tv.load(vp + static_cast<int64_t>(CH) * i * p.v_sl, p.v_sl, length(i), pcols, ht); };
   // for the wave ahead: q, dout and the gates
   auto request_q = [&](int i) {
     const int64_t row = static_cast<int64_t>(CH) * i;
-    tq.load(qp + row * p.q_sl, p.q_sl, length(i), p.N, l);
-    td.load(static_cast<const T*>(p.dout) + (s0 + row) * hp + static_cast<int64_t>(h) * p.P + PS * ps, hp, length(i), pcols, l);
+    tq.load(qp + row * p.q_sl, p.q_sl, length(i), p.N, ht);
+    td.load(static_cast<const T*>(p.dout) + (s0 + row) * hp + static_cast<int64_t>(h) * p.P + PS * ps, hp, length(i), pcols, ht);
 #pragma unroll
-    for (int k = 0; k < RWALK_GATES; ++k) tg[k] = p.gates[slot_head(i) * (GATES * CH) + k * CH + l];
+    for (int k = 0; k < GI; ++k) tg[k] = ht + k * Cf::HT < RWALK_GATES * CH ? p.gates[slot_head(i) * (GATES * CH) + ht + k * Cf::HT] : 0.f;
   };
   auto stage_q = [&](int i) {
-    tq.store(qbuf(i), l);
-    td.store(dobuf(i), l);
+    tq.store(qbuf(i), ht);
+    td.store(dobuf(i), ht);
 #pragma unroll
-    for (int k = 0; k < RWALK_GATES; ++k) gbuf(i)[k * CH + l] = tg[k];
+    for (int k = 0; k < GI; ++k)
+      if (ht + k * Cf::HT < RWALK_GATES * CH) gbuf(i)[ht + k * Cf::HT] = tg[k];
   };
   request_k(last);
   request_q(last);
-  tk.store(kbuf(last), l);
+  tk.store(kbuf(last), ht);
   stage_q(last);
   if (last > 0) request_q(last - 1);
   if (KB && last > 0) request_k(last - 1);
@@ -463,7 +466,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__
   __syncthreads();
   for (int i = last; i >= 0; --i) {
     if (!KB) {
-      if (i < last) tk.store(kbuf(i), l);
+      if (i < last) tk.store(kbuf(i), ht);
       if (i > 0) {
         stage_q(i - 1);
         request_k(i - 1);
@@ -472,14 +475,14 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 6) __attribute__
     }
     __syncthreads();
     if (KB) {
-      if (i > 0) tk.store(kbuf(i - 1), l);
+      if (i > 0) tk.store(kbuf(i - 1), ht);
       if (i > 1) {
         stage_q(i - 2);
         request_k(i - 2);
       }
       if (i > 2) request_q(i - 3);
     }
-    tv.store(vbuf(i), l);
+    tv.store(vbuf(i), ht);
     if (i > 0) request_v(i - 1);
     __syncthreads();
   }

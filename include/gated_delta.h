@@ -61,8 +61,8 @@ typedef struct {
   int64_t ngroups;  /* >= 1 */
   int64_t dstate;   /* N: multiple of 8 (bf16 io) or 4 (f32 io), <= 128 */
   int64_t nseqs;    /* number of sequence starts; == batch without seq_idx */
-  int64_t q_batch_stride, q_row_stride; /* elements, multiples of 8 (bf16) or 4 (f32); 0, 0: contiguous */
-  int64_t k_batch_stride, k_row_stride;
+  int64_t q_batch_stride, q_row_stride; /* elements, multiples of 8 (bf16) or 4 (f32); 0, 0: contiguous; */
+  int64_t k_batch_stride, k_row_stride; /* row strides, nheads * headdim and ngroups * dstate <= 2^26 */
   int64_t v_batch_stride, v_row_stride;
   float scale;
   int32_t io_dtype; /* SSD_IO_BF16 or SSD_IO_F32 */

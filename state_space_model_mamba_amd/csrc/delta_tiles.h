@@ -244,23 +244,28 @@ template <typename T, int SLICES, int NQ, int NTHR> struct SliceTile {
   }
 };
 
-// first column of tile t among columns in pair order, for load_tr<8>
-__device__ __forceinline__ constexpr int pair_col(int t) { return 32 * (t >> 1) + 4 * (t & 1); }
-
 // a pair of accumulator tiles as 8 values in fragment order
 __device__ __forceinline__ void pair8(f32x4_t a, f32x4_t b, float (&v)[8]) {
 #pragma unroll
   for (int r = 0; r < 4; ++r) { v[r] = a[r]; v[4 + r] = b[r]; }
 }
 
+// first column of tile t among columns in pair order, for load_tr<8>
+__device__ __forceinline__ constexpr int pair_col(int t) { return 32 * (t >> 1) + 4 * (t & 1); }
+
 // A ROWS x COLS tile of rows `stride` elements apart, held in registers between its loads and its store
 // to LDS by NTHR threads (tid: 0 .. NTHR - 1); rows >= nrows and columns >= ncols (a multiple of 16 bytes)
 // are zero and not read.  A thread's pieces share their column and lie STEP rows apart, so a whole tile
 // takes one vector offset and a uniform base per piece.
-template <typename T, int ROWS, int COLS, int NTHR> struct Tile {
+//
+// SWZ (256-byte rows of bf16): no padding, and row r's 16-byte piece p lies at place p ^ (4 (r % 4) + r / 8 % 4).  The walks
+// read such a tile by rows in pair order (16 rows at one piece) and by columns in pair order (4 rows at 4 pieces);
+// with any padding one of the two meets itself in the banks 2 to 4 times, so placed neither does.
+template <typename T, int ROWS, int COLS, int NTHR, bool SWZ = false> struct Tile {
   static constexpr int VEC = Vec16<T>::N, CV = COLS / VEC, STEP = NTHR / CV, IT = ROWS / STEP;
   static_assert(NTHR % CV == 0 && ROWS % STEP == 0, "tile");
-  static constexpr int LD = COLS + VEC;   // row pitch in LDS: 16 bytes of padding
+  static_assert(!SWZ || (CV == 16 && STEP % 4 == 0 && (STEP == 4 || STEP == 8)), "swizzled tile");
+  static constexpr int LD = SWZ ? COLS : COLS + VEC;   // row pitch in LDS: 16 bytes of padding
   static constexpr int LDS_ELEMS = ROWS * LD;
   f32x4_t buf[IT];
   // base: uniform; stride * ROWS elements span less than 2^31 bytes
@@ -281,9 +286,40 @@ template <typename T, int ROWS, int COLS, int NTHR> struct Tile {
     }
   }
   __device__ __forceinline__ void store(T* lds, int tid) const {
-    T* d = lds + (tid / CV) * LD + (tid % CV) * VEC;
+    if constexpr (SWZ) {
+      const int r = tid / CV, p = (tid % CV) ^ (4 * (r & 3));
 #pragma unroll
-    for (int k = 0; k < IT; ++k) *reinterpret_cast<f32x4_t*>(d + k * STEP * LD) = buf[k];
+      for (int k = 0; k < IT; ++k)   // rows r + k STEP: r / 8 % 4 is k's share alone
+        *reinterpret_cast<f32x4_t*>(lds + (r + k * STEP) * LD + (p ^ (k * STEP / 8 & 3)) * VEC) = buf[k];
+    } else {
+      T* d = lds + (tid / CV) * LD + (tid % CV) * VEC;
+#pragma unroll
+      for (int k = 0; k < IT; ++k) *reinterpret_cast<f32x4_t*>(d + k * STEP * LD) = buf[k];
+    }
+  }
+};
+
+// A chunk's rows of k or q as the walks read them: operand fragments of tile t's rows in pair order (columns 32 q ..),
+// and of tile j's columns in pair order (rows 32 ks ..)
+template <typename T, int NT, int NTHR> struct ChunkRows {
+  static constexpr bool SWZ = sizeof(T) == 2 && NT == 4;
+  using TileT = Tile<T, CH, 32 * NT, NTHR, SWZ>;
+  static __device__ __forceinline__ typename Fr<T>::X rows(const T* m, int t, int q) {
+    const int l = static_cast<int>(threadIdx.x) & 63, g = l >> 4, c = l & 15;
+    if constexpr (SWZ) return Fr<T>::load(m + perm_row(t, c) * TileT::LD + 8 * (4 * (q ^ (c & 3)) + (g ^ (c >> 2))));
+    else return Fr<T>::load(m + perm_row(t, c) * TileT::LD + 32 * q + 8 * g);
+  }
+  static __device__ __forceinline__ typename Fr<T>::X cols(const T* m, int j, int ks) {
+    const int l = static_cast<int>(threadIdx.x) & 63, g = l >> 4, c = l & 15;
+    if constexpr (SWZ) {
+      const T* at = m + (32 * ks + 8 * g + (c >> 2)) * TileT::LD + 8 * (4 * ((j >> 1) ^ (c >> 2)) + ((c & 3) ^ g)) + 4 * (j & 1);
+      union { ssd::s16x4_t h[2]; typename Fr<T>::X x; } u;
+      u.h[0] = ssd::lds_read_tr16(at);
+      u.h[1] = ssd::lds_read_tr16(at + 4 * TileT::LD);
+      return u.x;
+    } else {
+      return Fr<T>::template load_tr<8>(m + pair_col(j), TileT::LD, 32 * ks + 8 * g);
+    }
   }
 };
 

@@ -368,6 +368,7 @@ template <typename T, int NT, bool BWD, int NSW> struct WalkCfg {
   static constexpr int ND = 32 * NT, PS = SLICE * NSW, NOUT = BWD && NSW == 2 ? 2 : NSW / 2, NZ = NSW / NOUT, NST = 2, HT = 64 * NST, THREADS = 64 * (NSW + NOUT + NST);
   using TileN = Tile<T, CH, ND, HT>;
   using TileP = Tile<T, CH, PS, HT>;
+  using K = ChunkRows<T, NT, HT>;
   // q and the scores through LDS, or (512-byte rows: no room) straight into the output waves' registers
   static constexpr bool QLDS = sizeof(T) * ND <= 256;
   // terms of the entering states and the scores in o: one where o ends in bf16 (its error then is 2.4e-3, the
@@ -375,7 +376,8 @@ template <typename T, int NT, bool BWD, int NSW> struct WalkCfg {
   static constexpr int XP = BWD || sizeof(T) == 4 ? 2 : 1;
   static constexpr int PIECES = FRAG_PIECES / 2 * XP;   // of the scores
   static constexpr size_t N_BYTES = sizeof(T) * TileN::LDS_ELEMS, V_BYTES = sizeof(T) * TileP::LDS_ELEMS;
-  static constexpr size_t OFF_V = 2 * N_BYTES;
+  static constexpr size_t K_BYTES = sizeof(T) * K::TileT::LDS_ELEMS;
+  static constexpr size_t OFF_V = 2 * K_BYTES;
   static constexpr size_t OFF_Q = OFF_V + 2 * V_BYTES;
   static constexpr size_t OFF_P = OFF_Q + (QLDS ? 2 * N_BYTES : 0);
   static constexpr size_t OFF_XS = OFF_P + (QLDS ? 2 * 16 * PIECES : 0);
@@ -397,7 +399,7 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
   constexpr int LDN = TileN::LD, LDP = TileP::LD, XP = Cf::XP, PS = Cf::PS, XB = Cf::XBUF - 1;
   constexpr int HALVES = sizeof(T) / 2;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  auto kbuf = [&](int i) { return reinterpret_cast<T*>(smem + (i & 1) * Cf::N_BYTES); };
+  auto kbuf = [&](int i) { return reinterpret_cast<T*>(smem + (i & 1) * Cf::K_BYTES); };
   auto vbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_V + (i & 1) * Cf::V_BYTES); };
   auto qbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_Q + (i & 1) * Cf::N_BYTES); };
   auto pbuf = [&](int i) { return reinterpret_cast<uint4*>(smem + Cf::OFF_P) + (i & 1) * Cf::PIECES; };
@@ -447,7 +449,7 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) kf[t][q] = F::load(kt + perm_row(t, c) * LDN + 32 * q + 8 * g);
+        for (int t = 0; t < 4; ++t) kf[t][q] = Cf::K::rows(kt, t, q);
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -479,7 +481,7 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
         for (int j = 2 * q; j < 2 * q + 2; ++j) {
           S[j] *= last;
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) kc[j][ks] = F::template load_tr<8>(kt + pair_col(j), LDN, 32 * ks + 8 * g);
+          for (int ks = 0; ks < 2; ++ks) kc[j][ks] = Cf::K::cols(kt, j, ks);
         }
       }
       f32x4_t bo[4];
@@ -718,7 +720,8 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
   const T* kp = static_cast<const T*>(p.k) + row_offset(s0, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N;
   const T* vp = static_cast<const T*>(p.v) + row_offset(s0, p.L, p.v_sb, p.v_sl) + static_cast<int64_t>(h) * p.P + PS * ps;
   constexpr int GI = (WALK_GATES * CH + Cf::HT - 1) / Cf::HT;
-  TileN tk, tq;
+  typename Cf::K::TileT tk;
+  TileN tq;
   TileP tv;
   Pieces<Cf::PIECES, Cf::HT> tp;
   float tg[GI];

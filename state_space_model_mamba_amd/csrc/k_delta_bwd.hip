@@ -40,7 +40,8 @@ namespace delta {
 // ---------------------------------------------------------------------------
 template <typename T, int NT> struct RwalkCfg {
   static constexpr int ND = 32 * NT, NSW = 2, PS = SLICE * NSW, NST = 2, HT = 64 * NST, THREADS = 64 * (2 * NSW + 1 + NST);
-  using TileN = Tile<T, CH, ND, HT>;
+  using K = ChunkRows<T, NT, HT>;
+  using TileN = typename K::TileT;
   using TileP = Tile<T, CH, PS, HT>;
   static constexpr size_t N_BYTES = sizeof(T) * TileN::LDS_ELEMS, P_BYTES = sizeof(T) * TileP::LDS_ELEMS;
   // k and q twice, staged while the others work; 512-byte rows once, staged between the chunks
@@ -61,7 +62,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
   using F = Fr<T>;
   using TileN = typename Cf::TileN;
   using TileP = typename Cf::TileP;
-  constexpr int LDN = TileN::LD, LDP = TileP::LD, NSW = Cf::NSW, PS = Cf::PS, KB = Cf::KBUF - 1;
+  constexpr int LDP = TileP::LD, NSW = Cf::NSW, PS = Cf::PS, KB = Cf::KBUF - 1;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   auto kbuf = [&](int i) { return reinterpret_cast<T*>(smem + (i & KB) * Cf::N_BYTES); };
   auto qbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_Q + (i & KB) * Cf::N_BYTES); };
@@ -126,7 +127,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
 #pragma unroll
           for (int q = 0; q < NT; ++q) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) kf[t][q] = F::load(kt + perm_row(t, c) * LDN + 32 * q + 8 * g);
+            for (int t = 0; t < 4; ++t) kf[t][q] = Cf::K::rows(kt, t, q);
           }
         }
         __syncthreads();
@@ -134,7 +135,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
 #pragma unroll
           for (int q = 0; q < NT; ++q) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) kf[t][q] = F::load(kt + perm_row(t, c) * LDN + 32 * q + 8 * g);
+            for (int t = 0; t < 4; ++t) kf[t][q] = Cf::K::rows(kt, t, q);
           }
         }
 #pragma unroll
@@ -161,7 +162,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
             if constexpr (KB != 0) q0[j] = xq0(i)[(w * 2 * NT + j) * 64 + l];
             S[j] = dec * S[j] + q0[j];
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) kc[j][ks] = F::template load_tr<8>(kt + pair_col(j), LDN, 32 * ks + 8 * g);
+            for (int ks = 0; ks < 2; ++ks) kc[j][ks] = Cf::K::cols(kt, j, ks);
           }
         }
         f32x4_t bi[4];
@@ -298,7 +299,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
         for (int z = 0; z < NSW; ++z) acc[z] = zero4();
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          const typename F::X xq = F::template load_tr<8>(qt + pair_col(j), LDN, 32 * ks + 8 * g);
+          const typename F::X xq = Cf::K::cols(qt, j, ks);
 #pragma unroll
           for (int z = 0; z < NSW; ++z) acc[z] = mma(xq, fd[z][ks], acc[z]);
         }

@@ -36,9 +36,10 @@ BASE = dict(batch=2, seqlen=100, nheads=4, headdim=16, ngroups=2, dstate=32, nse
     (dict(batch=0), -2), (dict(seqlen=0), -2), (dict(nheads=5), -2), (dict(ngroups=0), -2), (dict(headdim=12), -2),
     (dict(headdim=1032), -2), (dict(dstate=20), -2), (dict(dstate=136), -2), (dict(io_dtype=3), -2), (dict(nseqs=0), -2),
     (dict(nheads=65538, ngroups=1), -2), (dict(batch=1 << 20, seqlen=1 << 12), -2), (dict(strides=(4, 0, 0, 0, 0, 0)), -2),
-    (dict(strides=(0, 0, 0, 0, -8, 64)), -2),
+    (dict(strides=(0, 0, 0, 0, -8, 64)), -2), (dict(strides=(0, 0, 0, 1 << 27, 0, 0)), -2),
+    (dict(nheads=65535, ngroups=1, headdim=1024), 0), (dict(nheads=65535, ngroups=65535, headdim=1032), -2),
 ])
-def test_unsupported_shapes_are_rejected(kw, code):
+def test_shapes_at_and_past_the_limits(kw, code):
     s = delta.make_shape(**{**BASE, **kw})
     n = ctypes.c_size_t(0)
     assert delta.load_library().delta_workspace_size(ctypes.byref(s), 0, ctypes.byref(n)) == code

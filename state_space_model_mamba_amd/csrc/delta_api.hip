@@ -50,7 +50,7 @@ size_t place(Problem& p, int io, bool backward, char* base) {
   };
   const size_t sh = static_cast<size_t>(p.nslots) * p.H, rows = static_cast<size_t>(p.rows);
   const size_t nd = p.N <= 64 ? 64 : 128, io_size = io == SSD_IO_BF16 ? 2 : 4, frags = sh * delta::FRAG_PIECES * 16;
-  p.starts = reinterpret_cast<int32_t*>(take((static_cast<size_t>(p.nseqs) + 1) * 4));
+  p.starts = reinterpret_cast<int32_t*>(take((2 * static_cast<size_t>(p.nseqs) + 1) * 4));
   p.gates = reinterpret_cast<float*>(take(sh * delta::GATES * delta::CH * 4));
   p.tf = reinterpret_cast<uint4*>(take(frags));
   p.pf = reinterpret_cast<uint4*>(take(frags));

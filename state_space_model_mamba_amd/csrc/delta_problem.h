@@ -29,7 +29,7 @@ struct Problem {
   void *o, *dq, *dk, *dv;
   float *final, *dg, *dbeta, *dinit;
   // workspace
-  int32_t* starts;   // (nseqs + 1) first rows (seq_idx given)
+  int32_t* starts;   // (nseqs + 1) first rows, then (nseqs) the sequences longest first (seq_idx given)
   float* gates;      // (slots, H, GATES, 64)
   uint4* tf;         // (slots, H, FRAG_PIECES): T' - I, T' = (I + N diag(beta))^-1, rows in pair order
   uint4* pf;         // the same of the causal scores, rows in order (bf16 forward: the first terms alone)
@@ -66,16 +66,15 @@ __device__ __forceinline__ int slot_base(int start, int s) { return (start >> 6)
 struct Chunk {
   int seq, row, len;   // sequence, first row (flat), rows of the chunk (0: the slot holds none)
 };
-// Sequence, head and value column block of a walk's block.  Consecutive ones run on the same XCD, whose L2 then serves
-// a head's chunk matrices to its column blocks and a group's q and k to its heads.
+// Sequence, head and value column block of a walk's block.  Packed sequences go longest first, so that none of them is
+// left to run alone at the end.  Within a sequence, consecutive (head, column block)s run on the same XCD, whose L2
+// then serves a head's chunk matrices to its column blocks and a group's q and k to its heads.
 struct Place {
   int seq, h, ps;
 };
-__device__ __forceinline__ Place place_of(int np) {
-  const int64_t across = gridDim.x;
-  const int64_t id = ssd::xcd_logical_block(static_cast<int64_t>(blockIdx.y) * across + blockIdx.x, across * gridDim.y);
-  const int x = static_cast<int>(id % across);
-  return Place{static_cast<int>(id / across), x / np, x % np};
+__device__ __forceinline__ Place place_of(const Problem& p, int np) {
+  const int x = static_cast<int>(ssd::xcd_logical_block(blockIdx.x, gridDim.x)), y = static_cast<int>(blockIdx.y);
+  return Place{p.seq_idx ? p.starts[p.nseqs + 1 + y] : y, x / np, x % np};
 }
 
 // which chunk a slot holds

@@ -27,8 +27,8 @@ namespace delta {
 
 // ---------------------------------------------------------------------------
 // k_delta_starts: the first rows of the sequences that seq_idx marks, in row
-// order.  One block: every thread takes 16 rows of a stretch of 16384, the
-// counts are scanned over the block.
+// order, and the order in which the walks take them.  One block: every thread
+// takes 16 rows of a stretch of 16384, the counts are scanned over the block.
 // ---------------------------------------------------------------------------
 constexpr int ST_THR = 1024, ST_ROWS = 16;
 
@@ -76,6 +76,23 @@ __global__ __launch_bounds__(ST_THR) void k_delta_starts(Problem p) {
     __syncthreads();
   }
   for (int64_t s = static_cast<int64_t>(base) + tid; s <= p.nseqs; s += ST_THR) p.starts[s] = p.total;
+  // the walks' order: longest first, equal ones by number (more sequences than ST_THR keep their own: with so many
+  // blocks no single one is the end)
+  __syncthreads();
+  int32_t* order = p.starts + p.nseqs + 1;
+  if (p.nseqs > ST_THR) {
+    for (int s = tid; s < p.nseqs; s += ST_THR) order[s] = s;
+    return;
+  }
+  __shared__ int len[ST_THR];
+  if (tid < p.nseqs) len[tid] = p.starts[tid + 1] - p.starts[tid];
+  __syncthreads();
+  if (tid < p.nseqs) {
+    const int mine = len[tid];
+    int rank = 0;
+    for (int s = 0; s < p.nseqs; ++s) rank += len[s] > mine || (len[s] == mine && s < tid) ? 1 : 0;
+    order[rank] = tid;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -409,7 +426,7 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
   auto xe = [&](int i) { return reinterpret_cast<f32x4_t*>(smem + Cf::OFF_XE) + (i & XB) * 64 * NSW * 4; };
 
   const int np = (p.P + PS - 1) / PS;
-  const Place at_block = place_of(np);
+  const Place at_block = place_of(p, np);
   const int h = at_block.h, ps = at_block.ps, seq = at_block.seq, grp = h / p.hpg;
   const int s0 = seq_start(p, seq), s1 = seq_start(p, seq + 1);
   const int nchunk = (s1 - s0 + CH - 1) / CH, slot0 = slot_base(s0, seq);

@@ -75,7 +75,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
   uint4* xs = reinterpret_cast<uint4*>(smem + Cf::OFF_XS);        // [wave][q][term][lane]
 
   const int np = (p.P + PS - 1) / PS;
-  const Place at_block = place_of(np);
+  const Place at_block = place_of(p, np);
   const int h = at_block.h, ps = at_block.ps, seq = at_block.seq, grp = h / p.hpg;
   const int s0 = seq_start(p, seq), s1 = seq_start(p, seq + 1);
   const int nchunk = (s1 - s0 + CH - 1) / CH, slot0 = slot_base(s0, seq), last = nchunk - 1;

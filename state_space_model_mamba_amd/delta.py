@@ -75,6 +75,11 @@ def _sized(batch, seqlen, nheads, headdim, ngroups, dstate, nseqs, io_dtype, sca
     return make_shape(batch, seqlen, nheads, headdim, ngroups, dstate, nseqs, io_dtype, scale, strides)
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, nseqs, io_dtype, backward) -> int:
+    return workspace_size(make_shape(batch, seqlen, nheads, headdim, ngroups, dstate, nseqs, io_dtype), backward)
+
+
 def row_strides(t, name):
     """(batch, row) strides of a (batch, rows, heads, width) tensor whose last two axes are contiguous."""
     if t.is_contiguous():
@@ -155,7 +160,8 @@ def _nseqs(q, initial_states, seq_idx, nseqs) -> int:
 
 
 def _workspace(shape, backward, workspace, dev):
-    nbytes = workspace_size(shape, backward)
+    nbytes = _workspace_bytes(shape.batch, shape.seqlen, shape.nheads, shape.headdim, shape.ngroups, shape.dstate,
+                              shape.nseqs, shape.io_dtype, backward)
     if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     if workspace.device != dev or not workspace.is_contiguous():

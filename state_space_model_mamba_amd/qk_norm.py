@@ -7,6 +7,7 @@ an error.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -60,7 +61,14 @@ def workspace_size(shape: QkNormShape) -> int:
     return n.value
 
 
-def _shape(q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved) -> QkNormShape:
+@functools.lru_cache(maxsize=256)
+def _sized(*sizes) -> tuple[QkNormShape, int]:
+    """make_shape and its workspace size, kept per sizes (callers read them only)."""
+    shape = make_shape(*sizes)
+    return shape, workspace_size(shape)
+
+
+def _shape(q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved) -> tuple[QkNormShape, int]:
     dev, io = q.device, q.dtype
     if dev.type != "cuda":
         raise ValueError(f"qk_norm_rope runs on a HIP device; got tensors on {dev}")
@@ -86,8 +94,8 @@ def _shape(q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved
             raise ValueError(f"inv_freq turns {rot} values of rows of {N}")
     elif positions is not None:
         raise ValueError("positions go with inv_freq")
-    return make_shape(b, L, Gq, 0 if k is None else k.shape[2], N, rot, interleaved, norm,
-                      ssd.SSD_IO_BF16 if io == torch.bfloat16 else ssd.SSD_IO_F32, float(eps), strides)
+    return _sized(b, L, Gq, 0 if k is None else k.shape[2], N, rot, bool(interleaved), norm,
+                  ssd.SSD_IO_BF16 if io == torch.bfloat16 else ssd.SSD_IO_F32, float(eps), strides)
 
 
 def qk_norm_rope_fwd(q, k=None, q_weight=None, k_weight=None, positions=None, inv_freq=None, eps: float = 1e-6,
@@ -100,7 +108,7 @@ def qk_norm_rope_fwd(q, k=None, q_weight=None, k_weight=None, positions=None, in
     (1 / sqrt(mean x^2 + eps)) or "l2" (1 / sqrt(sum x^2 + eps)); interleaved: pairs (2j, 2j+1) instead of
     (j, j + len(inv_freq)).
     """
-    shape = _shape(q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved)
+    shape, _ = _shape(q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved)
     dev = q.device
     q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev)
@@ -117,14 +125,13 @@ def qk_norm_rope_fwd(q, k=None, q_weight=None, k_weight=None, positions=None, in
 def qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, eps: float = 1e-6,
                      norm: str = "rms", interleaved: bool = False, workspace: Optional[torch.Tensor] = None) -> dict:
     """dict of dq, dk (like q and k, contiguous), dq_weight and dk_weight ((N) fp32, or None without the weight)."""
-    shape = _shape(q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved)
+    shape, nbytes = _shape(q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved)
     dev = q.device
     ssd._check(dq_out, "dq_out", q.dtype, tuple(q.shape), dev)
     if (k is None) != (dk_out is None):
         raise ValueError("dk_out goes with k")
     if k is not None:
         ssd._check(dk_out, "dk_out", k.dtype, tuple(k.shape), dev)
-    nbytes = workspace_size(shape)
     if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():

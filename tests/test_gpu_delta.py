@@ -122,6 +122,11 @@ def test_packed_sequences(io):
     check(make(1, sum(lengths), 4, 40, 2, 48, io, seed=5, lengths=lengths, initial=True), f"{io} packed")
 
 
+def test_more_sequences_than_a_block_ranks():
+    lengths = [1 + i % 3 for i in range(1100)]
+    check(make(1, sum(lengths), 1, 8, 1, 8, "f32", seed=21, lengths=lengths, initial=True), "1100 sequences")
+
+
 def test_packed_rows_of_a_batch_with_recurring_ids():
     d = make(2, 90, 2, 16, 1, 16, "f32", seed=6)
     ids = torch.zeros(2, 90, dtype=torch.int32)

@@ -65,6 +65,7 @@ size_t place(Problem& p, int io, bool backward, char* base) {
     p.vv = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));
     p.be = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));
     p.phi = reinterpret_cast<float*>(take(sh * p.nsl * 4));
+    if (p.ns > 1) p.parts = reinterpret_cast<float*>(take(static_cast<size_t>(p.nslots) * p.G * p.ns * 2 * delta::CH * nd * 4));
   }
   return at;
 }
@@ -85,6 +86,12 @@ Problem problem(const delta_shape& s) {
   // groups take 109 us at one head a block, 53 at four; 256 chunks 793 us at one, 275 at eight.
   p.hb = 1;
   while (p.hb < 8 && p.hb < p.hpg && static_cast<int64_t>(p.nslots) * p.H / (2 * p.hb) >= 1024) p.hb *= 2;
+  // and the gradients' groups are cut where there are fewer chunks and groups than CUs: 32 chunks of 64 heads of one
+  // group take 275 us in one part, 51 in eight; from 256 blocks on one part is the faster (299 us at 256 chunks)
+  p.ns = 1;
+  while (p.ns < p.hpg && static_cast<int64_t>(p.nslots) * p.G * p.ns < 256) p.ns *= 2;
+  p.hs = (p.hpg + p.ns - 1) / p.ns;
+  p.ns = (p.hpg + p.hs - 1) / p.hs;
   p.rows = (p.P + delta::PAD - 1) / delta::PAD * delta::PAD;
   p.nsl = p.rows / delta::SLICE;
   p.scale = s.scale;

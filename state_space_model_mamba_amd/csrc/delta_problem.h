@@ -17,6 +17,7 @@ struct Problem {
   int total;      // B * L rows
   int nslots;     // chunk slots: the chunks of sequence s are slots start(s) / 64 + s, ...
   int hb;         // heads of a group that one block of k_delta_prep takes
+  int ns, hs;     // parts that k_delta_grad takes a group's heads in, and heads of a part
   int rows;       // P rounded up to a multiple of PAD
   int nsl;        // slices of 16 value columns: rows / SLICE
   float scale;
@@ -44,6 +45,7 @@ struct Problem {
   float* vv;         // (slots, H, nsl, 64): dv . v
   float* be;         // (slots, H, nsl, 64): Du . e
   float* phi;        // (slots, H, nsl): <entering state, its gradient>
+  float* parts;      // (slots, G, ns, 2, 64, ND): the parts' dq and dk (ns > 1)
 };
 
 // Per slot and head, 64 values each: exp(c_i); beta_i exp(c_last - c_i); beta_i; exp(c_last - c_i); -beta_i exp(c_i);

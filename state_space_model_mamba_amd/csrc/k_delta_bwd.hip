@@ -492,7 +492,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
 // ---------------------------------------------------------------------------
 // k_delta_grad: dq and dk of one chunk and group, its heads one
 // after the other (dq and dk are sums over them, taken in registers in head
-// order).  Eight waves: 16 rows of the chunk times half of the N columns each.
+// order); on small grids parts of the heads, added up by k_delta_parts.  Eight waves: 16 rows of the chunk times half of the N columns each.
 // All products end in the io type, so every operand is a single term.
 // ---------------------------------------------------------------------------
 constexpr int GTHR = 512;
@@ -535,7 +535,8 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
   T* fm = reinterpret_cast<T*>(smem + Cf::OFF_F);
   float* gs = reinterpret_cast<float*>(smem + Cf::OFF_G);
 
-  const int slot = static_cast<int>(blockIdx.x), grp = static_cast<int>(blockIdx.y);
+  const int slot = static_cast<int>(blockIdx.x), grp = static_cast<int>(blockIdx.y) / p.ns, part = static_cast<int>(blockIdx.y) % p.ns;
+  const int first_head = part * p.hs, end_head = min(p.hpg, first_head + p.hs);   // of the group
   const Chunk ch = chunk_of(p, slot);
   if (ch.len == 0) return;
   const int tid = static_cast<int>(threadIdx.x), l = tid & 63, g = l >> 4, c = l & 15, w = ssd::wave_id_s();
@@ -552,7 +553,17 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
 #pragma unroll
   for (int t = 0; t < NT; ++t) dqa[t] = dka[t] = zero4();
 
-  for (int hh = 0; hh < p.hpg; ++hh) {
+  constexpr int HALVES = sizeof(T) / 2;
+  // the states of a head's slice are requested while the one before is worked on
+  typename Cf::TileS ts, tds;
+  auto request = [&](int hh, int p0) {
+    const int64_t first = (static_cast<int64_t>(slot) * p.H + grp * p.hpg + hh) * p.nsl + p0 / SLICE;
+    const int nslices = min(PSL / SLICE, p.nsl - p0 / SLICE);
+    ts.load(p.s + first * 2 * NT * 64, 2 * NT * 64, nslices, tid);   // bf16: the first terms
+    tds.load(p.ds + first * HALVES * NT * 64, HALVES * NT * 64, nslices, tid);
+  };
+  request(first_head, 0);
+  for (int hh = first_head; hh < end_head; ++hh) {
     const int h = grp * p.hpg + hh;
     const int64_t sh = static_cast<int64_t>(slot) * p.H + h;
     f32x4_t x1[NT], x2[NT], x3[NT], m1[2], m2[2];
@@ -563,16 +574,12 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
       const int pcols = min(PSL, p.P - p0);
       typename Cf::TileP td, tv;
       typename Cf::TileU tu;
-      typename Cf::TileS ts, tds;
       const int64_t at = static_cast<int64_t>(ch.row) * hp + static_cast<int64_t>(h) * p.P + p0;
       td.load(static_cast<const T*>(p.dout) + at, hp, ch.len, pcols, tid);
       tv.load(static_cast<const T*>(p.dv) + at, hp, ch.len, pcols, tid);
       const int64_t first = sh * p.nsl + p0 / SLICE;
       const int nslices = min(PSL / SLICE, p.nsl - p0 / SLICE);
-      constexpr int HALVES = sizeof(T) / 2;
       tu.load(p.u + first * HALVES * 2 * 64, HALVES * 2 * 64, nslices, tid);
-      ts.load(p.s + first * 2 * NT * 64, 2 * NT * 64, nslices, tid);   // bf16: the first terms
-      tds.load(p.ds + first * HALVES * NT * 64, HALVES * NT * 64, nslices, tid);
       const float tg = tid < GATES * CH ? p.gates[sh * (GATES * CH) + tid] : 0.f;
       __syncthreads();   // the previous head's last products are done
       td.store(dot, tid);
@@ -582,6 +589,8 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
       tds.store(dst, tid);
       if (tid < GATES * CH) gs[tid] = tg;
       __syncthreads();
+      if (p0 + PSL < p.P) request(hh, p0 + PSL);
+      else if (hh + 1 < end_head) request(hh + 1, 0);
 #pragma unroll
       for (int ks = 0; ks < PSL / 32; ++ks) {
         const typename F::X xdo = F::load(dot + row * LDP + 32 * ks + 8 * g), xdv = F::load(dvt + row * LDP + 32 * ks + 8 * g);
@@ -649,6 +658,16 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
       }
     }
   }
+  if (p.ns > 1) {   // this part's sums, for k_delta_parts
+    float* to = p.parts + ((static_cast<int64_t>(slot) * p.G + grp) * p.ns + part) * 2 * CH * Cf::ND + row * Cf::ND;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int n = 16 * (half * NT + t) + 4 * g;
+      *reinterpret_cast<f32x4_t*>(to + n) = dqa[t];
+      *reinterpret_cast<f32x4_t*>(to + CH * Cf::ND + n) = dka[t];
+    }
+    return;
+  }
   if (row < ch.len) {
     const int64_t at = ((static_cast<int64_t>(ch.row) + row) * p.G + grp) * p.N;
 #pragma unroll
@@ -659,6 +678,28 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
         ssd::store4f<T>(static_cast<T*>(p.dk) + at + n, dka[t]);
       }
     }
+  }
+}
+
+// dq and dk from the parts of a group's heads, in order.
+constexpr int PARTS_Z = 8;   // blocks of a chunk
+template <typename T, int NT> __global__ __launch_bounds__(256) void k_delta_parts(Problem p) {
+  constexpr int ND = 32 * NT;
+  const int slot = static_cast<int>(blockIdx.x), grp = static_cast<int>(blockIdx.y);
+  const Chunk ch = chunk_of(p, slot);
+  for (int i = static_cast<int>(blockIdx.z * 256 + threadIdx.x); i < ch.len * (ND / 4); i += 256 * PARTS_Z) {
+    const int row = i / (ND / 4), n = 4 * (i % (ND / 4));
+    if (n >= p.N) continue;
+    const float* from = p.parts + (static_cast<int64_t>(slot) * p.G + grp) * p.ns * 2 * CH * ND + row * ND + n;
+    f32x4_t q = zero4(), k = zero4();
+#pragma unroll 4
+    for (int s = 0; s < p.ns; ++s) {
+      q += *reinterpret_cast<const f32x4_t*>(from + s * 2 * CH * ND);
+      k += *reinterpret_cast<const f32x4_t*>(from + (2 * s + 1) * CH * ND);
+    }
+    const int64_t at = ((static_cast<int64_t>(ch.row) + row) * p.G + grp) * p.N + n;
+    ssd::store4f<T>(static_cast<T*>(p.dq) + at, q);
+    ssd::store4f<T>(static_cast<T*>(p.dk) + at, k);
   }
 }
 
@@ -711,7 +752,8 @@ template <typename T, int NT> int rwalk(const Problem& p, hipStream_t s) {
 }
 template <typename T, int NT> int grad(const Problem& p, hipStream_t s) {
   static_assert(GradCfg<T, NT>::LDS <= 160 * 1024, "LDS");
-  return go(k_delta_grad<T, NT>, dim3(p.nslots, p.G), GTHR, GradCfg<T, NT>::LDS, s, p);
+  const int rc = go(k_delta_grad<T, NT>, dim3(p.nslots, p.G * p.ns), GTHR, GradCfg<T, NT>::LDS, s, p);
+  return rc != SSD_OK || p.ns == 1 ? rc : go(k_delta_parts<T, NT>, dim3(p.nslots, p.G, PARTS_Z), 256, 0, s, p);
 }
 
 int launch_rwalk(const Problem& p, int io, hipStream_t s) {

@@ -122,6 +122,14 @@ def test_packed_sequences(io):
     check(make(1, sum(lengths), 4, 40, 2, 48, io, seed=5, lengths=lengths, initial=True), f"{io} packed")
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [3, 8, 21])
+def test_heads_of_one_group_in_parts(H, io):
+    # one group and few chunks: its heads go in parts of one or more, the last part short
+    check(make(1, 100, H, 16, 1, 72, io, seed=22 + H), f"{io} {H} heads of one group")
+    check(make(1, 64 * 60 + 1, H, 8, 1, 8, io, seed=23), f"{io} {H} heads of one group, 61 chunks")
+
+
 def test_more_sequences_than_a_block_ranks():
     lengths = [1 + i % 3 for i in range(1100)]
     check(make(1, sum(lengths), 1, 8, 1, 8, "f32", seed=21, lengths=lengths, initial=True), "1100 sequences")

@@ -37,6 +37,9 @@ namespace delta {
 //   * a wave each follows behind with what Du gives, for chunk i + 1: dv, the
 //     row sums for the gates' gradients, and the stores,
 //   * two waves stage the coming chunks' rows in LDS.
+// Bound by memory: a chunk and head reads the states (32 KB), residuals (16 KB),
+// matrices (24 KB), v and dout and writes dS and dv (24 KB), 16384 rows of 128
+// heads of 64 x 128 in 1.0 ms; in one kind of wave alone it took 2.7 ms.
 // ---------------------------------------------------------------------------
 template <typename T, int NT> struct RwalkCfg {
   static constexpr int ND = 32 * NT, NSW = 2, PS = SLICE * NSW, NST = 2, HT = 64 * NST, THREADS = 64 * (2 * NSW + 1 + NST);
@@ -493,7 +496,10 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
 // k_delta_grad: dq and dk of one chunk and group, its heads one
 // after the other (dq and dk are sums over them, taken in registers in head
 // order); on small grids parts of the heads, added up by k_delta_parts.  Eight waves: 16 rows of the chunk times half of the N columns each.
-// All products end in the io type, so every operand is a single term.
+// All products end in the io type, so every operand is a single term (bf16: dq
+// and dk come out 2.9e-3 off, 1.7e-3 of it their own rounding).  Bound by the
+// 56 KB that a chunk and head brings in and by one block a CU (LDS): 0.63 ms at
+// 16384 rows of 128 heads of 64 x 128, 2.9 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int GTHR = 512;
 

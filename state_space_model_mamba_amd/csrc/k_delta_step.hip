@@ -171,8 +171,8 @@ template <typename T, int NV, int RG> int go(StepArgs a, hipStream_t s) {
   hipLaunchKernelGGL((k_delta_step<T, NV, RG>), dim3(a.H * a.nblk, a.B), dim3(64 * STEP_WAVES), 0, s, a);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
-// Two rows a lane where that still gives every CU eight waves, else one (one sequence of 128 heads of 64 x 128: STEP1;
-// 64 of them: STEP2).
+// Two rows a lane where that still gives every CU eight waves, else one.  64 sequences of 128 heads of 64 x 128: 95 us
+// at one row, 80.5 at two (480 MB: 6.0 TB/s), 124 at four; one sequence: 5.3 us at one row, 5.9 at two.
 template <typename T> int by_size(const StepArgs& a, hipStream_t s) {
   if (static_cast<int64_t>(a.B) * a.H * ((a.P + 15) / 16) >= 8 * 256)
     return a.N <= 32 ? go<T, 1, 2>(a, s) : a.N <= 64 ? go<T, 2, 2>(a, s) : go<T, 4, 2>(a, s);

@@ -35,6 +35,9 @@
  * gates and every sum are float32; with bf16 io the products whose result
  * reaches a state or a gate's gradient take their float32 operands as two
  * bf16 terms (16 bits of mantissa), the others as one.
+ * A NaN or an infinity in a row of q, k, v, g or beta may reach every row of
+ * its sequence from the first of its chunk of 64 rows on (in the backward
+ * every row), and no other sequence.
  *
  * Ownership and calling convention: as for ssd_bwd (device pointers of the
  * caller, 16-byte aligned; outputs fully overwritten; no allocation; work
@@ -86,6 +89,7 @@ int delta_fwd(const delta_shape* shape, const void* q, const void* k, const void
  * Gradients of l = sum dout * o + sum d_final_states * final_states, the
  * forward recomputed from the inputs.  d_final_states (nullable: zeros) and
  * d_initial_states (nullable: not computed) are shaped like the states.
+ * Rows of sequences past nseqs are left as they were, as in delta_fwd.
  */
 int delta_bwd(const delta_shape* shape, const void* q, const void* k, const void* v, const float* g,
               const float* beta, const float* initial_states, const int32_t* seq_idx, const void* dout,
@@ -99,7 +103,8 @@ int delta_bwd(const delta_shape* shape, const void* q, const void* k, const void
  * states[b], nslots >= batch).  A row whose index is negative or not below
  * nslots is empty: its o is zero and no state changes.  Rows that name the
  * same state take their turns in row order, one after the other's tokens.
- * shape->nseqs is not read; no workspace.
+ * o may be none of q, k, v and states.  shape->nseqs is not read; no
+ * workspace.
  */
 int delta_step(const delta_shape* shape, const void* q, const void* k, const void* v, const float* g,
                const float* beta, float* states, int64_t nslots, const int32_t* state_indices, void* o,

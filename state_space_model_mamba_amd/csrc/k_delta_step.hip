@@ -200,6 +200,7 @@ extern "C" int delta_step(const delta_shape* shape, const void* q, const void* k
   if (sh.seqlen > 64 || sh.batch > 65535) return SSD_ERR_UNSUPPORTED_SHAPE;
   if (!q || !k || !v || !g || !beta || !states || !o || nslots < 1) return SSD_ERR_INVALID_ARG;
   if (!state_indices && nslots < sh.batch) return SSD_ERR_INVALID_ARG;
+  if (o == q || o == k || o == v || o == states) return SSD_ERR_INVALID_ARG;   // other blocks may still read them
   for (const void* p : {q, k, v, static_cast<const void*>(states), static_cast<const void*>(o)})
     if (reinterpret_cast<uintptr_t>(p) & 15u) return SSD_ERR_MISALIGNED;
   int64_t st[6];

@@ -107,6 +107,13 @@ def _check_strided(t, name, dtype, shape, device):
     return row_strides(t, name)
 
 
+def _gradient(t):
+    """An incoming gradient as the kernels read it: contiguous, from an address of 16 bytes (a slice of a larger
+    gradient may start anywhere)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _stream(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
@@ -255,9 +262,9 @@ class GatedDeltaRule(torch.autograd.Function):
         q, k, v, g, beta, h0, seq_idx = ctx.saved_tensors
         if do is None and d_final is None:
             return (None,) * 9
-        do = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if do is None else do.contiguous()
+        do = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if do is None else _gradient(do)
         want_h0 = h0 is not None and ctx.needs_input_grad[5]
-        r = delta_bwd(q, k, v, g, beta, do, h0, seq_idx, None if d_final is None else d_final.contiguous(), ctx.scale,
+        r = delta_bwd(q, k, v, g, beta, do, h0, seq_idx, None if d_final is None else _gradient(d_final), ctx.scale,
                       ctx.nseqs, want_d_initial_states=want_h0)
         return r["dq"], r["dk"], r["dv"], r["dg"], r["dbeta"], r["d_initial_states"], None, None, None
 
@@ -276,7 +283,8 @@ def delta_step(q, k, v, g, beta, states, state_indices=None, scale: Optional[flo
     q, k: (b, T, G, N), v: (b, T, H, P), g, beta: (b, T, H) as for delta_fwd; states: (slots, H, P, N) fp32,
     updated in place; state_indices: (b) int32, the state of each row (None: row b has state b).  A row whose index
     is negative (or past the pool) is empty: its o is zero.  Rows that name the same state take their turns in row
-    order.  Returns o (like v, contiguous; ``out`` when given).
+    order.  Returns o (like v, contiguous; ``out`` when given).  Not differentiable; autograd sees that states (and
+    out) change.
     """
     shape = _inputs("delta_step", q, k, v, g, beta, q.shape[0], scale)
     dev = q.device
@@ -303,4 +311,7 @@ def delta_step(q, k, v, g, beta, states, state_indices=None, scale: Optional[flo
                             _stream(dev))
     if rc:
         raise ssd.SsdError(rc, "delta_step")
+    for t in (states, out):
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
     return out

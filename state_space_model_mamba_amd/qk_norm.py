@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from state_space_model_mamba_amd import ssd
-from state_space_model_mamba_amd.delta import _check_strided, _on, _stream
+from state_space_model_mamba_amd.delta import _check_strided, _gradient, _on, _stream
 
 QK_NORM_RMS, QK_NORM_L2 = 0, 1
 NORMS = {"rms": QK_NORM_RMS, "l2": QK_NORM_L2}
@@ -165,8 +165,8 @@ class QkNormRope(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
-        r = qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, dq_out.contiguous(),
-                             None if k is None else dk_out.contiguous(), *ctx.args)
+        r = qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, _gradient(dq_out),
+                             None if k is None else _gradient(dk_out), *ctx.args)
         return r["dq"], r["dk"], r["dq_weight"], r["dk_weight"], None, None, None, None, None
 
 

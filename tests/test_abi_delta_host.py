@@ -169,3 +169,9 @@ def test_row_strides_of_slices():
             delta.row_strides(bad, "s")
     with pytest.raises(ValueError, match="broadcast"):
         delta.row_strides(x[:1, :1, :16].unflatten(-1, (2, 8)).expand(3, 7, 2, 8), "s")
+
+
+def test_step_refuses_its_output_in_an_inputs_place():
+    few = delta.make_shape(**{**BASE, "seqlen": 4})
+    for name in ("q", "k", "v", "states"):
+        assert step(few, dict(FAKE, o=FAKE[name])) == -1, name

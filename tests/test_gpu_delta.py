@@ -254,6 +254,54 @@ def test_autograd_from_both_outputs():
         assert torch.equal(a, z[k]), k
 
 
+def test_gradients_that_start_anywhere():
+    d = cuda(make(1, 70, 2, 8, 1, 16, "bf16", seed=23))
+    leaves = [x.clone().requires_grad_(True) for x in args(d)]
+    o, fin = delta.gated_delta_rule(*leaves)
+    od, fd = torch.zeros(d["do"].numel() + 1).bfloat16().cuda(), torch.zeros(d["dfin"].numel() + 1).cuda()
+    od[1:], fd[1:] = d["do"].flatten(), d["dfin"].flatten()
+    got = torch.autograd.grad((o, fin), leaves, (od[1:].view(o.shape), fd[1:].view(fin.shape)))
+    g = delta.delta_bwd(*args(d), d["do"], d_final_states=d["dfin"])
+    for a, k in zip(got, GRADS):
+        assert torch.equal(a, g[k]), k
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_value_that_is_no_number_stays_in_its_sequence(value, io):
+    """The middle sequences of a packed batch (one inside a chunk, one of several chunks) full of it."""
+    lengths = [70, 9, 1, 150, 30]
+    d = cuda(make(1, sum(lengths), 4, 24, 2, 40, io, seed=24, lengths=lengths, initial=True))
+    bad = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+    for k in ("q", "k", "v", "beta", "do"):
+        bad[k][:, 70:79] = value
+        bad[k][:, 80:230] = value
+    clean = torch.ones(sum(lengths), dtype=torch.bool)
+    clean[70:79] = clean[80:230] = False
+    kept = [0, 2, 4]
+    run = lambda x: (delta.delta_fwd(*args(x), x["initial_states"], x["seq_idx"], want_final_states=True),  # noqa: E731
+                     delta.delta_bwd(*args(x), x["do"], x["initial_states"], x["seq_idx"], x["dfin"]))
+    (f, g), (bf, bg) = run(d), run(bad)
+    rows = clean.cuda()
+    for k, a, b in [("o", f["o"], bf["o"])] + [(k, g[k], bg[k]) for k in ("dq", "dk", "dv", "dg", "dbeta")]:
+        assert torch.equal(a[:, rows], b[:, rows]), k
+    assert torch.equal(f["final_states"][kept], bf["final_states"][kept])
+    assert torch.equal(g["d_initial_states"][kept], bg["d_initial_states"][kept])
+    assert not torch.isfinite(bf["o"][:, ~rows].float()).all()
+
+
+def test_step_marks_the_states_as_changed():
+    d = cuda(make(1, 1, 2, 8, 1, 16, "bf16", seed=25))
+    states = torch.zeros(1, 2, 8, 16, device="cuda")
+    w = torch.ones(1, device="cuda", requires_grad=True)
+    y = (w * states).sum()   # its backward reads states
+    delta.delta_step(*args(d), states)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+    with torch.inference_mode():
+        delta.delta_step(*args(d), torch.zeros(1, 2, 8, 16, device="cuda"))
+
+
 def test_another_stream_and_replayed_graphs_that_share_a_workspace():
     a, b = cuda(make(1, 200, 4, 64, 1, 128, "bf16", seed=15)), cuda(make(1, 200, 4, 64, 1, 128, "bf16", seed=16))
     eager = [(delta.delta_fwd(*args(x))["o"], delta.delta_bwd(*args(x), x["do"])) for x in (a, b)]

@@ -58,7 +58,6 @@ size_t place(Problem& p, int io, bool backward, char* base) {
     p.ttf = reinterpret_cast<uint4*>(take(frags));
     p.ptf = reinterpret_cast<uint4*>(take(frags));
     p.e = reinterpret_cast<uint4*>(take(sh * rows * delta::CH * 4));
-    p.u = reinterpret_cast<uint4*>(take(sh * rows * delta::CH * io_size));
     p.s = reinterpret_cast<uint4*>(take(sh * rows * nd * 4));
     p.ds = reinterpret_cast<uint4*>(take(sh * rows * nd * io_size));
     p.oo = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));

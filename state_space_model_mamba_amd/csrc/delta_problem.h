@@ -38,7 +38,6 @@ struct Problem {
   uint4* ptf;        // transposed scores, rows in pair order (backward)
   uint4* e;          // (slots, H, nsl, 4, 64): the residuals, float32, accumulator layout (backward)
   // as the lanes hold them (delta_tiles.h), HALVES = 1 (bf16) or 2 (float32):
-  uint4* u;          // (slots, H, nsl, HALVES, 2, 64): beta * e, a chunk's rows (backward)
   uint4* s;          // (slots, H, nsl, 2, NQ, 64): entering states, 2 bf16 terms or float32 (backward)
   uint4* ds;         // (slots, H, nsl, HALVES, NQ, 64): gradient of the state after the chunk (backward)
   float* oo;         // (slots, H, nsl, 64): dout . o over the slice's columns (backward)

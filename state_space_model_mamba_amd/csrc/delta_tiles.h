@@ -214,7 +214,7 @@ __device__ __forceinline__ f32x4_t mma_term(const Fr<bf16_t>::S& a, const Fr<bf1
 // float32: the whole product, taken with the first term
 __device__ __forceinline__ f32x4_t mma_term(const f32x8_t& a, const f32x8_t& b, f32x4_t c, int term) { return term ? c : mma(a, b, c); }
 
-// What the backward keeps per slice of 16 value columns (states, their gradients, corrections) lies in memory as the
+// What the backward keeps per slice of 16 value columns (states and their gradients) lies in memory as the
 // lanes hold it, 16-byte pieces [half][q][lane]: piece (half, q) of lane (g, c) is column c's values 32 q + 8 g .. + 7
 // (bf16; half: the term) or 32 q + 8 g + 4 half .. + 3 (float32).  A wave then stores and loads whole kilobytes;
 // column by column they took 4 times as long in the memory pipeline.

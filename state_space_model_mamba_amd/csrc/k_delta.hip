@@ -377,15 +377,16 @@ template <typename T, int NT, bool BWD> __global__ __launch_bounds__(256, BWD ? 
 // the whole sequence and runs the sequential part alone:
 //     k S -> r -> T' r -> S   (three products a chunk, nothing else).
 // Beside them output waves form the previous chunk's o from the entering
-// state and the residuals that the state waves leave in LDS (in the backward dout . o, and the stores of states and
-// corrections), and two staging waves bring the coming chunks' rows in:
-// their loads are in flight for a whole chunk, which no wave waits for.
+// state and the residuals that the state waves leave in LDS (in the
+// backward dout . o, and the stores of states and residuals), and two staging
+// waves bring the coming chunks' rows in: their loads are in flight for a whole
+// chunk, which no wave waits for.
 //
 // What bounds it is the sequence itself: a chunk takes a state wave some 4400
 // cycles (98 MFMAs of 16, 400 vector instructions between them, two LDS round
 // trips), 2.0 us; 2048 rows of 128 heads 66 us, 16384 rows 0.52 ms.  One wave
 // doing everything took 4.85 us a chunk.  The backward's recomputation writes
-// 56 KB a chunk and head beside it and is bound by memory (0.84 ms, 16384 rows).
+// 48 KB a chunk and head beside it and is bound by memory (0.81 ms, 16384 rows).
 //
 // Between two barriers the state waves work on chunk i, the output waves on
 // chunk i - 1 and the staging waves on k, v of chunk i + 1 and q, scores of
@@ -425,7 +426,6 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
   using TileN = typename Cf::TileN;
   using TileP = typename Cf::TileP;
   constexpr int LDN = TileN::LD, LDP = TileP::LD, XP = Cf::XP, PS = Cf::PS, XB = Cf::XBUF - 1;
-  constexpr int HALVES = sizeof(T) / 2;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   auto kbuf = [&](int i) { return reinterpret_cast<T*>(smem + (i & 1) * Cf::K_BYTES); };
   auto vbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_V + (i & 1) * Cf::V_BYTES); };
@@ -667,13 +667,6 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) p.e[(at * 4 + t) * 64 + l] = __builtin_bit_cast(uint4, ee[z][t]);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint4 u[2];
-              F::pieces(uf[z][q], u);
-#pragma unroll
-              for (int t = 0; t < HALVES; ++t) p.u[((at * HALVES + t) * 2 + q) * 64 + l] = u[t];
-            }
           }
         }
       }

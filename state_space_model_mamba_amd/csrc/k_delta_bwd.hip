@@ -495,31 +495,48 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
 // ---------------------------------------------------------------------------
 // k_delta_grad: dq and dk of one chunk and group, its heads one
 // after the other (dq and dk are sums over them, taken in registers in head
-// order); on small grids parts of the heads, added up by k_delta_parts.  Eight waves: 16 rows of the chunk times half of the N columns each.
-// All products end in the io type, so every operand is a single term (bf16: dq
-// and dk come out 2.9e-3 off, 1.7e-3 of it their own rounding).  Bound by the
-// 56 KB that a chunk and head brings in and by one block a CU (LDS): 0.63 ms at
-// 16384 rows of 128 heads of 64 x 128, 2.9 TB/s.
+// order); on small grids parts of the heads, added up by k_delta_parts.  Eight
+// waves: 16 rows of the chunk times half of the N columns each.
+// With bf16 io, u, dP and F enter as two terms, the states and dv as one: dq
+// and dk come out 1.8e-3 off, 1.7e-3 of it their own rounding.  (u alone in two
+// terms: 2.4e-3 and 0.74 ms; all in one: 2.9e-3 and 0.63 ms, the walk then 0.03
+// ms longer for the u it stored.)  Bound by the 64 KB that a chunk and head
+// brings in and by one block a CU (LDS, registers): 0.78 ms at 16384 rows of
+// 128 heads of 64 x 128, 2.7 TB/s.  Requesting the next head's rows as early as
+// its states spills: 1.18 ms.
 // ---------------------------------------------------------------------------
 constexpr int GTHR = 512;
+
+// four values to LDS: float32 as they are, bf16 as two terms, the second `apart` elements after the first
+template <typename T> __device__ __forceinline__ void store_terms(T* at, int apart, f32x4_t v) {
+  ssd::store4f<T>(at, v);
+  if constexpr (sizeof(T) == 2) {
+    f32x4_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = v[i] - ssd::Elem<T>::to_f(ssd::Elem<T>::from_f(v[i]));
+    ssd::store4f<T>(at + apart, r);
+  }
+}
 
 template <typename T, int NT> struct GradCfg {
   static constexpr int ND = 32 * NT;
   static constexpr int PSL = sizeof(T) == 2 ? 64 : 32;   // value columns staged at once
   using TileN = Tile<T, CH, ND, GTHR>;
   using TileP = Tile<T, CH, PSL, GTHR>;    // dout, dv
-  using TileU = SliceTile<T, PSL / SLICE, 2, GTHR>;    // u, a value column per row
+  static constexpr int LDU = CH + Vec16<T>::N;   // u, a value column per row
+  static constexpr size_t U_BYTES = sizeof(T) * PSL * LDU;
+  static constexpr int TERMS = sizeof(T) == 2 ? 2 : 1;   // of u, dP and F
   using TileS = SliceTile<T, PSL / SLICE, NT, GTHR>;   // S, dS, a value column per row
   using TileM = Tile<T, CH, CH, GTHR>;     // dP, F + F^T (over the tiles above)
   static constexpr size_t OFF_Q = sizeof(T) * TileN::LDS_ELEMS;
   static constexpr size_t OFF_DO = 2 * OFF_Q;
   static constexpr size_t OFF_DV = OFF_DO + sizeof(T) * TileP::LDS_ELEMS;
   static constexpr size_t OFF_U = OFF_DV + sizeof(T) * TileP::LDS_ELEMS;
-  static constexpr size_t OFF_S = OFF_U + sizeof(T) * TileU::LDS_ELEMS;
+  static constexpr size_t OFF_S = OFF_U + TERMS * U_BYTES;
   static constexpr size_t OFF_DS = OFF_S + sizeof(T) * TileS::LDS_ELEMS;
   static constexpr size_t END1 = OFF_DS + sizeof(T) * TileS::LDS_ELEMS;
-  static constexpr size_t OFF_F = OFF_DO + sizeof(T) * TileM::LDS_ELEMS;
-  static constexpr size_t END2 = OFF_F + sizeof(T) * TileM::LDS_ELEMS;
+  static constexpr size_t OFF_F = OFF_DO + TERMS * sizeof(T) * TileM::LDS_ELEMS;
+  static constexpr size_t END2 = OFF_F + TERMS * sizeof(T) * TileM::LDS_ELEMS;
   static constexpr size_t OFF_G = END1 > END2 ? END1 : END2;
   static constexpr size_t LDS = OFF_G + sizeof(float) * GATES * CH;
 };
@@ -527,7 +544,7 @@ template <typename T, int NT> struct GradCfg {
 template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_grad(Problem p) {
   using Cf = GradCfg<T, NT>;
   using F = Fr<T>;
-  constexpr int LDN = Cf::TileN::LD, LDP = Cf::TileP::LD, LDU = Cf::TileU::LD, LDS_ = Cf::TileS::LD, LDMT = Cf::TileM::LD;
+  constexpr int LDN = Cf::TileN::LD, LDP = Cf::TileP::LD, LDU = Cf::LDU, LDS_ = Cf::TileS::LD, LDMT = Cf::TileM::LD;
   constexpr int PSL = Cf::PSL;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   T* kt = reinterpret_cast<T*>(smem);
@@ -537,6 +554,7 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
   T* ut = reinterpret_cast<T*>(smem + Cf::OFF_U);
   T* st = reinterpret_cast<T*>(smem + Cf::OFF_S);
   T* dst = reinterpret_cast<T*>(smem + Cf::OFF_DS);
+  constexpr int TERMS = Cf::TERMS, UL = Cf::U_BYTES / sizeof(T), ML = Cf::TileM::LDS_ELEMS;   // from first terms to second
   T* dpm = reinterpret_cast<T*>(smem + Cf::OFF_DO);
   T* fm = reinterpret_cast<T*>(smem + Cf::OFF_F);
   float* gs = reinterpret_cast<float*>(smem + Cf::OFF_G);
@@ -579,18 +597,28 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
     for (int p0 = 0; p0 < p.P; p0 += PSL) {
       const int pcols = min(PSL, p.P - p0);
       typename Cf::TileP td, tv;
-      typename Cf::TileU tu;
+      // u = beta e from the residuals as the lanes hold them: piece t of lane (g, c) is column c's rows pair_col(t) + 8 g ..
+      constexpr int PER = 4 * 64, UIT = PSL / SLICE * PER / GTHR;
+      static_assert(PSL / SLICE * PER % GTHR == 0 && GTHR % PER == 0, "residuals");
+      f32x4_t tu[UIT];
+      const int urow = pair_col(tid % PER / 64) + 8 * g;
       const int64_t at = static_cast<int64_t>(ch.row) * hp + static_cast<int64_t>(h) * p.P + p0;
       td.load(static_cast<const T*>(p.dout) + at, hp, ch.len, pcols, tid);
       tv.load(static_cast<const T*>(p.dv) + at, hp, ch.len, pcols, tid);
       const int64_t first = sh * p.nsl + p0 / SLICE;
       const int nslices = min(PSL / SLICE, p.nsl - p0 / SLICE);
-      tu.load(p.u + first * HALVES * 2 * 64, HALVES * 2 * 64, nslices, tid);
+      const f32x4_t be = *reinterpret_cast<const f32x4_t*>(p.gates + sh * (GATES * CH) + GATE_BETA * CH + urow);
+#pragma unroll
+      for (int k = 0; k < UIT; ++k) {
+        tu[k] = zero4();
+        if (tid / PER + k * (GTHR / PER) < nslices) tu[k] = reinterpret_cast<const f32x4_t*>(p.e)[first * PER + tid + k * GTHR];
+      }
       const float tg = tid < GATES * CH ? p.gates[sh * (GATES * CH) + tid] : 0.f;
       __syncthreads();   // the previous head's last products are done
       td.store(dot, tid);
       tv.store(dvt, tid);
-      tu.store(ut, tid);
+#pragma unroll
+      for (int k = 0; k < UIT; ++k) store_terms<T>(ut + ((tid / PER + k * (GTHR / PER)) * SLICE + c) * LDU + urow, UL, be * tu[k]);
       ts.store(st, tid);
       tds.store(dst, tid);
       if (tid < GATES * CH) gs[tid] = tg;
@@ -600,22 +628,28 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
 #pragma unroll
       for (int ks = 0; ks < PSL / 32; ++ks) {
         const typename F::X xdo = F::load(dot + row * LDP + 32 * ks + 8 * g), xdv = F::load(dvt + row * LDP + 32 * ks + 8 * g);
-        const typename F::X xu = F::load_tr(ut + 16 * rt, LDU, 32 * ks + 8 * g);
+        typename F::X xu[TERMS];
+#pragma unroll
+        for (int u = 0; u < TERMS; ++u) xu[u] = F::load_tr(ut + u * UL + 16 * rt, LDU, 32 * ks + 8 * g);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int n0 = 16 * (half * NT + t);
           const typename F::X xs = F::load_tr(st + n0, LDS_, 32 * ks + 8 * g), xds = F::load_tr(dst + n0, LDS_, 32 * ks + 8 * g);
           x1[t] = mma(xs, xdo, x1[t]);
           x2[t] = mma(xs, xdv, x2[t]);
-          x3[t] = mma(xds, xu, x3[t]);
+#pragma unroll
+          for (int u = TERMS - 1; u >= 0; --u) x3[t] = mma(xds, xu[u], x3[t]);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int jt = 2 * half + t;
           if (jt <= rt) {
-            const typename F::X xj = F::load_tr(ut + 16 * jt, LDU, 32 * ks + 8 * g);
-            m1[t] = mma(xj, xdo, m1[t]);
-            m2[t] = mma(xj, xdv, m2[t]);
+#pragma unroll
+            for (int u = TERMS - 1; u >= 0; --u) {
+              const typename F::X xj = F::load_tr(ut + u * UL + 16 * jt, LDU, 32 * ks + 8 * g);
+              m1[t] = mma(xj, xdo, m1[t]);
+              m2[t] = mma(xj, xdv, m2[t]);
+            }
           }
         }
       }
@@ -639,28 +673,42 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
           const float dec = expf((ci - gs[GATE_C * CH + j]) + (cl - gs[GATE_CLO * CH + j]));
           if (j <= row) dp[r] = p.scale * (dec * m1[t][r]);
           if (j < row) {
-            const T f = ssd::Elem<T>::from_f(-dec * m2[t][r]);
-            fm[row * LDMT + j] = f;
-            fm[j * LDMT + row] = f;
+            float f = -dec * m2[t][r];
+#pragma unroll
+            for (int u = 0; u < TERMS; ++u) {
+              const T x = ssd::Elem<T>::from_f(f);
+              fm[u * ML + row * LDMT + j] = x;
+              fm[u * ML + j * LDMT + row] = x;
+              f -= ssd::Elem<T>::to_f(x);
+            }
           } else if (j == row) {
-            fm[row * LDMT + row] = ssd::Elem<T>::from_f(0.f);
+#pragma unroll
+            for (int u = 0; u < TERMS; ++u) fm[u * ML + row * LDMT + row] = ssd::Elem<T>::from_f(0.f);
           }
         }
       }
-      ssd::store4f<T>(dpm + row * LDMT + 16 * jt + 4 * g, dp);
+      store_terms<T>(dpm + row * LDMT + 16 * jt + 4 * g, ML, dp);
     }
     __syncthreads();
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      const typename F::X xp = F::load(dpm + row * LDMT + 32 * ks + 8 * g), xf = F::load(fm + row * LDMT + 32 * ks + 8 * g);
-      const typename F::X xpt = F::load_tr(dpm + 16 * rt, LDMT, 32 * ks + 8 * g);
+      typename F::X xp[TERMS], xf[TERMS], xpt[TERMS];
+#pragma unroll
+      for (int u = 0; u < TERMS; ++u) {
+        xp[u] = F::load(dpm + u * ML + row * LDMT + 32 * ks + 8 * g);
+        xf[u] = F::load(fm + u * ML + row * LDMT + 32 * ks + 8 * g);
+        xpt[u] = F::load_tr(dpm + u * ML + 16 * rt, LDMT, 32 * ks + 8 * g);
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int n0 = 16 * (half * NT + t);
         const typename F::X xk = F::load_tr(kt + n0, LDN, 32 * ks + 8 * g), xq = F::load_tr(qt + n0, LDN, 32 * ks + 8 * g);
-        dqa[t] = mma(xk, xp, dqa[t]);
-        dka[t] = mma(xq, xpt, dka[t]);
-        dka[t] = mma(xk, xf, dka[t]);
+#pragma unroll
+        for (int u = TERMS - 1; u >= 0; --u) {
+          dqa[t] = mma(xk, xp[u], dqa[t]);
+          dka[t] = mma(xq, xpt[u], dka[t]);
+          dka[t] = mma(xk, xf[u], dka[t]);
+        }
       }
     }
   }

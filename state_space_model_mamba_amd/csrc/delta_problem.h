@@ -33,7 +33,7 @@ struct Problem {
   int32_t* starts;   // (nseqs + 1) first rows, then (nseqs) the sequences longest first (seq_idx given)
   float* gates;      // (slots, H, GATES, 64)
   uint4* tf;         // (slots, H, FRAG_PIECES): T' - I, T' = (I + N diag(beta))^-1, rows in pair order
-  uint4* pf;         // the same of the causal scores, rows in order (bf16 forward: the first terms alone)
+  uint4* pf;         // the same of the causal scores, rows in order
   uint4* ttf;        // transposed (I + diag(beta) N)^-1 - I, rows in pair order (backward)
   uint4* ptf;        // transposed scores, rows in pair order (backward)
   uint4* e;          // (slots, H, nsl, 4, 64): the residuals, float32, accumulator layout (backward)

@@ -335,8 +335,7 @@ template <typename T, int NT, bool BWD> __global__ __launch_bounds__(256, BWD ? 
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[4 * y + r] = p.scale * (qk[z][y][r] * decay(hi, li, hj[r], lj[r], j0 + 4 * y + r <= i));
         }
-        if constexpr (BWD || sizeof(T) == 4) put(p.pf, f, v);
-        else F::store(reinterpret_cast<T*>(p.pf + sh * (FRAG_PIECES / 2) + f * 64 + l), F::round8(v));
+        put(p.pf, f, v);
         if constexpr (BWD) {
           const int j = perm_row(upper_t(f), c), i0 = 32 * upper_k(f) + 8 * g;
           const float hj = chi[j], lj = clo[j];
@@ -400,19 +399,15 @@ template <typename T, int NT, bool BWD, int NSW> struct WalkCfg {
   using K = ChunkRows<T, NT, HT>;
   // q and the scores through LDS, or (512-byte rows: no room) straight into the output waves' registers
   static constexpr bool QLDS = sizeof(T) * ND <= 256;
-  // terms of the entering states and the scores in o: one where o ends in bf16 (its error then is 2.4e-3, the
-  // output's own rounding 1.7e-3 of it), two for the float32 dout . o; the corrections always enter as two
-  static constexpr int XP = BWD || sizeof(T) == 4 ? 2 : 1;
-  static constexpr int PIECES = FRAG_PIECES / 2 * XP;   // of the scores
   static constexpr size_t N_BYTES = sizeof(T) * TileN::LDS_ELEMS, V_BYTES = sizeof(T) * TileP::LDS_ELEMS;
   static constexpr size_t K_BYTES = sizeof(T) * K::TileT::LDS_ELEMS;
   static constexpr size_t OFF_V = 2 * K_BYTES;
   static constexpr size_t OFF_Q = OFF_V + 2 * V_BYTES;
   static constexpr size_t OFF_P = OFF_Q + (QLDS ? 2 * N_BYTES : 0);
-  static constexpr size_t OFF_XS = OFF_P + (QLDS ? 2 * 16 * PIECES : 0);
+  static constexpr size_t OFF_XS = OFF_P + (QLDS ? 2 * 16 * FRAG_PIECES : 0);
   // what the state waves leave, twice where there is room: then nobody waits for the output waves to take it
   static constexpr int XBUF = QLDS && NSW == 2 ? 2 : 1;
-  static constexpr size_t OFF_XE = OFF_XS + XBUF * 16 * 64 * NSW * NT * XP;
+  static constexpr size_t OFF_XE = OFF_XS + XBUF * 16 * 64 * NSW * NT * 2;
   static constexpr size_t OFF_G = OFF_XE + XBUF * 16 * 64 * NSW * 4;
   // gates of the chunks in work: the staged one, the state waves' and (with one barrier) the output waves'
   static constexpr int GBUF = 2 * XBUF;
@@ -425,15 +420,15 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
   using F = Fr<T>;
   using TileN = typename Cf::TileN;
   using TileP = typename Cf::TileP;
-  constexpr int LDN = TileN::LD, LDP = TileP::LD, XP = Cf::XP, PS = Cf::PS, XB = Cf::XBUF - 1;
+  constexpr int LDN = TileN::LD, LDP = TileP::LD, PS = Cf::PS, XB = Cf::XBUF - 1;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   auto kbuf = [&](int i) { return reinterpret_cast<T*>(smem + (i & 1) * Cf::K_BYTES); };
   auto vbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_V + (i & 1) * Cf::V_BYTES); };
   auto qbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_Q + (i & 1) * Cf::N_BYTES); };
-  auto pbuf = [&](int i) { return reinterpret_cast<uint4*>(smem + Cf::OFF_P) + (i & 1) * Cf::PIECES; };
+  auto pbuf = [&](int i) { return reinterpret_cast<uint4*>(smem + Cf::OFF_P) + (i & 1) * FRAG_PIECES; };
   auto gbuf = [&](int i) { return reinterpret_cast<float*>(smem + Cf::OFF_G) + (i & (Cf::GBUF - 1)) * WALK_GATES * CH; };
   // from the state waves: the entering state's terms [wave][q][term][lane], and the residuals [wave][t][lane]
-  auto xs = [&](int i) { return reinterpret_cast<uint4*>(smem + Cf::OFF_XS) + (i & XB) * 64 * NSW * NT * XP; };
+  auto xs = [&](int i) { return reinterpret_cast<uint4*>(smem + Cf::OFF_XS) + (i & XB) * 64 * NSW * NT * 2; };
   auto xe = [&](int i) { return reinterpret_cast<f32x4_t*>(smem + Cf::OFF_XE) + (i & XB) * 64 * NSW * 4; };
 
   const int np = (p.P + PS - 1) / PS;
@@ -491,7 +486,7 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
         uint4 u[2];
         F::pieces(sf[q], u);
 #pragma unroll
-        for (int t = 0; t < XP; ++t) xs(i)[((w * NT + q) * XP + t) * 64 + l] = u[t];
+        for (int t = 0; t < 2; ++t) xs(i)[((w * NT + q) * 2 + t) * 64 + l] = u[t];
       }
       // r = v - exp(c) k S, rows in pair order; beside it the decay of S, and k's columns for the last product
       f32x4_t x[4];
@@ -622,7 +617,7 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
         }
       }
     };
-    uint4 us[NZ][NT][XP];
+    uint4 us[NZ][NT][2];
     f32x4_t ee[NZ][4], be[4];
     float in[4];
     auto take = [&](int i) {
@@ -631,7 +626,7 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
 #pragma unroll
-          for (int t = 0; t < XP; ++t) us[z][q][t] = xs(i)[(((NZ * ow + z) * NT + q) * XP + t) * 64 + l];
+          for (int t = 0; t < 2; ++t) us[z][q][t] = xs(i)[(((NZ * ow + z) * NT + q) * 2 + t) * 64 + l];
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) ee[z][t] = xe(i)[((NZ * ow + z) * 4 + t) * 64 + l];
@@ -684,26 +679,17 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
           if constexpr (Cf::QLDS) x = F::load(qt + (16 * t + c) * LDN + 32 * q + 8 * g);
           else x = xq[t][q];
 #pragma unroll
-          for (int z = 0; z < NZ; ++z) {
-            if constexpr (XP == 2) acc[z] = mma(F::from_pieces(us[z][q]), x, acc[z]);
-            else acc[z] = mma(__builtin_bit_cast(typename F::X, us[z][q][0]), x, acc[z]);
-          }
+          for (int z = 0; z < NZ; ++z) acc[z] = mma(F::from_pieces(us[z][q]), x, acc[z]);
         }
 #pragma unroll
         for (int z = 0; z < NZ; ++z) acc[z] *= in[t];
 #pragma unroll
         for (int ks = 0; ks <= (t >> 1); ++ks) {
-          if constexpr (XP == 2) {
-            typename F::S sc;
-            if constexpr (Cf::QLDS) sc = frag_at<T>(pt, lower_frag(t, ks));
-            else sc = pf.get<T>(lower_frag(t, ks));
+          typename F::S sc;
+          if constexpr (Cf::QLDS) sc = frag_at<T>(pt, lower_frag(t, ks));
+          else sc = pf.get<T>(lower_frag(t, ks));
 #pragma unroll
-            for (int z = 0; z < NZ; ++z) acc[z] = mma(uf[z][ks], sc, acc[z]);
-          } else {
-            const typename F::X sc = F::load(reinterpret_cast<const T*>(pt + lower_frag(t, ks) * 64 + l));
-#pragma unroll
-            for (int z = 0; z < NZ; ++z) acc[z] = mma(uf[z][ks], sc, acc[z]);
-          }
+          for (int z = 0; z < NZ; ++z) acc[z] = mma(uf[z][ks], sc, acc[z]);
         }
 #pragma unroll
         for (int z = 0; z < NZ; ++z) {
@@ -744,7 +730,7 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
   typename Cf::K::TileT tk;
   TileN tq;
   TileP tv;
-  Pieces<Cf::PIECES, Cf::HT> tp;
+  Pieces<FRAG_PIECES, Cf::HT> tp;
   float tg[GI];
   auto request_state = [&](int i) {
     const int64_t row = static_cast<int64_t>(CH) * i;
@@ -763,7 +749,7 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
   auto request_scores = [&](int i) {
     if constexpr (Cf::QLDS) {
       tq.load(qp + static_cast<int64_t>(CH) * i * p.q_sl, p.q_sl, length(i), p.N, ht);
-      tp.load(p.pf + slot_head(i) * Cf::PIECES, ht);
+      tp.load(p.pf + slot_head(i) * FRAG_PIECES, ht);
     }
   };
   auto stage_scores = [&](int i) {

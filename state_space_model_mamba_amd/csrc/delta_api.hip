@@ -17,9 +17,8 @@ int delta_check(const delta_shape* s) {
   if (s->headdim % vec || s->dstate % vec || s->headdim > 1024 || s->dstate > 128) return SSD_ERR_UNSUPPORTED_SHAPE;
   for (const int64_t st : {s->q_batch_stride, s->q_row_stride, s->k_batch_stride, s->k_row_stride, s->v_batch_stride, s->v_row_stride})
     if (st < 0 || st % vec) return SSD_ERR_UNSUPPORTED_SHAPE;
-  // eight rows are addressed by a 32-bit byte offset
   for (const int64_t st : {s->q_row_stride, s->k_row_stride, s->v_row_stride, s->nheads * s->headdim, s->ngroups * s->dstate})
-    if (st > (int64_t{1} << 26)) return SSD_ERR_UNSUPPORTED_SHAPE;
+    if (st > delta::MAX_ROW_STRIDE) return SSD_ERR_UNSUPPORTED_SHAPE;
   return SSD_OK;
 }
 

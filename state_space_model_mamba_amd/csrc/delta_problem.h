@@ -10,6 +10,8 @@ namespace delta {
 
 constexpr int SLICE = 16;   // value columns of a state wave
 constexpr int PAD = 32;     // the workspace's value columns are a multiple of this
+// the widest row stride of q, k and v, and row of the contiguous tensors, in elements (checked on the host)
+constexpr int64_t MAX_ROW_STRIDE = int64_t{1} << 26;
 
 struct Problem {
   // sizes

@@ -20,6 +20,9 @@
 // v_mfma_f32_16x16x4_f32.
 #pragma once
 
+#include <type_traits>
+
+#include "delta_problem.h"
 #include "ssd_device.h"
 #include "ssd_tiles.h"
 
@@ -268,10 +271,14 @@ template <typename T, int ROWS, int COLS, int NTHR, bool SWZ = false> struct Til
   static constexpr int LD = SWZ ? COLS : COLS + VEC;   // row pitch in LDS: 16 bytes of padding
   static constexpr int LDS_ELEMS = ROWS * LD;
   f32x4_t buf[IT];
-  // base: uniform; stride * ROWS elements span less than 2^31 bytes
+  // A lane's offset in its piece reaches over STEP rows: 32 bits hold it at the widest stride for up to 32 rows of bf16
+  // or 16 of float32 (the walks' tiles), not for the 64 that 512 threads take of rows of 128 bytes.
+  static constexpr bool WIDE = int64_t{STEP} * MAX_ROW_STRIDE * static_cast<int64_t>(sizeof(T)) > (int64_t{1} << 32);
+  typedef typename std::conditional<WIDE, uint64_t, uint32_t>::type Offset;
+  // base: uniform; stride <= MAX_ROW_STRIDE
   __device__ __forceinline__ void load(const T* base, int64_t stride, int nrows, int ncols, int tid) {
     const int r = tid / CV, cc = (tid % CV) * VEC;
-    const uint32_t off = static_cast<uint32_t>(r * static_cast<uint32_t>(stride) + cc) * static_cast<uint32_t>(sizeof(T));
+    const Offset off = (static_cast<Offset>(r) * static_cast<Offset>(stride) + static_cast<Offset>(cc)) * static_cast<Offset>(sizeof(T));
     const char* at = reinterpret_cast<const char*>(base);
     const int64_t step = STEP * stride * static_cast<int64_t>(sizeof(T));
     if (nrows >= ROWS && ncols >= COLS) {

@@ -32,9 +32,9 @@
  *
  * Values.  g is a log decay: g <= 0, -inf included (the state is dropped);
  * values below -104, where exp is zero in float32, count as -104.  States,
- * gates and every sum are float32; with bf16 io the products whose result
- * reaches a state, o or a gate's gradient take their float32 operands as two
- * bf16 terms (16 bits of mantissa), those of dq and dk as two or one.
+ * gates and every sum are float32; with bf16 io the products take their
+ * float32 operands as two bf16 terms (16 bits of mantissa), what is added to a
+ * state as three.
  * A NaN or an infinity in a row of q, k, v, g or beta may reach every row of
  * its sequence from the first of its chunk of 64 rows on (in the backward
  * every row), and no other sequence.

@@ -48,7 +48,7 @@ size_t place(Problem& p, int io, bool backward, char* base) {
     return r;
   };
   const size_t sh = static_cast<size_t>(p.nslots) * p.H, rows = static_cast<size_t>(p.rows);
-  const size_t nd = p.N <= 64 ? 64 : 128, io_size = io == SSD_IO_BF16 ? 2 : 4, frags = sh * delta::FRAG_PIECES * 16;
+  const size_t nd = p.N <= 64 ? 64 : 128, frags = sh * delta::FRAG_PIECES * 16;
   p.starts = reinterpret_cast<int32_t*>(take((2 * static_cast<size_t>(p.nseqs) + 1) * 4));
   p.gates = reinterpret_cast<float*>(take(sh * delta::GATES * delta::CH * 4));
   p.tf = reinterpret_cast<uint4*>(take(frags));
@@ -58,7 +58,8 @@ size_t place(Problem& p, int io, bool backward, char* base) {
     p.ptf = reinterpret_cast<uint4*>(take(frags));
     p.e = reinterpret_cast<uint4*>(take(sh * rows * delta::CH * 4));
     p.s = reinterpret_cast<uint4*>(take(sh * rows * nd * 4));
-    p.ds = reinterpret_cast<uint4*>(take(sh * rows * nd * io_size));
+    p.ds = reinterpret_cast<uint4*>(take(sh * rows * nd * 4));
+    if (io == SSD_IO_BF16) p.dvl = reinterpret_cast<uint4*>(take(sh * rows * delta::CH * 2));
     p.oo = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));
     p.vv = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));
     p.be = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));

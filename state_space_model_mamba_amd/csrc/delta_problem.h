@@ -39,9 +39,10 @@ struct Problem {
   uint4* ttf;        // transposed (I + diag(beta) N)^-1 - I, rows in pair order (backward)
   uint4* ptf;        // transposed scores, rows in pair order (backward)
   uint4* e;          // (slots, H, nsl, 4, 64): the residuals, float32, accumulator layout (backward)
-  // as the lanes hold them (delta_tiles.h), HALVES = 1 (bf16) or 2 (float32):
-  uint4* s;          // (slots, H, nsl, 2, NQ, 64): entering states, 2 bf16 terms or float32 (backward)
-  uint4* ds;         // (slots, H, nsl, HALVES, NQ, 64): gradient of the state after the chunk (backward)
+  // as the lanes hold them (delta_tiles.h), 2 bf16 terms or float32:
+  uint4* s;          // (slots, H, nsl, 2, NQ, 64): entering states (backward)
+  uint4* ds;         // (slots, H, nsl, 2, NQ, 64): gradient of the state after the chunk (backward)
+  uint4* dvl;        // (slots, H, nsl, 2, 64): second terms of dv, 8 rows of a column a piece (backward, bf16)
   float* oo;         // (slots, H, nsl, 64): dout . o over the slice's columns (backward)
   float* vv;         // (slots, H, nsl, 64): dv . v
   float* be;         // (slots, H, nsl, 64): Du . e

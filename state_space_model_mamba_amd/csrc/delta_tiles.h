@@ -111,6 +111,7 @@ template <> struct Fr<bf16_t> {
   static __device__ __forceinline__ S from_pieces(const uint4 (&u)[2]) {
     return S{__builtin_bit_cast(X, u[0]), __builtin_bit_cast(X, u[1])};
   }
+  static __device__ __forceinline__ S terms(X first, X second) { return S{first, second}; }
   static __device__ __forceinline__ void floats(const S& s, float (&v)[8]) {
     const uint4 h = __builtin_bit_cast(uint4, s.hi), l = __builtin_bit_cast(uint4, s.lo);
 #pragma unroll
@@ -224,6 +225,7 @@ __device__ __forceinline__ f32x4_t mma_term(const f32x8_t& a, const f32x8_t& b, 
 //
 // SLICES slices of such pieces as an LDS tile with a row for every value column and NQ * 32 values in it, by NTHR
 // threads; slices >= nslices are zero and not read.
+// (Float32: both halves.  bf16: one term, `base` at its first slice's.)
 template <typename T, int SLICES, int NQ, int NTHR> struct SliceTile {
   static constexpr int HALVES = sizeof(T) / 2, PER = HALVES * NQ * 64, NV = SLICES * PER, IT = (NV + NTHR - 1) / NTHR;
   static constexpr int VEC = Vec16<T>::N, LD = NQ * 32 + VEC, LDS_ELEMS = SLICES * 16 * LD;

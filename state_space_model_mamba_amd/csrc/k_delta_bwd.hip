@@ -38,8 +38,8 @@ namespace delta {
 //     row sums for the gates' gradients, and the stores,
 //   * two waves stage the coming chunks' rows in LDS.
 // Bound by memory: a chunk and head reads the states (32 KB), residuals (16 KB),
-// matrices (24 KB), v and dout and writes dS and dv (24 KB), 16384 rows of 128
-// heads of 64 x 128 in 1.0 ms; in one kind of wave alone it took 2.7 ms.
+// matrices (24 KB), v and dout and writes dS and dv (48 KB, in two terms), 16384
+// rows of 128 heads of 64 x 128 in 1.12 ms; in one kind of wave alone it took 2.7 ms.
 // ---------------------------------------------------------------------------
 template <typename T, int NT> struct RwalkCfg {
   static constexpr int ND = 32 * NT, NSW = 2, PS = SLICE * NSW, NST = 2, HT = 64 * NST, THREADS = 64 * (2 * NSW + 1 + NST);
@@ -326,7 +326,6 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
     // ---- the waves behind, one for each state wave: with the residuals, and the entering state of the chunk after
     // (for its inner product)
     const int z = w - NSW - 1, slice = ps * NSW + z;
-    constexpr int HALVES = sizeof(T) / 2;
     uint4 te[4], ss[NT][2], us[NT][2];
     f32x4_t du[4];
     auto request = [&](int i) {
@@ -393,11 +392,20 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
           *reinterpret_cast<f32x4_t*>(p.vv + at + pair_col(t) + 8 * g) = vv[t];
         }
       }
-      uint4* ds = p.ds + (slot_head(i) * p.nsl + slice) * HALVES * NT * 64 + l;
+      uint4* ds = p.ds + (slot_head(i) * p.nsl + slice) * 2 * NT * 64 + l;
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
 #pragma unroll
-        for (int t = 0; t < HALVES; ++t) ds[(t * NT + q) * 64] = us[q][t];
+        for (int t = 0; t < 2; ++t) ds[(t * NT + q) * 64] = us[q][t];
+      }
+      if constexpr (sizeof(T) == 2) {   // what dv's own rounding leaves
+        uint4* lo = p.dvl + (slot_head(i) * p.nsl + slice) * 2 * 64 + l;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float v[8];
+          pair8(du[2 * q], du[2 * q + 1], v);
+          lo[q * 64] = __builtin_bit_cast(uint4, F::split(v).lo);
+        }
       }
       // dv by rows, through v's place in LDS: 16 two-byte stores of four 32-byte stretches each would hold up the
       // memory pipeline
@@ -497,13 +505,13 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
 // after the other (dq and dk are sums over them, taken in registers in head
 // order); on small grids parts of the heads, added up by k_delta_parts.  Eight
 // waves: 16 rows of the chunk times half of the N columns each.
-// With bf16 io, u, dP and F enter as two terms, the states and dv as one: dq
-// and dk come out 1.8e-3 off, 1.7e-3 of it their own rounding.  (u alone in two
-// terms: 2.4e-3 and 0.74 ms; all in one: 2.9e-3 and 0.63 ms, the walk then 0.03
-// ms longer for the u it stored.)  Bound by the 64 KB that a chunk and head
-// brings in and by one block a CU (LDS, registers): 0.78 ms at 16384 rows of
-// 128 heads of 64 x 128, 2.7 TB/s.  Requesting the next head's rows as early as
-// its states spills: 1.18 ms.
+// With bf16 io every float32 value enters as two terms (S, dS, u, dv, dP, F):
+// dq and dk are their exact values rounded once (1.7e-3 off).  With S, dS and
+// dv as one term 6% of their values rounded otherwise (1.8e-3), and the kernel
+// took 0.79 ms.  Bound by the 104 KB that a chunk and head brings in and by one
+// block a CU (LDS, registers): 0.96 ms at 16384 rows of 128 heads of 64 x 128,
+// 3.5 TB/s.  The loops over the contraction stay loops: unrolled, their
+// operands spill (2.98 ms).
 // ---------------------------------------------------------------------------
 constexpr int GTHR = 512;
 
@@ -518,6 +526,13 @@ template <typename T> __device__ __forceinline__ void store_terms(T* at, int apa
   }
 }
 
+// 8 rows of a column as load_tr gives them, from both terms
+template <typename T> __device__ __forceinline__ typename Fr<T>::S load_tr_terms(const T* base, int apart, int ld, int row0) {
+  const typename Fr<T>::X x = Fr<T>::load_tr(base, ld, row0);
+  if constexpr (sizeof(T) == 2) return Fr<T>::terms(x, Fr<T>::load_tr(base + apart, ld, row0));
+  else return x;
+}
+
 template <typename T, int NT> struct GradCfg {
   static constexpr int ND = 32 * NT;
   static constexpr int PSL = sizeof(T) == 2 ? 64 : 32;   // value columns staged at once
@@ -525,16 +540,18 @@ template <typename T, int NT> struct GradCfg {
   using TileP = Tile<T, CH, PSL, GTHR>;    // dout, dv
   static constexpr int LDU = CH + Vec16<T>::N;   // u, a value column per row
   static constexpr size_t U_BYTES = sizeof(T) * PSL * LDU;
-  static constexpr int TERMS = sizeof(T) == 2 ? 2 : 1;   // of u, dP and F
+  static constexpr int TERMS = sizeof(T) == 2 ? 2 : 1;   // of the float32 values
+  using TileL = SliceTile<T, PSL / SLICE, CH / 32, GTHR>;   // dv's second terms, a value column per row
   using TileS = SliceTile<T, PSL / SLICE, NT, GTHR>;   // S, dS, a value column per row
   using TileM = Tile<T, CH, CH, GTHR>;     // dP, F + F^T (over the tiles above)
   static constexpr size_t OFF_Q = sizeof(T) * TileN::LDS_ELEMS;
   static constexpr size_t OFF_DO = 2 * OFF_Q;
   static constexpr size_t OFF_DV = OFF_DO + sizeof(T) * TileP::LDS_ELEMS;
-  static constexpr size_t OFF_U = OFF_DV + sizeof(T) * TileP::LDS_ELEMS;
+  static constexpr size_t OFF_DVL = OFF_DV + sizeof(T) * TileP::LDS_ELEMS;
+  static constexpr size_t OFF_U = OFF_DVL + (TERMS > 1 ? sizeof(T) * TileL::LDS_ELEMS : 0);
   static constexpr size_t OFF_S = OFF_U + TERMS * U_BYTES;
-  static constexpr size_t OFF_DS = OFF_S + sizeof(T) * TileS::LDS_ELEMS;
-  static constexpr size_t END1 = OFF_DS + sizeof(T) * TileS::LDS_ELEMS;
+  static constexpr size_t OFF_DS = OFF_S + TERMS * sizeof(T) * TileS::LDS_ELEMS;
+  static constexpr size_t END1 = OFF_DS + TERMS * sizeof(T) * TileS::LDS_ELEMS;
   static constexpr size_t OFF_F = OFF_DO + TERMS * sizeof(T) * TileM::LDS_ELEMS;
   static constexpr size_t END2 = OFF_F + TERMS * sizeof(T) * TileM::LDS_ELEMS;
   static constexpr size_t OFF_G = END1 > END2 ? END1 : END2;
@@ -551,10 +568,11 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
   T* qt = reinterpret_cast<T*>(smem + Cf::OFF_Q);
   T* dot = reinterpret_cast<T*>(smem + Cf::OFF_DO);
   T* dvt = reinterpret_cast<T*>(smem + Cf::OFF_DV);
+  T* dvl = reinterpret_cast<T*>(smem + Cf::OFF_DVL);
   T* ut = reinterpret_cast<T*>(smem + Cf::OFF_U);
   T* st = reinterpret_cast<T*>(smem + Cf::OFF_S);
   T* dst = reinterpret_cast<T*>(smem + Cf::OFF_DS);
-  constexpr int TERMS = Cf::TERMS, UL = Cf::U_BYTES / sizeof(T), ML = Cf::TileM::LDS_ELEMS;   // from first terms to second
+  constexpr int TERMS = Cf::TERMS, UL = Cf::U_BYTES / sizeof(T), SL = Cf::TileS::LDS_ELEMS, ML = Cf::TileM::LDS_ELEMS;   // from first terms to second
   T* dpm = reinterpret_cast<T*>(smem + Cf::OFF_DO);
   T* fm = reinterpret_cast<T*>(smem + Cf::OFF_F);
   float* gs = reinterpret_cast<float*>(smem + Cf::OFF_G);
@@ -577,14 +595,16 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
 #pragma unroll
   for (int t = 0; t < NT; ++t) dqa[t] = dka[t] = zero4();
 
-  constexpr int HALVES = sizeof(T) / 2;
   // the states of a head's slice are requested while the one before is worked on
-  typename Cf::TileS ts, tds;
+  typename Cf::TileS ts[TERMS], tds[TERMS];
   auto request = [&](int hh, int p0) {
     const int64_t first = (static_cast<int64_t>(slot) * p.H + grp * p.hpg + hh) * p.nsl + p0 / SLICE;
     const int nslices = min(PSL / SLICE, p.nsl - p0 / SLICE);
-    ts.load(p.s + first * 2 * NT * 64, 2 * NT * 64, nslices, tid);   // bf16: the first terms
-    tds.load(p.ds + first * HALVES * NT * 64, HALVES * NT * 64, nslices, tid);
+#pragma unroll
+    for (int u = 0; u < TERMS; ++u) {
+      ts[u].load(p.s + (first * 2 + u) * NT * 64, 2 * NT * 64, nslices, tid);
+      tds[u].load(p.ds + (first * 2 + u) * NT * 64, 2 * NT * 64, nslices, tid);
+    }
   };
   request(first_head, 0);
   for (int hh = first_head; hh < end_head; ++hh) {
@@ -613,43 +633,47 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
         tu[k] = zero4();
         if (tid / PER + k * (GTHR / PER) < nslices) tu[k] = reinterpret_cast<const f32x4_t*>(p.e)[first * PER + tid + k * GTHR];
       }
+      typename Cf::TileL tl;
+      if constexpr (TERMS > 1) tl.load(p.dvl + first * 2 * 64, 2 * 64, nslices, tid);
       const float tg = tid < GATES * CH ? p.gates[sh * (GATES * CH) + tid] : 0.f;
       __syncthreads();   // the previous head's last products are done
       td.store(dot, tid);
       tv.store(dvt, tid);
 #pragma unroll
       for (int k = 0; k < UIT; ++k) store_terms<T>(ut + ((tid / PER + k * (GTHR / PER)) * SLICE + c) * LDU + urow, UL, be * tu[k]);
-      ts.store(st, tid);
-      tds.store(dst, tid);
+      if constexpr (TERMS > 1) tl.store(dvl, tid);
+#pragma unroll
+      for (int u = 0; u < TERMS; ++u) {
+        ts[u].store(st + u * SL, tid);
+        tds[u].store(dst + u * SL, tid);
+      }
       if (tid < GATES * CH) gs[tid] = tg;
       __syncthreads();
       if (p0 + PSL < p.P) request(hh, p0 + PSL);
       else if (hh + 1 < end_head) request(hh + 1, 0);
-#pragma unroll
+#pragma unroll 1
       for (int ks = 0; ks < PSL / 32; ++ks) {
-        const typename F::X xdo = F::load(dot + row * LDP + 32 * ks + 8 * g), xdv = F::load(dvt + row * LDP + 32 * ks + 8 * g);
-        typename F::X xu[TERMS];
-#pragma unroll
-        for (int u = 0; u < TERMS; ++u) xu[u] = F::load_tr(ut + u * UL + 16 * rt, LDU, 32 * ks + 8 * g);
+        const int k0 = 32 * ks + 8 * g;
+        const typename F::X xdo = F::load(dot + row * LDP + k0);
+        typename F::S xdv, xu;
+        if constexpr (TERMS > 1) xdv = F::terms(F::load(dvt + row * LDP + k0), F::load_tr(dvl + 16 * rt, Cf::TileL::LD, k0));
+        else xdv = F::load(dvt + row * LDP + k0);
+        xu = load_tr_terms<T>(ut + 16 * rt, UL, LDU, k0);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int n0 = 16 * (half * NT + t);
-          const typename F::X xs = F::load_tr(st + n0, LDS_, 32 * ks + 8 * g), xds = F::load_tr(dst + n0, LDS_, 32 * ks + 8 * g);
+          const typename F::S xs = load_tr_terms<T>(st + n0, SL, LDS_, k0), xds = load_tr_terms<T>(dst + n0, SL, LDS_, k0);
           x1[t] = mma(xs, xdo, x1[t]);
           x2[t] = mma(xs, xdv, x2[t]);
-#pragma unroll
-          for (int u = TERMS - 1; u >= 0; --u) x3[t] = mma(xds, xu[u], x3[t]);
+          x3[t] = mma(xds, xu, x3[t]);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int jt = 2 * half + t;
           if (jt <= rt) {
-#pragma unroll
-            for (int u = TERMS - 1; u >= 0; --u) {
-              const typename F::X xj = F::load_tr(ut + u * UL + 16 * jt, LDU, 32 * ks + 8 * g);
-              m1[t] = mma(xj, xdo, m1[t]);
-              m2[t] = mma(xj, xdv, m2[t]);
-            }
+            const typename F::S xj = load_tr_terms<T>(ut + 16 * jt, UL, LDU, k0);
+            m1[t] = mma(xj, xdo, m1[t]);
+            m2[t] = mma(xj, xdv, m2[t]);
           }
         }
       }
@@ -690,7 +714,7 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
       store_terms<T>(dpm + row * LDMT + 16 * jt + 4 * g, ML, dp);
     }
     __syncthreads();
-#pragma unroll
+#pragma unroll 1
     for (int ks = 0; ks < 2; ++ks) {
       typename F::X xp[TERMS], xf[TERMS], xpt[TERMS];
 #pragma unroll

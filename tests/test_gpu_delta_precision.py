@@ -43,3 +43,15 @@ def test_o_is_rounded_once(b, L, H, P, G, N, lengths):
     o = delta.delta_fwd(*args(c), c["initial_states"], c["seq_idx"], nseqs=d["nseqs"])["o"]
     seq = None if d["seq_idx"] is None else d["seq_idx"].numpy()
     rounded_once(o, od.forward(*[f64(x) for x in args(d)], f64(d["initial_states"]), seq)["o"], N, "o")
+
+
+@pytest.mark.parametrize("b,L,H,P,G,N,lengths", SHAPES)
+def test_gradients_of_rows_are_rounded_once(b, L, H, P, G, N, lengths):
+    print(f"[case] gradients b={b} L={L} H={H} P={P} G={G} N={N}", flush=True)
+    d = make(b, L, H, P, G, N, "bf16", seed=41 + L, lengths=lengths, initial=True)
+    c = cuda(d)
+    g = delta.delta_bwd(*args(c), c["do"], c["initial_states"], c["seq_idx"], c["dfin"], nseqs=d["nseqs"])
+    seq = None if d["seq_idx"] is None else d["seq_idx"].numpy()
+    ref = od.backward(*[f64(x) for x in args(d)], f64(d["do"]), f64(d["initial_states"]), seq, f64(d["dfin"]))
+    for k in ("dq", "dk", "dv"):
+        rounded_once(g[k], ref[k], N, k)

@@ -34,7 +34,9 @@
  * values below -104, where exp is zero in float32, count as -104.  States,
  * gates and every sum are float32; with bf16 io the products take their
  * float32 operands as two bf16 terms (16 bits of mantissa), what is added to a
- * state as three.
+ * state as three.  dg_t is a sum of terms that all hold exp(g_t): its error is
+ * relative to them however strong the decay, and dg is zero where g counts
+ * as -104.
  * A NaN or an infinity in a row of q, k, v, g or beta may reach every row of
  * its sequence from the first of its chunk of 64 rows on (in the backward
  * every row), and no other sequence.

@@ -52,18 +52,16 @@ size_t place(Problem& p, int io, bool backward, char* base) {
   p.starts = reinterpret_cast<int32_t*>(take((2 * static_cast<size_t>(p.nseqs) + 1) * 4));
   p.gates = reinterpret_cast<float*>(take(sh * delta::GATES * delta::CH * 4));
   p.tf = reinterpret_cast<uint4*>(take(frags));
-  p.pf = reinterpret_cast<uint4*>(take(frags));
-  if (backward) {
+  if (!backward) {
+    p.pf = reinterpret_cast<uint4*>(take(frags));
+  } else {
     p.ttf = reinterpret_cast<uint4*>(take(frags));
     p.ptf = reinterpret_cast<uint4*>(take(frags));
     p.e = reinterpret_cast<uint4*>(take(sh * rows * delta::CH * 4));
     p.s = reinterpret_cast<uint4*>(take(sh * rows * nd * 4));
     p.ds = reinterpret_cast<uint4*>(take(sh * rows * nd * 4));
     if (io == SSD_IO_BF16) p.dvl = reinterpret_cast<uint4*>(take(sh * rows * delta::CH * 2));
-    p.oo = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));
-    p.vv = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));
     p.be = reinterpret_cast<float*>(take(sh * p.nsl * delta::CH * 4));
-    p.phi = reinterpret_cast<float*>(take(sh * p.nsl * 4));
     if (p.ns > 1) p.parts = reinterpret_cast<float*>(take(static_cast<size_t>(p.nslots) * p.G * p.ns * 2 * delta::CH * nd * 4));
   }
   return at;

@@ -35,7 +35,7 @@ struct Problem {
   int32_t* starts;   // (nseqs + 1) first rows, then (nseqs) the sequences longest first (seq_idx given)
   float* gates;      // (slots, H, GATES, 64)
   uint4* tf;         // (slots, H, FRAG_PIECES): T' - I, T' = (I + N diag(beta))^-1, rows in pair order
-  uint4* pf;         // the same of the causal scores, rows in order
+  uint4* pf;         // the same of the causal scores, rows in order (forward)
   uint4* ttf;        // transposed (I + diag(beta) N)^-1 - I, rows in pair order (backward)
   uint4* ptf;        // transposed scores, rows in pair order (backward)
   uint4* e;          // (slots, H, nsl, 4, 64): the residuals, float32, accumulator layout (backward)
@@ -43,10 +43,7 @@ struct Problem {
   uint4* s;          // (slots, H, nsl, 2, NQ, 64): entering states (backward)
   uint4* ds;         // (slots, H, nsl, 2, NQ, 64): gradient of the state after the chunk (backward)
   uint4* dvl;        // (slots, H, nsl, 2, 64): second terms of dv, 8 rows of a column a piece (backward, bf16)
-  float* oo;         // (slots, H, nsl, 64): dout . o over the slice's columns (backward)
-  float* vv;         // (slots, H, nsl, 64): dv . v
-  float* be;         // (slots, H, nsl, 64): Du . e
-  float* phi;        // (slots, H, nsl): <entering state, its gradient>
+  float* be;         // (slots, H, nsl, 64): Du . e over the slice's columns (backward)
   float* parts;      // (slots, G, ns, 2, 64, ND): the parts' dq and dk (ns > 1)
 };
 

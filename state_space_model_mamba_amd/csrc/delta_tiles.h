@@ -229,14 +229,17 @@ __device__ __forceinline__ f32x4_t mma_term(const f32x8_t& a, const f32x8_t& b, 
 template <typename T, int SLICES, int NQ, int NTHR> struct SliceTile {
   static constexpr int HALVES = sizeof(T) / 2, PER = HALVES * NQ * 64, NV = SLICES * PER, IT = (NV + NTHR - 1) / NTHR;
   static constexpr int VEC = Vec16<T>::N, LD = NQ * 32 + VEC, LDS_ELEMS = SLICES * 16 * LD;
+  static_assert(NTHR % PER == 0 && NV % NTHR == 0, "slices");
   f32x4_t buf[IT];
-  // base: the first slice; pitch: pieces from one slice to the next
+  // base: the first slice (uniform); pitch: pieces from one slice to the next.  A thread's pieces share their place in
+  // the slice: one 32-bit lane offset, and a uniform base per piece.
   __device__ __forceinline__ void load(const uint4* base, int pitch, int nslices, int tid) {
+    const uint32_t off = static_cast<uint32_t>(tid / PER * pitch + tid % PER) * 16u;
+    const char* at = reinterpret_cast<const char*>(base);
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
-      const int v = tid + k * NTHR, s = v / PER;
       buf[k] = zero4();
-      if ((NV % NTHR == 0 || v < NV) && s < nslices) buf[k] = reinterpret_cast<const f32x4_t*>(base)[s * pitch + v % PER];
+      if (tid / PER + k * (NTHR / PER) < nslices) buf[k] = *reinterpret_cast<const f32x4_t*>(at + static_cast<int64_t>(k * (NTHR / PER) * 16) * pitch + off);
     }
   }
   __device__ __forceinline__ void store(T* lds, int tid) const {

@@ -96,8 +96,8 @@ __global__ __launch_bounds__(ST_THR) void k_delta_starts(Problem p) {
 }
 
 // ---------------------------------------------------------------------------
-// k_delta_prep: T' (and for the backward the transposed (I + diag(beta) N)^-1
-// and the transposed scores) and the scores of one chunk, as the walks'
+// k_delta_prep: T' and the scores of one chunk (for the backward T', the
+// transposed (I + diag(beta) N)^-1 and the transposed scores), as the walks'
 // operand fragments, for up to HB heads of one group.
 //
 // q k^T and k k^T are the group's: they are taken once, from operands loaded
@@ -111,9 +111,9 @@ __global__ __launch_bounds__(ST_THR) void k_delta_starts(Problem p) {
 // T21 = -T22 A21 T11 with float32 MFMA tiles, in place in LDS.
 //
 // Bound by the instructions of a head (some 1000 a wave, a third of them the
-// substitution) and in the backward by its 48 KB of fragments: 256 chunks of
-// 128 heads of 64 x 128 take 0.29 ms (18 KB a chunk and head, 2.0 TB/s), in
-// the backward 0.52 ms (3.0 TB/s).
+// substitution) and in the backward by its 36 KB of fragments: 256 chunks of
+// 128 heads of 64 x 128 take 0.30 ms (24 KB a chunk and head, 2.6 TB/s), in
+// the backward 0.41 ms (2.9 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int LDM = 68;   // pitch of the float32 64 x 64 matrices
 
@@ -254,7 +254,7 @@ template <typename T, int NT, bool BWD> __global__ __launch_bounds__(256, BWD ? 
   auto lower_k = [](int f) { return f < 2 ? 0 : (f - 2) & 1; };
   auto upper_t = [](int f) { return f < 4 ? f >> 1 : f - 2; };
   auto upper_k = [](int f) { return f < 4 ? f & 1 : 1; };
-  f32x4_t kk[4], qk[SF][2], kq[BWD ? SF : 1][2];
+  f32x4_t kk[4], qk[SF][2];
   auto products = [&](auto whole) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) kk[t] = zero4();
@@ -270,17 +270,13 @@ template <typename T, int NT, bool BWD> __global__ __launch_bounds__(256, BWD ? 
     for (int z = 0; z < SF; ++z) {
       const int f = sw + SW * z;
       qk[z][0] = qk[z][1] = zero4();
-      if constexpr (BWD) kq[z][0] = kq[z][1] = zero4();
 #pragma unroll
       for (int ks = 0; ks < NT; ++ks) {
-        const typename F::X x = operand(qp, p.q_sl, 16 * lower_t(f) + c, ks, whole);
+        const typename F::X x = BWD ? operand(kp, p.k_sl, perm_row(upper_t(f), c), ks, whole) : operand(qp, p.q_sl, 16 * lower_t(f) + c, ks, whole);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) qk[z][y] = mma(operand(kp, p.k_sl, perm_row(2 * lower_k(f) + y, c), ks, whole), x, qk[z][y]);
-        if constexpr (BWD) {
-          const typename F::X u = operand(kp, p.k_sl, perm_row(upper_t(f), c), ks, whole);
-#pragma unroll
-          for (int y = 0; y < 2; ++y) kq[z][y] = mma(operand(qp, p.q_sl, perm_row(2 * upper_k(f) + y, c), ks, whole), u, kq[z][y]);
-        }
+        for (int y = 0; y < 2; ++y)
+          qk[z][y] = mma(BWD ? operand(qp, p.q_sl, perm_row(2 * upper_k(f) + y, c), ks, whole)
+                             : operand(kp, p.k_sl, perm_row(2 * lower_k(f) + y, c), ks, whole), x, qk[z][y]);
       }
     }
   };
@@ -327,26 +323,26 @@ template <typename T, int NT, bool BWD> __global__ __launch_bounds__(256, BWD ? 
       for (int z = 0; z < SF; ++z) {
         const int f = sw + SW * z;
         float v[8];
-        const int i = 16 * lower_t(f) + c, j0 = 32 * lower_k(f) + 8 * g;
-        const float hi = chi[i], li = clo[i];
+        if constexpr (!BWD) {
+          const int i = 16 * lower_t(f) + c, j0 = 32 * lower_k(f) + 8 * g;
+          const float hi = chi[i], li = clo[i];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const f32x4_t hj = load4(chi + j0 + 4 * y), lj = load4(clo + j0 + 4 * y);
+          for (int y = 0; y < 2; ++y) {
+            const f32x4_t hj = load4(chi + j0 + 4 * y), lj = load4(clo + j0 + 4 * y);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[4 * y + r] = p.scale * (qk[z][y][r] * decay(hi, li, hj[r], lj[r], j0 + 4 * y + r <= i));
-        }
-        put(p.pf, f, v);
-        if constexpr (BWD) {
+            for (int r = 0; r < 4; ++r) v[4 * y + r] = p.scale * (qk[z][y][r] * decay(hi, li, hj[r], lj[r], j0 + 4 * y + r <= i));
+          }
+        } else {
           const int j = perm_row(upper_t(f), c), i0 = 32 * upper_k(f) + 8 * g;
           const float hj = chi[j], lj = clo[j];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const f32x4_t ih = load4(chi + i0 + 4 * y), il = load4(clo + i0 + 4 * y);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[4 * y + r] = p.scale * (kq[z][y][r] * decay(ih[r], il[r], hj, lj, j <= i0 + 4 * y + r));
+            for (int r = 0; r < 4; ++r) v[4 * y + r] = p.scale * (qk[z][y][r] * decay(ih[r], il[r], hj, lj, j <= i0 + 4 * y + r));
           }
-          put(p.ptf, f, v);
         }
+        put(BWD ? p.ptf : p.pf, f, v);
       }
     }
     __syncthreads();
@@ -377,15 +373,15 @@ template <typename T, int NT, bool BWD> __global__ __launch_bounds__(256, BWD ? 
 //     k S -> r -> T' r -> S   (three products a chunk, nothing else).
 // Beside them output waves form the previous chunk's o from the entering
 // state and the residuals that the state waves leave in LDS (in the
-// backward dout . o, and the stores of states and residuals), and two staging
+// backward they store both for the later kernels instead), and two staging
 // waves bring the coming chunks' rows in: their loads are in flight for a whole
 // chunk, which no wave waits for.
 //
 // What bounds it is the sequence itself: a chunk takes a state wave some 4400
 // cycles (98 MFMAs of 16, 400 vector instructions between them, two LDS round
-// trips), 2.0 us; 2048 rows of 128 heads 66 us, 16384 rows 0.52 ms.  One wave
+// trips), 2.0 us; 2048 rows of 128 heads 68 us, 16384 rows 0.55 ms.  One wave
 // doing everything took 4.85 us a chunk.  The backward's recomputation writes
-// 48 KB a chunk and head beside it and is bound by memory (0.81 ms, 16384 rows).
+// 48 KB a chunk and head beside it in the same time (0.56 ms, 2.9 TB/s).
 //
 // Between two barriers the state waves work on chunk i, the output waves on
 // chunk i - 1 and the staging waves on k, v of chunk i + 1 and q, scores of
@@ -397,8 +393,8 @@ template <typename T, int NT, bool BWD, int NSW> struct WalkCfg {
   using TileN = Tile<T, CH, ND, HT>;
   using TileP = Tile<T, CH, PS, HT>;
   using K = ChunkRows<T, NT, HT>;
-  // q and the scores through LDS, or (512-byte rows: no room) straight into the output waves' registers
-  static constexpr bool QLDS = sizeof(T) * ND <= 256;
+  // q and the scores (forward) through LDS, or (512-byte rows: no room) straight into the output waves' registers
+  static constexpr bool QLDS = !BWD && sizeof(T) * ND <= 256;
   static constexpr size_t N_BYTES = sizeof(T) * TileN::LDS_ELEMS, V_BYTES = sizeof(T) * TileP::LDS_ELEMS;
   static constexpr size_t K_BYTES = sizeof(T) * K::TileT::LDS_ELEMS;
   static constexpr size_t OFF_V = 2 * K_BYTES;
@@ -406,7 +402,7 @@ template <typename T, int NT, bool BWD, int NSW> struct WalkCfg {
   static constexpr size_t OFF_P = OFF_Q + (QLDS ? 2 * N_BYTES : 0);
   static constexpr size_t OFF_XS = OFF_P + (QLDS ? 2 * 16 * FRAG_PIECES : 0);
   // what the state waves leave, twice where there is room: then nobody waits for the output waves to take it
-  static constexpr int XBUF = QLDS && NSW == 2 ? 2 : 1;
+  static constexpr int XBUF = BWD || (QLDS && NSW == 2) ? 2 : 1;
   static constexpr size_t OFF_XE = OFF_XS + XBUF * 16 * 64 * NSW * NT * 2;
   static constexpr size_t OFF_G = OFF_XE + XBUF * 16 * 64 * NSW * 4;
   // gates of the chunks in work: the staged one, the state waves' and (with one barrier) the output waves'
@@ -585,14 +581,36 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
     constexpr int NZ = Cf::NZ;
     const int ow = w - NSW;
     const int col0 = PS * ps + NZ * SLICE * ow, slice0 = ps * NSW + NZ * ow;
+    if constexpr (BWD) {
+      auto keep = [&](int i) {
+#pragma unroll
+        for (int z = 0; z < NZ; ++z) {
+          if (slice0 + z < p.nsl) {
+            const int64_t at = slot_head(i) * p.nsl + slice0 + z;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+              for (int q = 0; q < NT; ++q) p.s[((at * 2 + t) * NT + q) * 64 + l] = xs(i)[(((NZ * ow + z) * NT + q) * 2 + t) * 64 + l];
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) p.e[(at * 4 + t) * 64 + l] = __builtin_bit_cast(uint4, xe(i)[((NZ * ow + z) * 4 + t) * 64 + l]);
+          }
+        }
+      };
+      __syncthreads();
+      for (int i = 0; i < nchunk; ++i) {
+        if (i > 0) keep(i - 1);   // left twice: the state waves are on the other one
+        __syncthreads();
+      }
+      keep(nchunk - 1);
+      return;
+    }
     typename F::X xq[Cf::QLDS ? 1 : 4][NT];
     FragRegs pf;
-    typedef typename std::conditional<sizeof(T) == 2, uint2, uint4>::type Raw4;   // four values as they lie
-    Raw4 dox[NZ][4];
     auto request_out = [&](int i) {
-      const int len = length(i);
-      const int64_t row0 = static_cast<int64_t>(CH) * i;
       if constexpr (!Cf::QLDS) {
+        const int len = length(i);
+        const int64_t row0 = static_cast<int64_t>(CH) * i;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
 #pragma unroll
@@ -603,18 +621,6 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
           }
         }
         pf.request(p.pf + slot_head(i) * FRAG_PIECES);
-      }
-      if constexpr (BWD) {
-#pragma unroll
-        for (int z = 0; z < NZ; ++z) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int row = 16 * t + c, cc = col0 + SLICE * z + 4 * g;
-            dox[z][t] = Raw4{};
-            if (row < len && cc < p.P)
-              dox[z][t] = *reinterpret_cast<const Raw4*>(static_cast<const T*>(p.dout) + (s0 + row0 + row) * hp + static_cast<int64_t>(h) * p.P + cc);
-          }
-        }
       }
     };
     uint4 us[NZ][NT][2];
@@ -639,7 +645,6 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
     };
     auto out = [&](int i) {
       const int len = length(i);
-      const int64_t sh = slot_head(i);
       typename F::S uf[NZ][2];
 #pragma unroll
       for (int z = 0; z < NZ; ++z) {
@@ -648,21 +653,6 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
           float v[8];
           pair8(ee[z][2 * q] * be[2 * q], ee[z][2 * q + 1] * be[2 * q + 1], v);
           uf[z][q] = F::split(v);
-        }
-      }
-      if constexpr (BWD) {
-#pragma unroll
-        for (int z = 0; z < NZ; ++z) {
-          if (slice0 + z < p.nsl) {
-            const int64_t at = sh * p.nsl + slice0 + z;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-              for (int q = 0; q < NT; ++q) p.s[((at * 2 + t) * NT + q) * 64 + l] = us[z][q][t];
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) p.e[(at * 4 + t) * 64 + l] = __builtin_bit_cast(uint4, ee[z][t]);
-          }
         }
       }
       const T* qt = qbuf(i);
@@ -693,15 +683,9 @@ __global__ __launch_bounds__(64 * (NSW + (BWD && NSW == 2 ? 2 : NSW / 2) + 2)) _
         }
 #pragma unroll
         for (int z = 0; z < NZ; ++z) {
-          if constexpr (BWD) {
-            const f32x4_t d = acc[z] * ssd::load4f<T>(reinterpret_cast<const T*>(&dox[z][t]));
-            const float s = ssd::sum_kgroups((d[0] + d[1]) + (d[2] + d[3]));
-            if (g == 0 && slice0 + z < p.nsl) p.oo[(sh * p.nsl + slice0 + z) * CH + 16 * t + c] = s;
-          } else {
-            const int cc = col0 + SLICE * z + 4 * g;
-            if (16 * t + c < len && cc < p.P)
-              ssd::store4f<T>(static_cast<T*>(p.o) + (s0 + static_cast<int64_t>(CH) * i + 16 * t + c) * hp + static_cast<int64_t>(h) * p.P + cc, acc[z]);
-          }
+          const int cc = col0 + SLICE * z + 4 * g;
+          if (16 * t + c < len && cc < p.P)
+            ssd::store4f<T>(static_cast<T*>(p.o) + (s0 + static_cast<int64_t>(CH) * i + 16 * t + c) * hp + static_cast<int64_t>(h) * p.P + cc, acc[z]);
         }
       }
     };

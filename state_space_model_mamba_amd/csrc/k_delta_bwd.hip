@@ -12,13 +12,14 @@
 //     dk_j  = sum_{i>=j} dP_ij q_i + sum_i (F_ij + F_ji) k_i - exp(c_j) S dv_j + exp(c_last - c_j) dS u_j,
 //             F_ij = -G_ij dv_i . u_j  (j < i)
 //
-// The decay's gradient needs none of the products above once more: scaling
-// every row of a chunk's decay history is the same as scaling v and o, so
-//     dg_t - dg_{t+1} = dout_t . o_t - dv_t . v_t,
-// and at a chunk's first row dg is <S, dS_in>.  dg is that inner product, taken
-// at every chunk, less the row sums before t: no cancellation reaches further
-// than 64 rows.  What the sums miss the next chunk's inner product by is spread
-// over the rows, as their errors add up (dg 1.7 times nearer).
+// The decay of row t scales all that passes from before t to t and after:
+//     dg_t = sum_{i>=t>j} M_ij + sum_{i>=t} a_i + sum_{j<t} b_j + exp(c_last) <S, dS>,
+//     M_ij = dP_ij (q_i . k_j) + F_ij (k_i . k_j)                         (within the chunk)
+//     a_i  = exp(c_i) (scale q_i . S dout_i - k_i . S dv_i)               (from the entering state)
+//     b_j  = exp(c_last - c_j) k_j . dS u_j                               (to the state after)
+// Every term holds exp(g_t), so dg_t keeps its bits however strong the decay.  (dg_t - dg_{t+1} = dout_t . o_t -
+// dv_t . v_t is shorter, but a difference of terms that do not get smaller with exp(g_t): at g = -8 dg was 2e-2 off
+// with bf16 io, at -30 nothing of it was left.)
 #include "delta_problem.h"
 #include "delta_tiles.h"
 #include "ssd_bwd.h"
@@ -35,11 +36,11 @@ namespace delta {
 //   * one wave forms ahead what does not need dS, for chunk i - 1: the scores'
 //     part of du, and q^T dout,
 //   * a wave each follows behind with what Du gives, for chunk i + 1: dv, the
-//     row sums for the gates' gradients, and the stores,
+//     row sums for dbeta, and the stores,
 //   * two waves stage the coming chunks' rows in LDS.
-// Bound by memory: a chunk and head reads the states (32 KB), residuals (16 KB),
-// matrices (24 KB), v and dout and writes dS and dv (48 KB, in two terms), 16384
-// rows of 128 heads of 64 x 128 in 1.12 ms; in one kind of wave alone it took 2.7 ms.
+// Bound by memory: a chunk and head reads the residuals (16 KB), matrices (24 KB)
+// and dout (8 KB) and writes dS and dv (48 KB, in two terms), 16384 rows of 128
+// heads of 64 x 128 in 0.89 ms, 3.6 TB/s; in one kind of wave alone it took 2.7 ms.
 // ---------------------------------------------------------------------------
 template <typename T, int NT> struct RwalkCfg {
   static constexpr int ND = 32 * NT, NSW = 2, PS = SLICE * NSW, NST = 2, HT = 64 * NST, THREADS = 64 * (2 * NSW + 1 + NST);
@@ -51,8 +52,8 @@ template <typename T, int NT> struct RwalkCfg {
   static constexpr int KBUF = sizeof(T) * ND <= 256 ? 2 : 1;
   static constexpr size_t OFF_Q = KBUF * N_BYTES;
   static constexpr size_t OFF_DO = 2 * OFF_Q;
-  static constexpr size_t OFF_V = OFF_DO + 2 * P_BYTES;
-  static constexpr size_t OFF_D0 = OFF_V + 2 * P_BYTES;      // scores^T dout
+  static constexpr size_t OFF_V = OFF_DO + 2 * P_BYTES;      // dv on its way to its rows
+  static constexpr size_t OFF_D0 = OFF_V + P_BYTES;          // scores^T dout
   static constexpr size_t OFF_Q0 = OFF_D0 + 16 * 64 * NSW * 4;
   static constexpr size_t OFF_DU = OFF_Q0 + KBUF * 16 * 64 * NSW * 2 * NT;   // q^T dout, twice as k
   static constexpr size_t OFF_XS = OFF_DU + 16 * 64 * NSW * 4;
@@ -70,7 +71,6 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
   auto kbuf = [&](int i) { return reinterpret_cast<T*>(smem + (i & KB) * Cf::N_BYTES); };
   auto qbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_Q + (i & KB) * Cf::N_BYTES); };
   auto dobuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_DO + (i & 1) * Cf::P_BYTES); };
-  auto vbuf = [&](int i) { return reinterpret_cast<T*>(smem + Cf::OFF_V + (i & 1) * Cf::P_BYTES); };
   auto gbuf = [&](int i) { return reinterpret_cast<float*>(smem + Cf::OFF_G) + (i & 3) * RWALK_GATES * CH; };
   f32x4_t* xd0 = reinterpret_cast<f32x4_t*>(smem + Cf::OFF_D0);   // [wave][t][lane]
   auto xq0 = [&](int i) { return reinterpret_cast<f32x4_t*>(smem + Cf::OFF_Q0) + (i & KB) * 64 * NSW * 2 * NT; };   // [wave][j][lane]
@@ -225,20 +225,6 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
         }
       }
       __syncthreads();
-      // the first chunk's <entering state, its gradient>: the entering state is the initial state
-      float phi = 0.f;
-      if (p.h0 && col < p.P) {
-#pragma unroll
-        for (int j = 0; j < 2 * NT; ++j) {
-          const int n = pair_col(j) + 8 * g;
-          if (n < p.N) {
-            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p.h0 + state_at + n) * S[j];
-            phi += (v[0] + v[1]) + (v[2] + v[3]);
-          }
-        }
-      }
-      phi = ssd::wave_sum(phi);
-      if (l == 0) p.phi[slot_head(0) * p.nsl + ps * NSW + w] = phi;
     }
     if (p.dinit && col < p.P) {
 #pragma unroll
@@ -323,23 +309,14 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
   }
 
   if (w < 2 * NSW + 1) {
-    // ---- the waves behind, one for each state wave: with the residuals, and the entering state of the chunk after
-    // (for its inner product)
+    // ---- the waves behind, one for each state wave: with the residuals
     const int z = w - NSW - 1, slice = ps * NSW + z;
-    uint4 te[4], ss[NT][2], us[NT][2];
-    f32x4_t du[4];
+    T* vt = reinterpret_cast<T*>(smem + Cf::OFF_V) + SLICE * z;   // this wave's columns
+    f32x4_t te[4], us[NT][2], du[4];
     auto request = [&](int i) {
-      const uint4* e = p.e + (slot_head(i) * p.nsl + slice) * 4 * 64 + l;
+      const f32x4_t* e = reinterpret_cast<const f32x4_t*>(p.e) + (slot_head(i) * p.nsl + slice) * 4 * 64 + l;
 #pragma unroll
       for (int t = 0; t < 4; ++t) te[t] = e[t * 64];
-      if (i < last) {
-        const uint4* at = p.s + (slot_head(i + 1) * p.nsl + slice) * 2 * NT * 64 + l;
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          ss[q][0] = at[q * 64];
-          ss[q][1] = at[(NT + q) * 64];
-        }
-      }
     };
     auto take = [&]() {
 #pragma unroll
@@ -347,52 +324,30 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) us[q][t] = xs[((z * NT + q) * 2 + t) * 64 + l];
+        for (int t = 0; t < 2; ++t) us[q][t] = reinterpret_cast<const f32x4_t*>(xs)[((z * NT + q) * 2 + t) * 64 + l];
       }
     };
     auto behind = [&](int i) {
       const int len = length(i);
       const float* gs = gbuf(i);
-      T* vt = vbuf(i) + SLICE * z;   // this wave's columns of v, and then of dv
       const int64_t at = (slot_head(i) * p.nsl + slice) * CH;
-      if (i < last) {
-        float phi = 0.f;
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          float a[8], b[8];
-          F::floats(F::from_pieces(us[q]), a);
-          F::floats(F::from_pieces(ss[q]), b);
-#pragma unroll
-          for (int r = 0; r < 8; ++r) phi += a[r] * b[r];
-        }
-        phi = ssd::wave_sum(phi);
-        if (l == 0) p.phi[slot_head(i + 1) * p.nsl + slice] = phi;
-      }
-      f32x4_t be[4], vv[4];
+      f32x4_t be[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        be[t] = du[t] * __builtin_bit_cast(f32x4_t, te[t]);
-        const int row = pair_col(t) + 8 * g;
-        du[t] *= *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + row);   // dv
-        vv[t] = du[t] * F::load4_tr(vt, LDP, row);
+        be[t] = du[t] * te[t];
+        du[t] *= *reinterpret_cast<const f32x4_t*>(gs + GATE_BETA * CH + pair_col(t) + 8 * g);   // dv
       }
       if (i > 0) request(i - 1);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          be[t][r] = ssd::sum16(be[t][r]);
-          vv[t][r] = ssd::sum16(vv[t][r]);
-        }
+        for (int r = 0; r < 4; ++r) be[t][r] = ssd::sum16(be[t][r]);
       }
       if (c == 0) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          *reinterpret_cast<f32x4_t*>(p.be + at + pair_col(t) + 8 * g) = be[t];
-          *reinterpret_cast<f32x4_t*>(p.vv + at + pair_col(t) + 8 * g) = vv[t];
-        }
+        for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4_t*>(p.be + at + pair_col(t) + 8 * g) = be[t];
       }
-      uint4* ds = p.ds + (slot_head(i) * p.nsl + slice) * 2 * NT * 64 + l;
+      f32x4_t* ds = reinterpret_cast<f32x4_t*>(p.ds) + (slot_head(i) * p.nsl + slice) * 2 * NT * 64 + l;
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
 #pragma unroll
@@ -407,7 +362,7 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
           lo[q * 64] = __builtin_bit_cast(uint4, F::split(v).lo);
         }
       }
-      // dv by rows, through v's place in LDS: 16 two-byte stores of four 32-byte stretches each would hold up the
+      // dv by rows, through LDS: 16 two-byte stores of four 32-byte stretches each would hold up the
       // memory pipeline
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -442,12 +397,10 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
   const int pcols = min(PS, p.P - PS * ps);
   const T* kp = static_cast<const T*>(p.k) + row_offset(s0, p.L, p.k_sb, p.k_sl) + static_cast<int64_t>(grp) * p.N;
   const T* qp = static_cast<const T*>(p.q) + row_offset(s0, p.L, p.q_sb, p.q_sl) + static_cast<int64_t>(grp) * p.N;
-  const T* vp = static_cast<const T*>(p.v) + row_offset(s0, p.L, p.v_sb, p.v_sl) + static_cast<int64_t>(h) * p.P + PS * ps;
   TileN tk, tq;
-  TileP td, tv;
+  TileP td;
   float tg[GI];
   auto request_k = [&](int i) { tk.load(kp + static_cast<int64_t>(CH) * i * p.k_sl, p.k_sl, length(i), p.N, ht); };
-  auto request_v = [&](int i) { tv.load(vp + static_cast<int64_t>(CH) * i * p.v_sl, p.v_sl, length(i), pcols, ht); };
   // for the wave ahead: q, dout and the gates
   auto request_q = [&](int i) {
     const int64_t row = static_cast<int64_t>(CH) * i;
@@ -469,7 +422,6 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
   stage_q(last);
   if (last > 0) request_q(last - 1);
   if (KB && last > 0) request_k(last - 1);
-  request_v(last);
   __syncthreads();
   if (KB && last > 0) {
     stage_q(last - 1);
@@ -494,24 +446,25 @@ template <typename T, int NT> __global__ __launch_bounds__(64 * 7) __attribute__
       }
       if (i > 2) request_q(i - 3);
     }
-    tv.store(vbuf(i), ht);
-    if (i > 0) request_v(i - 1);
     __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
-// k_delta_grad: dq and dk of one chunk and group, its heads one
+// k_delta_grad: dq, dk and dg of one chunk and group, its heads one
 // after the other (dq and dk are sums over them, taken in registers in head
 // order); on small grids parts of the heads, added up by k_delta_parts.  Eight
 // waves: 16 rows of the chunk times half of the N columns each.
+// For dg a lane holds a row i of M for 8 columns j: the sums over j < t run
+// within the row, those over i >= t over the lanes that hold t, and what a row
+// has left of its column 32 (CUT_L) enters the rows' sums of the second half.
 // With bf16 io every float32 value enters as two terms (S, dS, u, dv, dP, F):
 // dq and dk are their exact values rounded once (1.7e-3 off).  With S, dS and
 // dv as one term 6% of their values rounded otherwise (1.8e-3), and the kernel
-// took 0.79 ms.  Bound by the 104 KB that a chunk and head brings in and by one
-// block a CU (LDS, registers): 0.96 ms at 16384 rows of 128 heads of 64 x 128,
-// 3.5 TB/s.  The loops over the contraction stay loops: unrolled, their
-// operands spill (2.98 ms).
+// took 0.79 ms without dg.  Bound by one block a CU (LDS, registers), whose
+// products and sums wait for each other at two barriers a head: 1.22 ms at
+// 16384 rows of 128 heads of 64 x 128 (104 KB a chunk and head, 2.8 TB/s), 0.96
+// without dg.
 // ---------------------------------------------------------------------------
 constexpr int GTHR = 512;
 
@@ -555,7 +508,11 @@ template <typename T, int NT> struct GradCfg {
   static constexpr size_t OFF_F = OFF_DO + TERMS * sizeof(T) * TileM::LDS_ELEMS;
   static constexpr size_t END2 = OFF_F + TERMS * sizeof(T) * TileM::LDS_ELEMS;
   static constexpr size_t OFF_G = END1 > END2 ? END1 : END2;
-  static constexpr size_t LDS = OFF_G + sizeof(float) * GATES * CH;
+  // for dg: a and b from both halves of N, the rows' sums of M left of column 32, M's sums at a column from each row
+  // tile, and <S, dS> from every wave
+  static constexpr int CUT_A = 0, CUT_B = CUT_A + 2 * CH, CUT_L = CUT_B + 2 * CH, CUT_M = CUT_L + CH, CUT_S = CUT_M + 4 * CH, CUTS = CUT_S + GTHR / 64;
+  static constexpr size_t OFF_CUT = OFF_G + sizeof(float) * GATES * CH;
+  static constexpr size_t LDS = OFF_CUT + sizeof(float) * CUTS;
 };
 
 template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_grad(Problem p) {
@@ -576,6 +533,7 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
   T* dpm = reinterpret_cast<T*>(smem + Cf::OFF_DO);
   T* fm = reinterpret_cast<T*>(smem + Cf::OFF_F);
   float* gs = reinterpret_cast<float*>(smem + Cf::OFF_G);
+  float* cut = reinterpret_cast<float*>(smem + Cf::OFF_CUT);
 
   const int slot = static_cast<int>(blockIdx.x), grp = static_cast<int>(blockIdx.y) / p.ns, part = static_cast<int>(blockIdx.y) % p.ns;
   const int first_head = part * p.hs, end_head = min(p.hpg, first_head + p.hs);   // of the group
@@ -591,6 +549,13 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
     tk.store(kt, tid);
     tq.store(qt, tid);
   }
+  // A lane's places are taken anew where they are used: the addresses made of them would be kept over the heads, and
+  // spill (their reloads then wait for the requests in flight: 2.7 ms instead of 1.2).
+  const int tid0 = tid, l0 = l;
+  auto anew = [](int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+  };
   f32x4_t dqa[NT], dka[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) dqa[t] = dka[t] = zero4();
@@ -598,6 +563,7 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
   // the states of a head's slice are requested while the one before is worked on
   typename Cf::TileS ts[TERMS], tds[TERMS];
   auto request = [&](int hh, int p0) {
+    const int tid = anew(tid0);
     const int64_t first = (static_cast<int64_t>(slot) * p.H + grp * p.hpg + hh) * p.nsl + p0 / SLICE;
     const int nslices = min(PSL / SLICE, p.nsl - p0 / SLICE);
 #pragma unroll
@@ -614,6 +580,7 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
 #pragma unroll
     for (int t = 0; t < NT; ++t) x1[t] = x2[t] = x3[t] = zero4();
     m1[0] = m1[1] = m2[0] = m2[1] = zero4();
+    float ssum = 0.f;   // <S, dS>
     for (int p0 = 0; p0 < p.P; p0 += PSL) {
       const int pcols = min(PSL, p.P - p0);
       typename Cf::TileP td, tv;
@@ -647,6 +614,19 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
         ts[u].store(st + u * SL, tid);
         tds[u].store(dst + u * SL, tid);
       }
+#pragma unroll
+      for (int k = 0; k < Cf::TileS::IT; ++k) {
+        if constexpr (TERMS > 1) {
+          float x[8], y[8];
+          F::floats(F::terms(__builtin_bit_cast(typename F::X, ts[0].buf[k]), __builtin_bit_cast(typename F::X, ts[1].buf[k])), x);
+          F::floats(F::terms(__builtin_bit_cast(typename F::X, tds[0].buf[k]), __builtin_bit_cast(typename F::X, tds[1].buf[k])), y);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) ssum += x[r] * y[r];
+        } else {
+          const f32x4_t x = ts[0].buf[k] * tds[0].buf[k];
+          ssum += (x[0] + x[1]) + (x[2] + x[3]);
+        }
+      }
       if (tid < GATES * CH) gs[tid] = tg;
       __syncthreads();
       if (p0 + PSL < p.P) request(hh, p0 + PSL);
@@ -678,19 +658,47 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
         }
       }
     }
+    const int l = anew(l0), g = l >> 4, c = l & 15, row = 16 * rt + c;
     const float in = gs[GATE_IN * CH + row], out = gs[GATE_OUT * CH + row];
+    float ca = 0.f, cb = 0.f;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      dqa[t] += (p.scale * in) * x1[t];
-      dka[t] += out * x3[t] - in * x2[t];
+      const int n = 16 * (half * NT + t) + 4 * g;
+      const f32x4_t kv = ssd::load4f<T>(kt + row * LDN + n), qv = ssd::load4f<T>(qt + row * LDN + n);
+      x1[t] *= p.scale * in;
+      x2[t] *= in;
+      x3[t] *= out;
+      dqa[t] += x1[t];
+      dka[t] += x3[t] - x2[t];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        ca += qv[r] * x1[t][r] - kv[r] * x2[t][r];
+        cb += kv[r] * x3[t][r];
+      }
     }
+    ca = ssd::sum_kgroups(ca);
+    cb = ssd::sum_kgroups(cb);
+    ssum = ssd::wave_sum(ssum);
     __syncthreads();
+    if (g == 0) {
+      cut[Cf::CUT_A + half * CH + row] = ca;
+      cut[Cf::CUT_B + half * CH + row] = cb;
+      if (c == 0) cut[Cf::CUT_S + w] = ssum;
+    }
+    float left = 0.f;   // the row's sum of M left of the tile
     const float ci = gs[GATE_C * CH + row], cl = gs[GATE_CLO * CH + row];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int jt = 2 * half + t;
-      f32x4_t dp = zero4();
+      f32x4_t dp = zero4(), m = zero4(), at_col = zero4();
       if (jt <= rt) {
+        f32x4_t qk = zero4(), kk = zero4();   // of rows i (columns) and j (rows), as m1 and m2
+#pragma unroll
+        for (int ks = 0; ks < NT; ++ks) {
+          const typename F::X kj = F::load(kt + (16 * jt + c) * LDN + 32 * ks + 8 * g);
+          qk = mma(kj, F::load(qt + row * LDN + 32 * ks + 8 * g), qk);
+          kk = mma(kj, F::load(kt + row * LDN + 32 * ks + 8 * g), kk);
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int j = 16 * jt + 4 * g + r;
@@ -698,6 +706,7 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
           if (j <= row) dp[r] = p.scale * (dec * m1[t][r]);
           if (j < row) {
             float f = -dec * m2[t][r];
+            m[r] = qk[r] * dp[r] + kk[r] * f;
 #pragma unroll
             for (int u = 0; u < TERMS; ++u) {
               const T x = ssd::Elem<T>::from_f(f);
@@ -711,9 +720,45 @@ template <typename T, int NT> __global__ __launch_bounds__(GTHR) void k_delta_gr
           }
         }
       }
+      if (jt <= rt) {
+        // the sums over the row's columns before j, and of those over the rows from j on
+        float by_g[4], before = left;
+        ssd::gather_kgroups((m[0] + m[1]) + (m[2] + m[3]), by_g);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          if (q < g) before += by_g[q];
+        left += (by_g[0] + by_g[1]) + (by_g[2] + by_g[3]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          at_col[r] = ssd::sum16(16 * jt + 4 * g + r <= row ? before : 0.f);
+          before += m[r];
+        }
+      }
+      if (c == 0) *reinterpret_cast<f32x4_t*>(cut + Cf::CUT_M + rt * CH + 16 * jt + 4 * g) = at_col;
       store_terms<T>(dpm + row * LDMT + 16 * jt + 4 * g, ML, dp);
     }
+    if (half == 0 && g == 0) cut[Cf::CUT_L + row] = left;
     __syncthreads();
+    if (w == (hh & 7)) {   // dg, row l: suffix sums of a and of what is left of column 32, prefix sums of b
+      float a = cut[Cf::CUT_A + l] + cut[Cf::CUT_A + CH + l], b = cut[Cf::CUT_B + l] + cut[Cf::CUT_B + CH + l];
+      float lower = l < 32 ? 0.f : cut[Cf::CUT_L + l];
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const float ad = __shfl_down(a, d), ld = __shfl_down(lower, d), bu = __shfl_up(b, d);
+        if (l + d < 64) {
+          a += ad;
+          lower += ld;
+        }
+        if (l >= d) b += bu;
+      }
+      b = __shfl_up(b, 1);
+      float sum = a + (l > 0 ? b : 0.f) + (l < 32 ? 0.f : lower), ss = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum += cut[Cf::CUT_M + q * CH + l];
+#pragma unroll
+      for (int q = 0; q < GTHR / 64; ++q) ss += cut[Cf::CUT_S + q];
+      if (l < ch.len) p.dg[(static_cast<int64_t>(ch.row) + l) * p.H + h] = sum + gs[GATE_IN * CH + CH - 1] * ss;
+    }
 #pragma unroll 1
     for (int ks = 0; ks < 2; ++ks) {
       typename F::X xp[TERMS], xf[TERMS], xpt[TERMS];
@@ -782,36 +827,18 @@ template <typename T, int NT> __global__ __launch_bounds__(256) void k_delta_par
 }
 
 // ---------------------------------------------------------------------------
-// k_delta_gates: dg and dbeta of one chunk, a wave per head: the slices' row
-// sums added in slice order, dg by a scan over the rows.
+// k_delta_gates: dbeta of one chunk, a wave per head: the slices' row sums added
+// in slice order.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void k_delta_gates(Problem p) {
   const int slot = static_cast<int>(blockIdx.x), h = static_cast<int>(blockIdx.y) * 4 + ssd::wave_id_s(), l = ssd::lane_id();
   const Chunk ch = chunk_of(p, slot);
   if (ch.len == 0 || h >= p.H) return;
   const int64_t sh = static_cast<int64_t>(slot) * p.H + h;
-  const bool more = ch.row + ch.len < seq_start(p, ch.seq + 1);   // another chunk of the sequence follows
-  float d = 0.f, b = 0.f, phi = 0.f, next = 0.f;
+  float b = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < p.nsl; ++s) {
-    d += p.oo[(sh * p.nsl + s) * CH + l] - p.vv[(sh * p.nsl + s) * CH + l];
-    b += p.be[(sh * p.nsl + s) * CH + l];
-    phi += p.phi[sh * p.nsl + s];
-    if (more) next += p.phi[(sh + p.H) * p.nsl + s];
-  }
-  float run = d;
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) {
-    const float o = __shfl_up(run, k);
-    if (l >= k) run += o;
-  }
-  // the next inner product: 0 past the last chunk, unless a final state's gradient came in (then it is not known)
-  const float miss = more || !p.dfinal ? next - (phi - __shfl(run, 63)) : 0.f;
-  if (l < ch.len) {
-    const int64_t at = (static_cast<int64_t>(ch.row) + l) * p.H + h;
-    p.dg[at] = phi - (run - d) + miss * (static_cast<float>(l) / static_cast<float>(ch.len));
-    p.dbeta[at] = b;
-  }
+  for (int s = 0; s < p.nsl; ++s) b += p.be[(sh * p.nsl + s) * CH + l];
+  if (l < ch.len) p.dbeta[(static_cast<int64_t>(ch.row) + l) * p.H + h] = b;
 }
 
 // ---------------------------------------------------------------------------

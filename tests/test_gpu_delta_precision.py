@@ -17,7 +17,7 @@ import torch
 
 from oracle import delta as od
 from state_space_model_mamba_amd import delta
-from tests.test_gpu_delta import args, cuda, f64, make
+from tests.test_gpu_delta import args, cuda, f64, make, tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,73 @@ def test_gradients_of_rows_are_rounded_once(b, L, H, P, G, N, lengths):
     ref = od.backward(*[f64(x) for x in args(d)], f64(d["do"]), f64(d["initial_states"]), seq, f64(d["dfin"]))
     for k in ("dq", "dk", "dv"):
         rounded_once(g[k], ref[k], N, k)
+
+
+# decays of a head, the same at every row: from next to none to one that leaves nothing in float32
+DECAYS = (0.0, -0.1, -1.0, -4.0, -8.0, -12.0, -30.0, -80.0)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("initial", [False, True])
+def test_dg_of_every_head_however_strong_its_decay(initial, io):
+    """dg_t is exp(g_t) times an inner product of the state before and a gradient after: its error is held against
+    each head's own dg, with the parity tests' bound for one head, not against the milder heads beside it."""
+    H, N = len(DECAYS), 64
+    d = make(1, 200, H, 32, 2, N, io, seed=51, initial=initial)
+    d["g"] = torch.tensor(DECAYS).expand(1, 200, H).contiguous()
+    c = cuda(d)
+    ref = od.backward(*[f64(x) for x in args(d)], f64(d["do"]), f64(d["initial_states"]), None, f64(d["dfin"]))["dg"]
+    dg = f64(delta.delta_bwd(*args(c), c["do"], c["initial_states"], None, c["dfin"])["dg"])
+    tol = tolerance(torch.float32, d["q"].dtype, N)
+    errs = [np.linalg.norm(dg[..., h] - ref[..., h]) / np.linalg.norm(ref[..., h]) for h in range(H)]
+    for h in range(H):
+        print(f"  {io} g = {DECAYS[h]}: dg {errs[h]:.2e} off (tolerance {tol:.1e})", flush=True)
+    assert max(errs) <= tol
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_dg_of_a_dropped_state_is_zero(io):
+    d = make(1, 150, 2, 24, 1, 40, io, seed=52, initial=True)
+    rows = [0, 17, 64, 65, 149]
+    d["g"][0, rows, 0] = -float("inf")
+    d["g"][0, rows, 1] = -500.0
+    c = cuda(d)
+    dg = delta.delta_bwd(*args(c), c["do"], c["initial_states"], None, c["dfin"])["dg"]
+    assert bool((dg[0, rows] == 0).all()), dg[0, rows]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_dg_of_single_rows_among_mild_ones(io):
+    """One strong decay here and there: those rows' dg is small beside their neighbours' and still their own."""
+    N = 64
+    d = make(1, 192, 2, 32, 1, N, io, seed=53, initial=True)
+    rows = [5, 63, 64, 100, 191]
+    d["g"][0, rows] = -9.0
+    c = cuda(d)
+    ref = od.backward(*[f64(x) for x in args(d)], f64(d["do"]), f64(d["initial_states"]), None, f64(d["dfin"]))["dg"][0, rows]
+    dg = f64(delta.delta_bwd(*args(c), c["do"], c["initial_states"], None, c["dfin"])["dg"])[0, rows]
+    err, tol = np.linalg.norm(dg - ref) / np.linalg.norm(ref), tolerance(torch.float32, d["q"].dtype, N)
+    print(f"  {io} rows of strong decay: dg {err:.2e} off (tolerance {tol:.1e})", flush=True)
+    assert err <= tol
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_dg_is_the_differences(io):
+    """dg against central differences of the oracle's loss in single gates, strong ones among them."""
+    d = make(1, 70, 1, 8, 1, 16, io, seed=54, initial=True)
+    d["g"][0, 40], d["g"][0, 66] = -6.0, -3.0
+    c = cuda(d)
+    dg = f64(delta.delta_bwd(*args(c), c["do"], c["initial_states"], None, c["dfin"])["dg"])
+    x, h0, h = [f64(t) for t in args(d)], f64(d["initial_states"]), 1e-4
+
+    def loss(row, step):
+        y = [t.copy() for t in x]
+        y[3][0, row, 0] += step
+        r = od.forward(*y, h0)
+        return (r["o"] * f64(d["do"])).sum() + (r["final_states"] * f64(d["dfin"])).sum()
+
+    for row in (0, 1, 30, 40, 63, 64, 66, 69):
+        up, down = loss(row, h), loss(row, -h)
+        # truncation h^2 / 6 of third derivatives no larger than the terms of the loss, cancellation 2^-52 |loss| / h
+        slack = h * h * max(abs(dg).max(), 1.0) + 2.0 ** -50 * (abs(up) + 1) / h
+        assert abs((up - down) / (2 * h) - dg[0, row, 0]) <= slack + 2 * tolerance(torch.float32, d["q"].dtype, 16) * np.abs(dg).max(), row

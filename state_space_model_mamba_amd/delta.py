@@ -149,7 +149,13 @@ def _inputs(what, q, k, v, g, beta, nseqs, scale) -> DeltaShape:
                *_check_strided(v, "v", io, (b, L, H, P), dev))
     ssd._check(g, "g", torch.float32, (b, L, H), dev)
     ssd._check(beta, "beta", torch.float32, (b, L, H), dev)
-    return _sized(b, L, H, P, G, N, nseqs, ssd.SSD_IO_BF16 if io == torch.bfloat16 else ssd.SSD_IO_F32, scale, strides)
+    return _sized(b, L, H, P, G, N, nseqs, ssd.SSD_IO_BF16 if io == torch.bfloat16 else ssd.SSD_IO_F32,
+                  None if scale is None else float(scale), strides)
+
+
+def _copy(shape: DeltaShape) -> DeltaShape:
+    """A shape for the caller to keep (_sized's is shared by all calls of its sizes)."""
+    return DeltaShape.from_buffer_copy(shape)
 
 
 def _nseqs(q, initial_states, seq_idx, nseqs) -> int:
@@ -203,7 +209,7 @@ def delta_fwd(q, k, v, g, beta, initial_states=None, seq_idx=None, scale: Option
                            _stream(dev))
     if rc:
         raise ssd.SsdError(rc, "delta_fwd")
-    return {"o": o, "final_states": final, "workspace": workspace, "shape": shape}
+    return {"o": o, "final_states": final, "workspace": workspace, "shape": _copy(shape)}
 
 
 def delta_bwd(q, k, v, g, beta, do, initial_states=None, seq_idx=None, d_final_states=None,
@@ -240,7 +246,7 @@ def delta_bwd(q, k, v, g, beta, do, initial_states=None, seq_idx=None, d_final_s
     if rc:
         raise ssd.SsdError(rc, "delta_bwd")
     out["workspace"] = workspace
-    out["shape"] = shape
+    out["shape"] = _copy(shape)
     return out
 
 
@@ -251,6 +257,7 @@ class GatedDeltaRule(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, beta, initial_states, seq_idx, scale, nseqs):
         ctx.set_materialize_grads(False)
+        scale = None if scale is None else float(scale)   # the backward's too, whatever a tensor holds by then
         r = delta_fwd(q, k, v, g, beta, initial_states, seq_idx, scale, nseqs, want_final_states=True)
         ctx.save_for_backward(q, k, v, g, beta, initial_states, seq_idx)
         ctx.scale, ctx.nseqs = scale, nseqs

@@ -158,7 +158,7 @@ class QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved):
         ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
-        ctx.args = (eps, norm, interleaved)
+        ctx.args = (float(eps), norm, interleaved)
         return qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved)
 
     @staticmethod

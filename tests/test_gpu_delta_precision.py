@@ -125,3 +125,25 @@ def test_dg_is_the_differences(io):
         # truncation h^2 / 6 of third derivatives no larger than the terms of the loss, cancellation 2^-52 |loss| / h
         slack = h * h * max(abs(dg).max(), 1.0) + 2.0 ** -50 * (abs(up) + 1) / h
         assert abs((up - down) / (2 * h) - dg[0, row, 0]) <= slack + 2 * tolerance(torch.float32, d["q"].dtype, 16) * np.abs(dg).max(), row
+
+
+def test_calls_do_not_share_what_they_return_or_were_given():
+    """A result's shape is the caller's own, and a scale given as a tensor counts as it is at the call."""
+    d = cuda(make(1, 70, 2, 16, 1, 16, "f32", seed=55))
+    want = delta.delta_fwd(*args(d))["o"]
+    for call in (lambda: delta.delta_fwd(*args(d)), lambda: delta.delta_bwd(*args(d), d["do"])):
+        r = call()
+        r["shape"].seqlen, r["shape"].scale = 1, 0.0
+        assert call()["shape"].seqlen == 70
+        assert torch.equal(delta.delta_fwd(*args(d))["o"], want)
+    scale = torch.tensor(0.5)
+    one = delta.delta_fwd(*args(d), scale=scale)["o"]
+    scale.mul_(2)
+    two = delta.delta_fwd(*args(d), scale=scale)["o"]
+    assert torch.equal(one, delta.delta_fwd(*args(d), scale=0.5)["o"]) and torch.equal(two, 2 * one)
+    leaves = [x.clone().requires_grad_(True) for x in args(d)]
+    o, _ = delta.gated_delta_rule(*leaves, scale=scale)
+    scale.zero_()
+    got = torch.autograd.grad(o, leaves, d["do"])
+    ref = delta.delta_bwd(*args(d), d["do"], scale=1.0)
+    assert all(torch.equal(a, ref[k]) for a, k in zip(got, ("dq", "dk", "dv", "dg", "dbeta")))

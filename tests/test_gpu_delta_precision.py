@@ -147,3 +147,35 @@ def test_calls_do_not_share_what_they_return_or_were_given():
     got = torch.autograd.grad(o, leaves, d["do"])
     ref = delta.delta_bwd(*args(d), d["do"], scale=1.0)
     assert all(torch.equal(a, ref[k]) for a, k in zip(got, ("dq", "dk", "dv", "dg", "dbeta")))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_what_is_added_to_a_state_keeps_float32(io):
+    """Every row of a chunk with a key (or query) direction of its own, so a state's columns are single products:
+    S[:, n] = beta_n exp(c_last - c_n) v_n, and backwards dS_in[:, n] = scale exp(c_n) dout_n for keys of zero.  With
+    |c| <= 2 the exponent's rounding is 2 * 2^-24 of the result, exp and the products' roundings and the operand's three
+    terms at most a dozen 2^-24 more: within 2^-20 (two terms would be off by up to 2^-16)."""
+    L = N = 64
+    d = make(1, L, 2, 32, 1, N, io, seed=56)
+    d["g"] = d["g"] * 0.1
+    gen = torch.Generator().manual_seed(57)
+    ways = torch.eye(N)[torch.randperm(N, generator=gen)].reshape(1, L, 1, N).to(d["k"].dtype)
+    c = d["g"].double().cumsum(1)
+    assert float(c.abs().max()) <= 2
+    at = ways[0, :, 0].argmax(-1)
+
+    def placed(rows):   # (L, H, P): row t in column at[t] of (1, H, P, N)
+        S = torch.zeros(1, 2, 32, N, dtype=torch.float64)
+        S[0][..., at] = rows.permute(1, 2, 0)
+        return S
+
+    def near(got, want):
+        got = got.double().cpu()
+        assert bool(((got - want).abs() <= 2.0 ** -20 * want.abs()).all()), ((got - want).abs() / want.abs()).max()
+
+    x = cuda(dict(d, q=torch.zeros_like(ways), k=ways))
+    near(delta.delta_fwd(*args(x), want_final_states=True)["final_states"],
+         placed(((d["beta"].double() * (c[:, -1:] - c).exp())[..., None] * d["v"].double())[0]))
+    x = cuda(dict(d, q=ways, k=torch.zeros_like(ways), initial_states=torch.zeros(1, 2, 32, N)))
+    near(delta.delta_bwd(*args(x), x["do"], x["initial_states"], scale=0.5)["d_initial_states"],
+         placed((0.5 * c.exp()[..., None] * d["do"].double())[0]))

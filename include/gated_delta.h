@@ -59,13 +59,13 @@ extern "C" {
 #endif
 
 typedef struct {
-  int64_t batch;    /* >= 1 */
+  int64_t batch;    /* >= 1; <= 65535 for delta_step */
   int64_t seqlen;   /* >= 1; batch * seqlen < 2^31 */
   int64_t nheads;   /* >= 1, <= 65535, multiple of ngroups */
   int64_t headdim;  /* P: multiple of 8 (bf16 io) or 4 (f32 io), <= 1024 */
   int64_t ngroups;  /* >= 1 */
   int64_t dstate;   /* N: multiple of 8 (bf16 io) or 4 (f32 io), <= 128 */
-  int64_t nseqs;    /* number of sequence starts; == batch without seq_idx */
+  int64_t nseqs;    /* number of sequence starts, 1 .. 65535; == batch without seq_idx */
   int64_t q_batch_stride, q_row_stride; /* elements, multiples of 8 (bf16) or 4 (f32); 0, 0: contiguous; */
   int64_t k_batch_stride, k_row_stride; /* row strides, nheads * headdim and ngroups * dstate <= 2^26 */
   int64_t v_batch_stride, v_row_stride;
@@ -73,7 +73,12 @@ typedef struct {
   int32_t io_dtype; /* SSD_IO_BF16 or SSD_IO_F32 */
 } delta_shape;
 
-/* Workspace bytes of delta_fwd (backward == 0) or delta_bwd (backward != 0). */
+/*
+ * Workspace bytes of delta_fwd (backward == 0) or delta_bwd (backward != 0):
+ * 26 KB for every head and chunk of 64 rows (a sequence has its own chunks),
+ * in the backward 38 KB and for every 64 value columns 57 (dstate <= 64) or 89
+ * KB: 0.87 and 4.27 GB at 16384 rows of 128 heads of 64 x 128.
+ */
 int delta_workspace_size(const delta_shape* shape, int backward, size_t* bytes);
 
 /*

@@ -67,7 +67,6 @@ template <> struct Fr<bf16_t> {
   }
   typedef ssd::s16x4_t X4;   // 4 rows of one column as they lie
   static __device__ __forceinline__ X4 load4_raw(const bf16_t* base, int ld, int row0) { return tr4<4>(base, ld, row0); }
-  static __device__ __forceinline__ f32x4_t load4_tr(const bf16_t* base, int ld, int row0) { return floats4(tr4<4>(base, ld, row0)); }
   static __device__ __forceinline__ f32x4_t floats4(X4 v) {
     f32x4_t f;
 #pragma unroll
@@ -103,7 +102,6 @@ template <> struct Fr<bf16_t> {
     s.lo = t.lo;
     return s;
   }
-  static __device__ __forceinline__ X hi(const S& s) { return s.hi; }
   static __device__ __forceinline__ void pieces(const S& s, uint4 (&u)[2]) {
     u[0] = __builtin_bit_cast(uint4, s.hi);
     u[1] = __builtin_bit_cast(uint4, s.lo);
@@ -120,7 +118,6 @@ template <> struct Fr<bf16_t> {
       v[2 * i + 1] = __uint_as_float((&h.x)[i] & 0xffff0000u) + __uint_as_float((&l.x)[i] & 0xffff0000u);
     }
   }
-  static __device__ __forceinline__ void store(bf16_t* p, X x) { *reinterpret_cast<X*>(p) = x; }
   static __device__ __forceinline__ void floats(X x, float (&v)[8]) {
     const uint4 h = __builtin_bit_cast(uint4, x);
 #pragma unroll
@@ -156,13 +153,11 @@ template <> struct Fr<float> {
     return x;
   }
   typedef f32x4_t X4;
-  static __device__ __forceinline__ X4 load4_raw(const float* base, int ld, int row0) { return load4_tr(base, ld, row0); }
   static __device__ __forceinline__ f32x4_t floats4(X4 v) { return v; }
-  static __device__ __forceinline__ f32x4_t load4_tr(const float* base, int ld, int row0) {
+  static __device__ __forceinline__ X4 load4_raw(const float* base, int ld, int row0) {
     const float* p = base + row0 * ld + (static_cast<int>(threadIdx.x) & 15);
     return f32x4_t{p[0], p[ld], p[2 * ld], p[3 * ld]};
   }
-  static __device__ __forceinline__ X round8(const float (&v)[8]) { return split(v); }
   static __device__ __forceinline__ S split(const float (&v)[8]) {
     S s;
 #pragma unroll
@@ -170,7 +165,6 @@ template <> struct Fr<float> {
     return s;
   }
   static __device__ __forceinline__ S3 split3(const float (&v)[8]) { return split(v); }
-  static __device__ __forceinline__ X hi(const S& s) { return s; }
   static __device__ __forceinline__ void pieces(const S& s, uint4 (&u)[2]) {
     u[0] = __builtin_bit_cast(uint4, f32x4_t{s[0], s[1], s[2], s[3]});
     u[1] = __builtin_bit_cast(uint4, f32x4_t{s[4], s[5], s[6], s[7]});
@@ -182,10 +176,6 @@ template <> struct Fr<float> {
   static __device__ __forceinline__ void floats(const S& s, float (&v)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = s[e];
-  }
-  static __device__ __forceinline__ void store(float* p, X x) {
-    *reinterpret_cast<f32x4_t*>(p) = f32x4_t{x[0], x[1], x[2], x[3]};
-    *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
   }
 };
 
@@ -227,7 +217,7 @@ __device__ __forceinline__ f32x4_t mma_term(const f32x8_t& a, const f32x8_t& b, 
 // threads; slices >= nslices are zero and not read.
 // (Float32: both halves.  bf16: one term, `base` at its first slice's.)
 template <typename T, int SLICES, int NQ, int NTHR> struct SliceTile {
-  static constexpr int HALVES = sizeof(T) / 2, PER = HALVES * NQ * 64, NV = SLICES * PER, IT = (NV + NTHR - 1) / NTHR;
+  static constexpr int HALVES = sizeof(T) / 2, PER = HALVES * NQ * 64, NV = SLICES * PER, IT = NV / NTHR;
   static constexpr int VEC = Vec16<T>::N, LD = NQ * 32 + VEC, LDS_ELEMS = SLICES * 16 * LD;
   static_assert(NTHR % PER == 0 && NV % NTHR == 0, "slices");
   f32x4_t buf[IT];
@@ -246,8 +236,7 @@ template <typename T, int SLICES, int NQ, int NTHR> struct SliceTile {
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
       const int v = tid + k * NTHR, r = v % PER, l = r & 63, q = (r >> 6) % NQ, half = (r >> 6) / NQ;
-      if (NV % NTHR == 0 || v < NV)
-        *reinterpret_cast<f32x4_t*>(lds + (v / PER * 16 + (l & 15)) * LD + 32 * q + 8 * (l >> 4) + 4 * half) = buf[k];
+      *reinterpret_cast<f32x4_t*>(lds + (v / PER * 16 + (l & 15)) * LD + 32 * q + 8 * (l >> 4) + 4 * half) = buf[k];
     }
   }
 };

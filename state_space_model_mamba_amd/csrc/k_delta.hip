@@ -379,7 +379,7 @@ template <typename T, int NT, bool BWD> __global__ __launch_bounds__(256, BWD ? 
 //
 // What bounds it is the sequence itself: a chunk takes a state wave some 4400
 // cycles (98 MFMAs of 16, 400 vector instructions between them, two LDS round
-// trips), 2.0 us; 2048 rows of 128 heads 68 us, 16384 rows 0.55 ms.  One wave
+// trips), 2.0 us; 2048 rows of 128 heads 70 us, 16384 rows 0.55 ms.  One wave
 // doing everything took 4.85 us a chunk.  The backward's recomputation writes
 // 48 KB a chunk and head beside it in the same time (0.56 ms, 2.9 TB/s).
 //
@@ -779,7 +779,9 @@ template <typename T, int NT, bool BWD, int NSW> int walk_of(const Problem& p, h
   return go(k_delta_walk<T, NT, BWD, NSW>, dim3(p.H * ((p.P + Cf::PS - 1) / Cf::PS), p.nseqs), Cf::THREADS, Cf::LDS, s, p);
 }
 // A CU holds one block (LDS).  Blocks of 32 value columns while they all fit the 256 CUs at once, of 64 above that
-// (twice the columns on each CU for the same staging).
+// (twice the columns on each CU for the same staging).  2048 rows of 128 x 64 columns (256 blocks of 32): 72 us with 32,
+// 105 with 64 (backward 72, 89); 144 x 64: 127 and 100 (124, 99); twice 128 x 64: 144 and 113 (145, 117).  float32
+// takes 32: in the backward 64 have no room in LDS (the forward alone would take 415 instead of 650 us at 144 x 64).
 template <typename T, int NT, bool BWD> int walk(const Problem& p, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
     if (p.P > 32 && static_cast<int64_t>(p.H) * (p.rows / PAD) * p.nseqs > 256) return walk_of<T, NT, BWD, 4>(p, s);

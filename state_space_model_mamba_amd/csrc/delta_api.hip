@@ -80,11 +80,12 @@ Problem problem(const delta_shape& s) {
   p.total = p.B * p.L;
   p.nslots = p.total / delta::CH + p.nseqs;
   // Several heads share the group's products while that leaves every CU four blocks: 32 chunks of 128 heads of 8
-  // groups take 109 us at one head a block, 53 at four; 256 chunks 793 us at one, 275 at eight.
+  // groups take 108 us at one head a block, 65 at four; 256 chunks 678 us at one, 296 at eight.
   p.hb = 1;
   while (p.hb < 8 && p.hb < p.hpg && static_cast<int64_t>(p.nslots) * p.H / (2 * p.hb) >= 1024) p.hb *= 2;
   // and the gradients' groups are cut where there are fewer chunks and groups than CUs: 32 chunks of 64 heads of one
-  // group take 275 us in one part, 51 in eight; from 256 blocks on one part is the faster (299 us at 256 chunks)
+  // group take 526 us in one part, 87 in eight; from 256 blocks on one part is the faster (256 chunks: 581 us, 654 in
+  // eight)
   p.ns = 1;
   while (p.ns < p.hpg && static_cast<int64_t>(p.nslots) * p.G * p.ns < 256) p.ns *= 2;
   p.hs = (p.hpg + p.ns - 1) / p.ns;

@@ -21,7 +21,8 @@ OBJDIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(PKG, "libssd_bwd.so")
 ARCH = "gfx950"
 SOURCES = ["k_prep.hip", "k_state.hip", "k_group.hip", "k_dbdc.hip", "k_grp.hip", "k_head.hip", "k_fwd.hip",
-           "ssd_api.hip", "k_conv.hip", "k_delta.hip", "k_delta_bwd.hip", "k_delta_step.hip", "delta_api.hip", "k_qk_norm.hip"]
+           "ssd_api.hip", "k_conv.hip", "k_delta.hip", "k_delta_bwd.hip", "k_delta_step.hip", "delta_api.hip", "k_qk_norm.hip",
+           "k_block_norm.hip", "k_linrec.hip", "k_linrec_bwd.hip", "k_linrec_step.hip", "linrec_api.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",

@@ -1,0 +1,252 @@
+"""ctypes binding of the gated linear recurrence of libssd_bwd.so (include/linear_recurrence.h).
+
+Argument marshalling only, as in ``ssd``; every arithmetic step runs in the
+library's kernels, and the calls raise if the library is missing or returns
+an error.
+
+``linrec_fwd`` / ``linrec_bwd`` run whole sequences, ``linear_recurrence``
+pairs them as an autograd function, ``linrec_step`` runs few tokens on a pool
+of states kept in memory (the states that ``linrec_fwd`` returns have its
+layout).
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+from typing import Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from state_space_model_mamba_amd import ssd
+from state_space_model_mamba_amd.block_norm import _io, _strided, _workspace
+from state_space_model_mamba_amd.delta import MAX_STEP_TOKENS, _gradient, _nseqs, _on, _stream
+
+GATES = {"log": 0, "sigmoid": 1, "decay": 2}
+INPUT_SCALES = {"one": 0, "complement": 1, "unit": 2}
+EXPORTED = ("linrec_fwd", "linrec_bwd", "linrec_step", "linrec_workspace_size", "linrec_chunks")
+
+
+class LinrecShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "seqlen", "channels", "nseqs", "x_batch_stride", "x_row_stride",
+                                               "g_batch_stride", "g_row_stride", "i_batch_stride", "i_row_stride")] +
+                [(n, ctypes.c_int32) for n in ("gate", "input_scale", "io_dtype", "reserved")])
+
+
+_lib = None
+
+
+def load_library():
+    """The shared library with the linrec entry points' argument types set (raises if it is not built)."""
+    global _lib
+    if _lib is None:
+        lib = ssd.load_library()
+        vp, sp, n = ctypes.c_void_p, ctypes.POINTER(LinrecShape), ctypes.c_size_t
+        lib.linrec_chunks.restype = ctypes.c_int
+        lib.linrec_chunks.argtypes = [sp, ctypes.POINTER(ctypes.c_int64)]
+        lib.linrec_workspace_size.restype = ctypes.c_int
+        lib.linrec_workspace_size.argtypes = [sp, ctypes.c_int, ctypes.POINTER(n)]
+        lib.linrec_fwd.restype = ctypes.c_int
+        lib.linrec_fwd.argtypes = [sp] + [vp] * 10 + [n, vp]
+        lib.linrec_bwd.restype = ctypes.c_int
+        lib.linrec_bwd.argtypes = [sp] + [vp] * 15 + [n, vp]
+        lib.linrec_step.restype = ctypes.c_int
+        lib.linrec_step.argtypes = [sp] + [vp] * 5 + [ctypes.c_int64] + [vp] * 3
+        _lib = lib
+    return _lib
+
+
+def make_shape(batch, seqlen, channels, nseqs, gate="sigmoid", input_scale="one", io_dtype=ssd.SSD_IO_BF16,
+               strides=(0, 0, 0, 0, 0, 0)) -> LinrecShape:
+    gate = GATES[gate] if isinstance(gate, str) else int(gate)
+    input_scale = INPUT_SCALES[input_scale] if isinstance(input_scale, str) else int(input_scale)
+    return LinrecShape(batch, seqlen, channels, nseqs, *strides, gate, input_scale, io_dtype, 0)
+
+
+def chunks(shape: LinrecShape) -> int:
+    """Rows of chunk_states."""
+    n = ctypes.c_int64(0)
+    rc = load_library().linrec_chunks(ctypes.byref(shape), ctypes.byref(n))
+    if rc:
+        raise ssd.SsdError(rc, "linrec_chunks")
+    return n.value
+
+
+def workspace_size(shape: LinrecShape, backward: bool = False) -> int:
+    """Bytes of workspace linrec_fwd, or with ``backward`` linrec_bwd, needs."""
+    n = ctypes.c_size_t(0)
+    rc = load_library().linrec_workspace_size(ctypes.byref(shape), int(bool(backward)), ctypes.byref(n))
+    if rc:
+        raise ssd.SsdError(rc, "linrec_workspace_size")
+    return n.value
+
+
+@functools.lru_cache(maxsize=256)
+def _sized(*sizes) -> tuple[LinrecShape, int, int, int]:
+    """make_shape, its workspace sizes and its chunks, kept per sizes (callers read them only)."""
+    shape = make_shape(*sizes)
+    return shape, workspace_size(shape), workspace_size(shape, True), chunks(shape)
+
+
+def _inputs(what, x, g, in_gate, decay, nseqs, gate, input_scale):
+    dev, io = x.device, x.dtype
+    if dev.type != "cuda":
+        raise ValueError(f"{what} runs on a HIP device; got tensors on {dev}")
+    if io not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"unsupported io dtype {io}")
+    if gate not in GATES:
+        raise ValueError(f"gate is one of {sorted(GATES)}; got {gate!r}")
+    if input_scale not in INPUT_SCALES:
+        raise ValueError(f"input_scale is one of {sorted(INPUT_SCALES)}; got {input_scale!r}")
+    if x.dim() != 3:
+        raise ValueError("x, g and in_gate are (batch, seqlen, channels)")
+    b, L, C = x.shape
+    strides = (*_strided(x, "x", io, (b, L, C), dev),
+               *_strided(g, "g", torch.float32 if gate == "log" else io, (b, L, C), dev),
+               *_strided(in_gate, "in_gate", io, (b, L, C), dev))
+    if (gate == "decay") != (decay is not None):
+        raise ValueError('decay goes with gate="decay"')
+    ssd._check(decay, "decay", torch.float32, (C,), dev)
+    return _sized(b, L, C, nseqs, gate, input_scale, _io(io), strides)
+
+
+def linrec_fwd(x, g, in_gate=None, decay=None, initial_states=None, seq_idx=None, gate: str = "sigmoid",
+               input_scale: str = "one", nseqs: Optional[int] = None, want_final_states: bool = False,
+               want_chunk_states: bool = False, workspace: Optional[torch.Tensor] = None) -> dict:
+    """The gated linear recurrence over whole sequences (include/linear_recurrence.h): h_t = a_t h_{t-1} + m_t u_t.
+
+    x: (b, L, C) in bf16 or fp32; u is x, or x * sigmoid(in_gate).  gate: "log" (a = exp(g), g fp32), "sigmoid"
+    (a = sigmoid(g)) or "decay" (a = exp(decay * sigmoid(g)), decay (C) fp32, <= 0); input_scale: "one" (m = 1),
+    "complement" (1 - a) or "unit" (sqrt(1 - a^2)).  x, g and in_gate have one dtype but for g with "log", and may be
+    slices of wider rows.  initial_states: (S, C) fp32 or None, seq_idx: (b, L) int32 or None; ``nseqs`` is needed
+    only when seq_idx is given without initial_states.  Returns a dict with y (like x, contiguous), final_states
+    ((S, C) fp32, or None) and chunk_states (for linrec_bwd, or None).
+    """
+    S = _nseqs(x, initial_states, seq_idx, nseqs)
+    shape, nbytes, _, n = _inputs("linrec_fwd", x, g, in_gate, decay, S, gate, input_scale)
+    dev = x.device
+    b, L, C = x.shape
+    ssd._check(initial_states, "initial_states", torch.float32, (S, C), dev)
+    ssd._check(seq_idx, "seq_idx", torch.int32, (b, L), dev)
+    workspace = _workspace(workspace, nbytes, dev)
+    out = {"y": torch.empty((b, L, C), dtype=x.dtype, device=dev),
+           "final_states": torch.empty((S, C), dtype=torch.float32, device=dev) if want_final_states else None,
+           "chunk_states": torch.empty((n, C), dtype=torch.float32, device=dev) if want_chunk_states else None}
+    lib = load_library()
+    with _on(dev):
+        rc = lib.linrec_fwd(ctypes.byref(shape), ssd._ptr(x), ssd._ptr(g), ssd._ptr(in_gate), ssd._ptr(decay),
+                            ssd._ptr(initial_states), ssd._ptr(seq_idx), ssd._ptr(out["y"]),
+                            ssd._ptr(out["final_states"]), ssd._ptr(out["chunk_states"]), ssd._ptr(workspace),
+                            workspace.numel() * workspace.element_size(), _stream(dev))
+    if rc:
+        raise ssd.SsdError(rc, "linrec_fwd")
+    return out
+
+
+def linrec_bwd(x, g, in_gate, decay, dy, initial_states=None, seq_idx=None, d_final_states=None, chunk_states=None,
+               gate: str = "sigmoid", input_scale: str = "one", nseqs: Optional[int] = None,
+               want_ddecay: bool = True, want_d_initial_states: bool = True,
+               workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of sum(dy * y) + sum(d_final_states * final_states) of linrec_fwd, from its inputs.
+
+    ``chunk_states``: as linrec_fwd returned them for the same inputs, or None (they are formed again).  Returns a
+    dict with dx, dg, d_in_gate (like the inputs, contiguous; None without in_gate), ddecay ((C) fp32, or None) and
+    d_initial_states ((S, C) fp32, or None).
+    """
+    S = _nseqs(x, initial_states, seq_idx, nseqs)
+    shape, _, nbytes, n = _inputs("linrec_bwd", x, g, in_gate, decay, S, gate, input_scale)
+    dev = x.device
+    b, L, C = x.shape
+    ssd._check(dy, "dy", x.dtype, (b, L, C), dev)
+    ssd._check(initial_states, "initial_states", torch.float32, (S, C), dev)
+    ssd._check(d_final_states, "d_final_states", torch.float32, (S, C), dev)
+    ssd._check(seq_idx, "seq_idx", torch.int32, (b, L), dev)
+    ssd._check(chunk_states, "chunk_states", torch.float32, (n, C), dev)
+    workspace = _workspace(workspace, nbytes, dev)
+    out = {"dx": torch.empty((b, L, C), dtype=x.dtype, device=dev),
+           "dg": torch.empty((b, L, C), dtype=g.dtype, device=dev),
+           "d_in_gate": None if in_gate is None else torch.empty((b, L, C), dtype=x.dtype, device=dev),
+           "ddecay": torch.empty((C,), dtype=torch.float32, device=dev) if decay is not None and want_ddecay else None,
+           "d_initial_states": (torch.empty((S, C), dtype=torch.float32, device=dev)
+                                if want_d_initial_states else None)}
+    lib = load_library()
+    with _on(dev):
+        rc = lib.linrec_bwd(ctypes.byref(shape), ssd._ptr(x), ssd._ptr(g), ssd._ptr(in_gate), ssd._ptr(decay),
+                            ssd._ptr(initial_states), ssd._ptr(seq_idx), ssd._ptr(chunk_states), ssd._ptr(dy),
+                            ssd._ptr(d_final_states), ssd._ptr(out["dx"]), ssd._ptr(out["dg"]),
+                            ssd._ptr(out["d_in_gate"]), ssd._ptr(out["ddecay"]), ssd._ptr(out["d_initial_states"]),
+                            ssd._ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev))
+    if rc:
+        raise ssd.SsdError(rc, "linrec_bwd")
+    return out
+
+
+class LinearRecurrence(torch.autograd.Function):
+    """linrec_fwd paired with linrec_bwd: besides the inputs, the float32 states between the chunks are kept."""
+
+    @staticmethod
+    def forward(ctx, x, g, in_gate, decay, initial_states, seq_idx, gate, input_scale, nseqs):
+        ctx.set_materialize_grads(False)
+        keep = any(ctx.needs_input_grad[:5])
+        r = linrec_fwd(x, g, in_gate, decay, initial_states, seq_idx, gate, input_scale, nseqs, want_final_states=True,
+                       want_chunk_states=keep)
+        ctx.save_for_backward(x, g, in_gate, decay, initial_states, seq_idx, r["chunk_states"])
+        ctx.args = (gate, input_scale, nseqs)
+        return r["y"], r["final_states"]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, d_final):
+        x, g, in_gate, decay, h0, seq_idx, states = ctx.saved_tensors
+        if dy is None and d_final is None:
+            return (None,) * 9
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _gradient(dy)
+        need = ctx.needs_input_grad
+        r = linrec_bwd(x, g, in_gate, decay, dy, h0, seq_idx, None if d_final is None else _gradient(d_final), states,
+                       *ctx.args, want_ddecay=need[3], want_d_initial_states=h0 is not None and need[4])
+        return r["dx"], r["dg"], r["d_in_gate"], r["ddecay"], r["d_initial_states"], None, None, None, None
+
+
+def linear_recurrence(x, g, in_gate=None, decay=None, initial_states=None, seq_idx=None, gate: str = "sigmoid",
+                      input_scale: str = "one", nseqs: Optional[int] = None):
+    """(y, final_states) of linrec_fwd with autograd support: gradients reach x, g, in_gate, decay and
+    initial_states, from y and from final_states."""
+    return LinearRecurrence.apply(x, g, in_gate, decay, initial_states, seq_idx, gate, input_scale, nseqs)
+
+
+def linrec_step(x, g, states, in_gate=None, decay=None, state_indices=None, gate: str = "sigmoid",
+                input_scale: str = "one", out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The recurrence for T = x.shape[1] tokens (1 .. 64) of each of b sequences, on a pool of states.
+
+    x, g, in_gate: (b, T, C), decay: (C) and the modes as for linrec_fwd; states: (slots, C) fp32, updated in place;
+    state_indices: (b) int32, the state of each row (None: row b has state b).  A row whose index is negative (or
+    past the pool) is empty: its y is zero.  Rows that name the same state take their turns in row order.  Returns y
+    (like x, contiguous; ``out`` when given).  Not differentiable; autograd sees that states (and out) change.
+    """
+    shape = _inputs("linrec_step", x, g, in_gate, decay, x.shape[0], gate, input_scale)[0]
+    dev = x.device
+    b, T, C = x.shape
+    if T > MAX_STEP_TOKENS:
+        raise ValueError(f"linrec_step takes up to {MAX_STEP_TOKENS} tokens a row; got {T} (use linrec_fwd)")
+    if states.dim() != 2:
+        raise ValueError("states is (slots, channels)")
+    ssd._check(states, "states", torch.float32, (states.shape[0], C), dev)
+    if state_indices is None:
+        if states.shape[0] < b:
+            raise ValueError(f"states holds {states.shape[0]} states for {b} rows")
+    else:
+        ssd._check(state_indices, "state_indices", torch.int32, (b,), dev)
+    if out is None:
+        out = torch.empty((b, T, C), dtype=x.dtype, device=dev)
+    else:
+        ssd._check(out, "out", x.dtype, (b, T, C), dev)
+    lib = load_library()
+    with _on(dev):
+        rc = lib.linrec_step(ctypes.byref(shape), ssd._ptr(x), ssd._ptr(g), ssd._ptr(in_gate), ssd._ptr(decay),
+                             states.data_ptr(), states.shape[0], ssd._ptr(state_indices), out.data_ptr(), _stream(dev))
+    if rc:
+        raise ssd.SsdError(rc, "linrec_step")
+    for t in (states, out):
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+    return out

@@ -1,0 +1,354 @@
+"""GPU parity of the gated linear recurrence, its gradients and its few-token form
+with the fp64 oracle, elementwise: the oracle carries along what float32
+arithmetic may add to each element (oracle/recurrence.py), and a bf16 output may
+be off by its own rounding, 2^-8 of its value, besides."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import recurrence as orc
+from state_space_model_mamba_amd import recurrence as rec
+
+pytestmark = pytest.mark.gpu
+IO = {"f32": torch.float32, "bf16": torch.bfloat16}
+GATES, SCALES = ("log", "sigmoid", "decay"), ("one", "complement", "unit")
+
+
+def f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def near(got, ref, err, label):
+    own = 2.0 ** -8 if got.dtype == torch.bfloat16 else 2.0 ** -24
+    off = np.abs(f64(got) - ref)
+    room = (1 + own) * err + own * np.abs(ref) + 1e-36
+    worst = float(np.max(off / room)) if off.size else 0.0
+    print(f"  {label}: {worst:.2f} of what is allowed", flush=True)
+    assert not np.isnan(off).any() and worst <= 1, f"{label}: {worst:.2f} of what is allowed"
+
+
+def make(b, L, C, io, gate="sigmoid", in_gate=True, lengths=None, initial=True, seed=0, shift=0.0):
+    gen = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(s, generator=gen)  # noqa: E731
+    t = IO[io]
+    d = {"x": rn(b, L, C).to(t), "in_gate": rn(b, L, C).mul(2).to(t) if in_gate else None,
+         "g": -torch.nn.functional.softplus(2 * rn(b, L, C) - 3 + shift) if gate == "log" else (rn(b, L, C).mul(2) + 1 - shift).to(t),
+         "decay": -8 * torch.rand((C,), generator=gen) if gate == "decay" else None, "dy": rn(b, L, C).to(t), "seq_idx": None}
+    n = b
+    if lengths is not None:   # per batch row
+        d["seq_idx"] = torch.stack([torch.repeat_interleave(torch.arange(len(r), dtype=torch.int32) * 3 % 7, torch.tensor(r)) for r in lengths]).contiguous()
+        n = len(orc.starts_of((b, L), d["seq_idx"].numpy()))
+    d["h0"], d["dfinal"], d["nseqs"] = rn(n, C) if initial else None, rn(n, C) if initial else None, n
+    return d
+
+
+def cuda(d):
+    return {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+
+
+def forward(c, **kw):
+    return rec.linrec_fwd(c["x"], c["g"], c["in_gate"], c["decay"], c["h0"], c["seq_idx"], nseqs=c["nseqs"], want_final_states=True, **kw)
+
+
+def backward(c, **kw):
+    return rec.linrec_bwd(c["x"], c["g"], c["in_gate"], c["decay"], c["dy"], c["h0"], c["seq_idx"], c["dfinal"], nseqs=c["nseqs"], **kw)
+
+
+GRADS = ("dx", "dg", "d_in_gate", "ddecay", "d_initial_states")
+
+
+def check(d, label, gate="sigmoid", scale="one"):
+    print(f"[case] linrec {label} {gate} {scale}", flush=True)
+    c, h = cuda(d), {k: f64(v) for k, v in d.items() if k not in ("seq_idx", "nseqs")}
+    seq = None if d["seq_idx"] is None else d["seq_idx"].numpy()
+    kw = dict(gate=gate, input_scale=scale)
+    r = forward(c, want_chunk_states=True, **kw)
+    g = backward(c, chunk_states=r["chunk_states"], **kw)
+    again = backward(c, **kw)   # without the kept states
+    torch.cuda.synchronize()
+    ref = orc.forward(h["x"], h["g"], h["in_gate"], h["decay"], h["h0"], seq, **kw)
+    near(r["y"], ref["y"], ref["y_err"], "y")
+    near(r["final_states"], ref["final_states"], ref["final_err"], "final_states")
+    ref = orc.backward(h["x"], h["g"], h["in_gate"], h["decay"], h["dy"], h["h0"], seq, h["dfinal"], **kw)
+    for k in GRADS:
+        if g[k] is None:
+            assert (k == "d_in_gate" and d["in_gate"] is None) or (k == "ddecay" and gate != "decay")
+            continue
+        near(g[k], ref[k], ref[k + "_err"], k)
+        assert torch.equal(g[k], again[k]), k
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("in_gate", [False, True])
+def test_every_mode(io, gate, scale, in_gate):
+    check(make(2, 150, 40, io, gate, in_gate, lengths=[[37, 1, 112], [150]], seed=1), f"{io} in_gate={in_gate}", gate, scale)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("b,L,C", [(1, 1, 8), (3, 1, 64), (1, 2, 128), (1, 63, 16), (1, 64, 256), (1, 65, 264), (2, 128, 136), (1, 129, 1000), (5, 77, 520),
+                                   (1, 700, 24), (40, 3, 72), (1, 2500, 8)])
+def test_sizes(io, b, L, C):
+    check(make(b, L, C, io, "decay", seed=L + C), f"{io} {b}x{L}x{C}", "decay", "unit")
+
+
+@pytest.mark.parametrize("lengths", [[64] * 5, [1] * 70, [63, 1, 64, 65, 127, 1, 1, 199], [8, 8, 7, 9, 288], [512], [300, 1]])
+def test_packed_sequences(lengths):
+    check(make(1, sum(lengths), 264, "f32", "decay", lengths=[lengths], seed=3), f"f32 {lengths}", "decay", "unit")
+    check(make(1, sum(lengths), 264, "bf16", "log", False, lengths=[lengths], initial=False, seed=4), f"bf16 {lengths}", "log", "one")
+
+
+def test_long_memory():
+    # decays within 1e-3 of one over 3000 rows
+    check(make(1, 3000, 16, "f32", "log", False, seed=5, shift=-6.0), "f32 decays near one", "log", "unit")
+    check(make(1, 3000, 16, "f32", "sigmoid", False, seed=5, shift=-7.0), "f32 decays near one", "sigmoid", "complement")
+
+
+@pytest.mark.parametrize("scale", SCALES)
+def test_dropped_states_and_closed_gates(scale):
+    d = make(1, 200, 32, "f32", "log", seed=6)
+    d["g"][0, ::17] = float("-inf")
+    d["g"][0, 5] = -200.0
+    d["g"][0, 9, :16] = 0.0   # a of one: nothing is lost, nothing comes in with "complement" and "unit"
+    check(d, "-inf, -200 and 0", "log", scale)
+    d = make(1, 200, 32, "bf16", "decay", seed=7)
+    d["g"][0, ::13] = -100.0
+    d["g"][0, 1::13] = 100.0
+    d["in_gate"][0, ::11] = 80.0
+    d["decay"][:4] = 0.0
+    check(d, "gates at their ends", "decay", scale)
+
+
+@pytest.mark.parametrize("where", [0, 63, 70, 139])
+def test_a_bad_value_stays_in_its_sequence_and_channel(where):
+    d = cuda(make(1, 300, 24, "f32", "decay", lengths=[[70, 70, 1, 159]], seed=8))
+    kw = dict(gate="decay", input_scale="unit")
+    good, gg = forward(d, **kw), backward(d, **kw)
+    for bad in (float("nan"), float("inf")):
+        for name in ("x", "g", "dy"):
+            e = dict(d, **{name: d[name].clone()})
+            e[name][0, where, 5] = bad
+            r, gr = forward(e, **kw), backward(e, **kw)
+            mine = range(0, 70) if where < 70 else range(70, 140)
+            rows = [t for t in range(300) if t not in mine]
+            chans = [k for k in range(24) if k != 5]
+            for a, b in ((good["y"], r["y"]), (gg["dx"], gr["dx"]), (gg["dg"], gr["dg"]), (gg["d_in_gate"], gr["d_in_gate"])):
+                assert torch.equal(a[:, rows], b[:, rows]) and torch.equal(a[..., chans], b[..., chans]), (name, bad)
+
+
+def test_numbered_sequences_past_the_last_and_beyond_the_count():
+    d = cuda(make(1, 200, 32, "f32", lengths=[[50, 60, 90]], seed=9))
+    ref, rg = forward(d), backward(d)
+    # two more states than sequences: they stay as they were
+    more = dict(d, h0=torch.cat([d["h0"], d["h0"][:2] + 1]), dfinal=torch.cat([d["dfinal"], d["dfinal"][:2] - 1]), nseqs=5)
+    r, g = forward(more), backward(more)
+    assert torch.equal(r["y"], ref["y"]) and torch.equal(r["final_states"][:3], ref["final_states"]) and torch.equal(r["final_states"][3:], more["h0"][3:])
+    assert torch.equal(g["dx"], rg["dx"]) and torch.equal(g["d_initial_states"][:3], rg["d_initial_states"])
+    assert torch.equal(g["d_initial_states"][3:], more["dfinal"][3:])
+    # one fewer: the last sequence enters with zeros
+    fewer = dict(d, h0=d["h0"][:2].contiguous(), dfinal=d["dfinal"][:2].contiguous(), nseqs=2)
+    r, g = forward(fewer), backward(fewer)
+    zero = dict(d, h0=torch.cat([d["h0"][:2], torch.zeros_like(d["h0"][:1])]), dfinal=torch.cat([d["dfinal"][:2], torch.zeros_like(d["h0"][:1])]))
+    assert torch.equal(r["y"], forward(zero)["y"]) and torch.equal(r["final_states"], ref["final_states"][:2]) and torch.equal(g["dx"], backward(zero)["dx"])
+
+
+def test_slices_of_wider_rows_bits_on_repeat_and_any_workspace():
+    d = cuda(make(2, 1000, 264, "bf16", "decay", seed=10))
+    row = torch.cat([d["in_gate"], d["x"], d["g"], d["dy"]], -1)
+    s = dict(d, in_gate=row[..., :264], x=row[..., 264:528], g=row[..., 528:792])
+    kw, first = dict(gate="decay", input_scale="unit"), None
+    for i, t in enumerate((d, s, d, d)):
+        ws = torch.full((1 << 21,), 255 if i == 2 else 0, dtype=torch.uint8, device="cuda") if i > 1 else torch.randint(0, 256, (1 << 21,), dtype=torch.uint8, device="cuda")
+        r = forward(t, workspace=ws, want_chunk_states=True, **kw)
+        g = backward(t, workspace=ws, **kw)
+        out = [r["y"], r["final_states"], r["chunk_states"], *[g[k] for k in GRADS]]
+        first = first or out
+        assert all(torch.equal(p, q) for p, q in zip(first, out))
+
+
+def test_many_blocks_repeat_their_bits():
+    d = cuda(make(1, 8192, 2048, "bf16", "decay", initial=False, seed=11))
+    kw, first = dict(gate="decay", input_scale="unit"), None
+    for _ in range(4):
+        r = forward(d, want_chunk_states=True, **kw)
+        g = backward(d, chunk_states=r["chunk_states"], **kw)
+        out = [r["y"], r["final_states"], r["chunk_states"], *[g[k] for k in GRADS]]
+        first = first or out
+        assert all(torch.equal(p, q) for p, q in zip(first, out))
+    # channels are alone: a few of them against the oracle over the whole length
+    at = [0, 1, 255, 256, 1000, 2040, 2047]
+    h = {k: f64(d[k][..., at]) for k in ("x", "g", "in_gate", "decay", "dy", "dfinal") if d[k] is not None}
+    ref = orc.forward(h["x"], h["g"], h["in_gate"], h["decay"], **kw)
+    near(first[0][..., at], ref["y"], ref["y_err"], "y")
+    ref = orc.backward(h["x"], h["g"], h["in_gate"], h["decay"], h["dy"], **kw)
+    for k, t in zip(("dx", "dg", "d_in_gate", "ddecay"), first[3:]):
+        near(t[..., at], ref[k], ref[k + "_err"], k)
+
+
+def test_rows_past_32_bits():
+    wide = torch.empty((300, 1 << 23), dtype=torch.bfloat16, device="cuda")   # rows 2^23 elements apart: the last past 2^31
+    d = cuda(make(1, 300, 64, "bf16", seed=12))
+    s = dict(d, x=wide[None, :, :64], g=wide[None, :, 64:128], in_gate=wide[None, :, 128:192])
+    for k in ("x", "g", "in_gate"):
+        s[k].copy_(d[k])
+    assert torch.equal(forward(d)["y"], forward(s)["y"])
+    a, b = backward(d), backward(s)
+    assert all(torch.equal(a[k], b[k]) for k in ("dx", "dg", "d_in_gate"))
+
+
+def test_a_sequence_in_two_calls():
+    d = cuda(make(1, 400, 64, "f32", "decay", seed=13))
+    kw = dict(gate="decay", input_scale="unit")
+    whole, wg = forward(d, **kw), backward(d, **kw)
+    part = lambda lo, hi: {k: v[:, lo:hi].contiguous() if k in ("x", "g", "in_gate", "dy") else v for k, v in d.items()}  # noqa: E731
+    one, two = part(0, 170), part(170, 400)
+    r1 = forward(one, **kw)
+    two["h0"] = r1["final_states"]
+    r2, g2 = forward(two, **kw), backward(two, **kw)
+    one["dfinal"] = g2["d_initial_states"]
+    g1 = backward(one, **kw)
+    # both differ from the whole by float32 roundings of 400 rows at most
+    for a, b in ((whole["y"], torch.cat([r1["y"], r2["y"]], 1)), (wg["dx"], torch.cat([g1["dx"], g2["dx"]], 1)), (wg["dg"], torch.cat([g1["dg"], g2["dg"]], 1)),
+                 (wg["ddecay"], g1["ddecay"] + g2["ddecay"])):
+        assert float((a - b).norm() / a.norm()) < 400 * 16 * 2.0 ** -24
+
+
+def test_autograd_matches_the_entry_points_and_a_replayed_graph():
+    d = cuda(make(1, 300, 64, "bf16", "decay", lengths=[[100, 200]], seed=14))
+    kw = dict(gate="decay", input_scale="unit")
+    leaves = [d[k].clone().requires_grad_(True) for k in ("x", "g", "in_gate", "decay", "h0")]
+    y, final = rec.linear_recurrence(*leaves, d["seq_idx"], **kw)
+    got = torch.autograd.grad((y, final), leaves, (d["dy"], d["dfinal"]))
+    g = backward(d, **kw)
+    assert all(torch.equal(a, g[k]) for a, k in zip(got, GRADS))
+    y, final = rec.linear_recurrence(*leaves, d["seq_idx"], **kw)
+    only = torch.autograd.grad(final, leaves[:2], d["dfinal"])
+    z = backward(dict(d, dy=torch.zeros_like(d["dy"])), **kw)
+    assert torch.equal(only[0], z["dx"]) and torch.equal(only[1], z["dg"])
+    del y, final, got, only
+    ref = forward(d, **kw)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        r = forward(d, want_chunk_states=True, **kw)
+        b = backward(d, chunk_states=r["chunk_states"], **kw)
+    for turn in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(r["y"], ref["y"]) and torch.equal(r["final_states"], ref["final_states"]), turn
+        assert all(torch.equal(b[k], g[k]) for k in GRADS), turn
+        for t in (r["y"], r["final_states"], r["chunk_states"], *[b[k] for k in GRADS]):
+            t.zero_()
+
+
+def test_two_streams_at_once():
+    ds = [cuda(make(1, 4096, 512, "bf16", "decay", seed=15 + i)) for i in range(2)]
+    kw = dict(gate="decay", input_scale="unit")
+    refs = [(forward(d, **kw), backward(d, **kw)) for d in ds]
+    streams = [torch.cuda.Stream() for _ in ds]
+    torch.cuda.synchronize()
+    outs = []
+    for d, s in zip(ds, streams):
+        with torch.cuda.stream(s):
+            outs.append([(forward(d, **kw), backward(d, **kw)) for _ in range(3)])
+    torch.cuda.synchronize()
+    for (rf, rb), out in zip(refs, outs):
+        for f, b in out:
+            assert torch.equal(f["y"], rf["y"]) and all(torch.equal(b[k], rb[k]) for k in GRADS)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("gate,scale", list(itertools.product(GATES, SCALES)))
+def test_step(io, gate, scale):
+    b, T, C, slots = 5, 3, 264, 9
+    d = make(b, T, C, io, gate, in_gate=scale != "one", seed=20)
+    states = torch.randn((slots, C), generator=torch.Generator().manual_seed(21))
+    index = torch.tensor([4, -1, 0, 8, 9], dtype=torch.int32)   # -1 and 9 are empty
+    c = cuda(d)
+    pool = states.cuda()
+    kw = dict(gate=gate, input_scale=scale)
+    y = rec.linrec_step(c["x"], c["g"], pool, c["in_gate"], c["decay"], index.cuda(), **kw)
+    torch.cuda.synchronize()
+    live = [0, 2, 3]
+    h = {k: f64(d[k][live]) if d[k] is not None else None for k in ("x", "g", "in_gate")}
+    at = index[live].long()
+    ref = orc.forward(h["x"], h["g"], h["in_gate"], f64(d["decay"]), f64(states[at]), **kw)
+    near(y[live], ref["y"], ref["y_err"], "y")
+    near(pool[at.cuda()], ref["final_states"], ref["final_err"], "states")
+    rest = [s for s in range(slots) if s not in (4, 0, 8)]
+    assert bool((y[[1, 4]] == 0).all()) and torch.equal(pool[rest].cpu(), states[rest])
+
+
+def test_step_rows_of_one_state_take_turns():
+    C = 72
+    for b, index in ((4, [2, 1, 2, 2]), (130, [i % 3 for i in range(130)]), (70, [0] * 70)):
+        d = cuda(make(b, 2, C, "f32", seed=b))
+        pool = torch.randn((3, C), generator=torch.Generator().manual_seed(b)).cuda()
+        one = pool.clone()
+        idx = torch.tensor(index, dtype=torch.int32, device="cuda")
+        y = rec.linrec_step(d["x"], d["g"], pool, d["in_gate"], state_indices=idx)
+        for r in range(b):
+            part = rec.linrec_step(d["x"][r:r + 1], d["g"][r:r + 1], one, d["in_gate"][r:r + 1], state_indices=idx[r:r + 1].contiguous())
+            assert torch.equal(part[0], y[r]), r
+        assert torch.equal(pool, one)
+
+
+def test_steps_continue_a_sequence():
+    d = cuda(make(3, 80, 136, "bf16", "decay", seed=30))
+    kw = dict(gate="decay", input_scale="unit")
+    whole = forward(d, **kw)
+    part = {k: v[:, :70].contiguous() if k in ("x", "g", "in_gate", "dy") else v for k, v in d.items()}
+    pool = forward(part, **kw)["final_states"]
+    ys = []
+    for lo, hi in ((70, 71), (71, 75), (75, 80)):
+        ys.append(rec.linrec_step(d["x"][:, lo:hi], d["g"][:, lo:hi], pool, d["in_gate"][:, lo:hi], d["decay"], **kw))
+    y = torch.cat(ys, 1).float()
+    assert float((y - whole["y"][:, 70:].float()).norm() / y.norm()) < 2.0 ** -8
+    assert float((pool - whole["final_states"]).norm() / pool.norm()) < 80 * 16 * 2.0 ** -24
+
+
+def test_step_marks_its_states_and_replays():
+    d = cuda(make(2, 1, 64, "bf16", seed=31))
+    pool = torch.zeros((2, 64), device="cuda")
+    v = pool._version
+    out = torch.empty((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    assert rec.linrec_step(d["x"], d["g"], pool, out=out) is out and pool._version > v
+    ref = pool.clone()
+    pool.zero_()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        rec.linrec_step(d["x"], d["g"], pool, out=out)
+    for _ in range(3):
+        pool.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(pool, ref)
+
+
+def test_refusals_on_the_device():
+    x = torch.zeros((2, 5, 16), dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros((2, 16), device="cuda")
+    with pytest.raises(ValueError, match="gate is one of"):
+        rec.linrec_fwd(x, x, gate="tanh")
+    with pytest.raises(ValueError, match="input_scale is one of"):
+        rec.linrec_fwd(x, x, input_scale="half")
+    with pytest.raises(ValueError, match="dtype"):
+        rec.linrec_fwd(x, x, gate="log")   # log decays are float32
+    with pytest.raises(ValueError, match="decay goes with"):
+        rec.linrec_fwd(x, x, gate="decay")
+    with pytest.raises(ValueError, match="decay goes with"):
+        rec.linrec_fwd(x, x, decay=pool[0])
+    with pytest.raises(ValueError, match="nseqs"):
+        rec.linrec_fwd(x, x, seq_idx=torch.zeros((2, 5), dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="shape"):
+        rec.linrec_bwd(x, x, None, None, x, chunk_states=torch.zeros((2, 16), device="cuda"))
+    with pytest.raises(ValueError, match="up to 64 tokens"):
+        rec.linrec_step(torch.zeros((1, 65, 16), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, 65, 16), dtype=torch.bfloat16, device="cuda"), pool)
+    with pytest.raises(ValueError, match="states for"):
+        rec.linrec_step(x, x, pool[:1])
+    with pytest.raises(Exception, match="shape|-2"):
+        rec.linrec_fwd(x[:, :0], x[:, :0])

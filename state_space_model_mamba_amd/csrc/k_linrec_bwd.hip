@@ -15,12 +15,16 @@ namespace linrec {
 
 using ssd::bf16_t;
 
-template <typename T, int GATE, int SCALE, bool ING, bool AGG> __global__ __launch_bounds__(THR) void k_linrec_bwd(Problem p) {
+template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(THR) void k_linrec_bwd(Problem p) {
   constexpr int V = VALS<T>, CB = 64 * V;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
-  __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], fc[WAVES][CB];
+  __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], fc[WAVES][CB], enter[CB];
+  __shared__ int cuts;
   const int lane = ssd::lane_id(), wave = ssd::wave_id_s();
-  const int chunk = static_cast<int>(blockIdx.x / p.cblocks), cb = static_cast<int>(blockIdx.x % p.cblocks);
+  if (threadIdx.x == 0) cuts = 0;
+  const uint32_t id = ticket(p);
+  const int place = static_cast<int>(id / p.cblocks), cb = static_cast<int>(id % p.cblocks);
+  const int chunk = p.chunks - 1 - place;   // from the end
   const int c0 = cb * CB + lane * V;
   const bool live = c0 < p.C;
   const int c = live ? c0 : p.C - V;
@@ -32,8 +36,8 @@ template <typename T, int GATE, int SCALE, bool ING, bool AGG> __global__ __laun
     const int r = r0 + j < p.R ? r0 + j : p.R - 1;
     g[j].load(static_cast<const G*>(p.g) + row_offset(r, p, p.g_sb, p.g_sl) + c);
     dy[j].load(static_cast<const T*>(p.dy) + static_cast<int64_t>(r) * p.C + c);
-    if (!AGG) x[j].load(static_cast<const T*>(p.x) + row_offset(r, p, p.x_sb, p.x_sl) + c);
-    if (!AGG && ING) in[j].load(static_cast<const T*>(p.i) + row_offset(r, p, p.i_sb, p.i_sl) + c);
+    x[j].load(static_cast<const T*>(p.x) + row_offset(r, p, p.x_sb, p.x_sl) + c);
+    if (ING) in[j].load(static_cast<const T*>(p.i) + row_offset(r, p, p.i_sb, p.i_sl) + c);
   }
   Raw<float, V> dk;
   if (GATE == LINREC_GATE_DECAY) dk.load(p.decay + c);
@@ -61,11 +65,9 @@ template <typename T, int GATE, int SCALE, bool ING, bool AGG> __global__ __laun
       const Gate q = gate_of<T, GATE, SCALE>(g[j].get(v), decay(v));
       a[j][v] = q.a;
       h[j][v] = H[v];
-      if (!AGG) {
-        float u = x[j].get(v);
-        if (ING) u *= Fn<T>::sigmoid(in[j].get(v));
-        H[v] = fmaf(q.a, H[v], q.m * u);
-      }
+      float u = x[j].get(v);
+      if (ING) u *= Fn<T>::sigmoid(in[j].get(v));
+      H[v] = fmaf(q.a, H[v], q.m * u);
       A[v] *= q.a;
     }
   }
@@ -100,9 +102,17 @@ template <typename T, int GATE, int SCALE, bool ING, bool AGG> __global__ __laun
     fh[wave][lane * V + v] = H[v];
     fc[wave][lane * V + v] = cr[v];
   }
+  if (p.chunks == 1) __syncthreads();   // cuts is cleared
+  if (lane == 0 && cut) cuts = 1;
   __syncthreads();
-  if constexpr (AGG) {
-    if (wave == 0 && live) {
+  float hin[V], sum[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    hin[v] = chunk > 0 ? p.states[static_cast<int64_t>(chunk - 1) * p.C + c + v] : 0.f;
+    cr[v] = sum[v] = 0.f;
+  }
+  if (p.chunks > 1) {
+    if (wave == 0) {
       float B[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) B[v] = 0.f, A[v] = 1.f;
@@ -114,128 +124,112 @@ template <typename T, int GATE, int SCALE, bool ING, bool AGG> __global__ __laun
           A[v] = both(A[v], f);
         }
       }
+      const int last = p.chunks - 1;
+      join<V>(p, p.carry, place, cb, c, live, cuts != 0, A, B, cr, [last](int k) { return last - k; });
 #pragma unroll
-      for (int v = 0; v < V; ++v) p.agg[static_cast<int64_t>(chunk) * p.C + c + v] = float2{A[v], B[v]};
+      for (int v = 0; v < V; ++v) enter[lane * V + v] = cr[v];
     }
-  } else {
-    float hin[V], sum[V];
+    __syncthreads();
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      hin[v] = chunk > 0 ? p.states[static_cast<int64_t>(chunk - 1) * p.C + c + v] : 0.f;
-      cr[v] = chunk + 1 < p.chunks ? p.carry[static_cast<int64_t>(chunk + 1) * p.C + c + v] : 0.f;
-      sum[v] = 0.f;
-    }
-    for (int w = 0; w < wave; ++w) {
+    for (int v = 0; v < V; ++v) cr[v] = enter[lane * V + v];
+  }
+  for (int w = 0; w < wave; ++w) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) hin[v] = onto(fa[w][lane * V + v], fh[w][lane * V + v], hin[v]);
-    }
-    for (int w = WAVES - 1; w > wave; --w) {
+    for (int v = 0; v < V; ++v) hin[v] = onto(fa[w][lane * V + v], fh[w][lane * V + v], hin[v]);
+  }
+  for (int w = WAVES - 1; w > wave; --w) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) cr[v] = onto(fa[w][lane * V + v], fc[w][lane * V + v], cr[v]);
-    }
-    // the states before the rows up to the first start get what is left of the entering one
-    float left[V];
+    for (int v = 0; v < V; ++v) cr[v] = onto(fa[w][lane * V + v], fc[w][lane * V + v], cr[v]);
+  }
+  // the states before the rows up to the first start get what is left of the entering one
+  float left[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) left[v] = hin[v];
-    bool inside = true;
+  for (int v = 0; v < V; ++v) left[v] = hin[v];
+  bool inside = true;
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-      if ((starts >> j) & 1u) inside = false;
-      if (inside) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          h[j][v] += left[v];
-          left[v] *= a[j][v];
-        }
-      }
-    }
-#pragma unroll
-    for (int j = ROWS - 1; j >= 0; --j) {
-      const int r = r0 + j;
-      if (r >= p.R) continue;
-      float e[V], ox[V], og[V], oi[V];
-      const bool start = (starts >> j) & 1u;
-#pragma unroll
-      for (int v = 0; v < V; ++v) e[v] = dy[j].get(v) + cr[v];
-      final_gradient(j, e);
+  for (int j = 0; j < ROWS; ++j) {
+    if ((starts >> j) & 1u) inside = false;
+    if (inside) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Gate q = gate_of<T, GATE, SCALE>(g[j].get(v), decay(v));
-        const float xv = x[j].get(v);
-        float si = 1.f, ri = 0.f;
-        if (ING) {
-          const float2 sr = Fn<T>::sigmoids(in[j].get(v));
-          si = sr.x;
-          ri = sr.y;
-        }
-        const float u = xv * si, du = q.m * e[v];
-        const float dl = e[v] * fmaf(q.a, h[j][v], q.dm * u);
-        ox[v] = du * si;
-        oi[v] = du * u * ri;
-        og[v] = dl * q.dg;
-        sum[v] += dl * q.sg;
-        cr[v] = q.a * e[v];
-      }
-      if (live) {
-        const int64_t at = static_cast<int64_t>(r) * p.C + c;
-        Raw<T, V> o;
-        o.set(ox);
-        o.store(static_cast<T*>(p.dx) + at);
-        Raw<G, V> og_;
-        og_.set(og);
-        og_.store(static_cast<G*>(p.dg) + at);
-        if (ING) {
-          o.set(oi);
-          o.store(static_cast<T*>(p.di) + at);
-        }
-        if (start && p.dh0) {
-          const int s = sequence_of(p, r);
-          if (s >= 0) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) p.dh0[static_cast<int64_t>(s) * p.C + c + v] = cr[v];
-          }
-        }
-      }
-      if (start) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) cr[v] = 0.f;
-      }
-    }
-    if (p.dh0 && p.seq_idx && chunk == 0 && wave == 0 && live) {   // numbered sequences past the last one
-      for (int s = p.nseqs - 1; s >= 0 && p.starts[s] >= p.R; --s) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) p.dh0[static_cast<int64_t>(s) * p.C + c + v] = p.dfinal ? p.dfinal[static_cast<int64_t>(s) * p.C + c + v] : 0.f;
-      }
-    }
-    if constexpr (GATE == LINREC_GATE_DECAY) {
-      if (p.ddecay) {
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < V; ++v) fc[wave][lane * V + v] = sum[v];
-        __syncthreads();
-        if (wave == 0 && live) {
-          for (int w = 1; w < WAVES; ++w) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) sum[v] += fc[w][lane * V + v];
-          }
-#pragma unroll
-          for (int v = 0; v < V; ++v) p.slots[static_cast<int64_t>(chunk) * p.C + c + v] = sum[v];
-        }
+        h[j][v] += left[v];
+        left[v] *= a[j][v];
       }
     }
   }
-}
-
-// What the chunks hand back, a channel a lane.
-__global__ __launch_bounds__(64) void k_linrec_rchain(Problem p) {
-  const int c = static_cast<int>(blockIdx.x) * 64 + static_cast<int>(threadIdx.x);
-  if (c >= p.C) return;
-  float h = 0.f;
-#pragma unroll 8
-  for (int k = p.chunks - 1; k >= 0; --k) {
-    const float2 f = p.agg[static_cast<int64_t>(k) * p.C + c];
-    h = onto(f.x, f.y, h);
-    p.carry[static_cast<int64_t>(k) * p.C + c] = h;
+#pragma unroll
+  for (int j = ROWS - 1; j >= 0; --j) {
+    const int r = r0 + j;
+    if (r >= p.R) continue;
+    float e[V], ox[V], og[V], oi[V];
+    const bool start = (starts >> j) & 1u;
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = dy[j].get(v) + cr[v];
+    final_gradient(j, e);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const Gate q = gate_of<T, GATE, SCALE>(g[j].get(v), decay(v));
+      const float xv = x[j].get(v);
+      float si = 1.f, ri = 0.f;
+      if (ING) {
+        const float2 sr = Fn<T>::sigmoids(in[j].get(v));
+        si = sr.x;
+        ri = sr.y;
+      }
+      const float u = xv * si, du = q.m * e[v];
+      const float dl = e[v] * fmaf(q.a, h[j][v], q.dm * u);
+      ox[v] = du * si;
+      oi[v] = du * u * ri;
+      og[v] = dl * q.dg;
+      sum[v] += dl * q.sg;
+      cr[v] = q.a * e[v];
+    }
+    if (live) {
+      const int64_t at = static_cast<int64_t>(r) * p.C + c;
+      Raw<T, V> o;
+      o.set(ox);
+      o.store(static_cast<T*>(p.dx) + at);
+      Raw<G, V> og_;
+      og_.set(og);
+      og_.store(static_cast<G*>(p.dg) + at);
+      if (ING) {
+        o.set(oi);
+        o.store(static_cast<T*>(p.di) + at);
+      }
+      if (start && p.dh0) {
+        const int s = sequence_of(p, r);
+        if (s >= 0) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) p.dh0[static_cast<int64_t>(s) * p.C + c + v] = cr[v];
+        }
+      }
+    }
+    if (start) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) cr[v] = 0.f;
+    }
+  }
+  if (p.dh0 && p.seq_idx && chunk == 0 && wave == 0 && live) {   // numbered sequences past the last one
+    for (int s = p.nseqs - 1; s >= 0 && p.starts[s] >= p.R; --s) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.dh0[static_cast<int64_t>(s) * p.C + c + v] = p.dfinal ? p.dfinal[static_cast<int64_t>(s) * p.C + c + v] : 0.f;
+    }
+  }
+  if constexpr (GATE == LINREC_GATE_DECAY) {
+    if (p.ddecay) {
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v) fc[wave][lane * V + v] = sum[v];
+      __syncthreads();
+      if (wave == 0 && live) {
+        for (int w = 1; w < WAVES; ++w) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) sum[v] += fc[w][lane * V + v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.slots[static_cast<int64_t>(chunk) * p.C + c + v] = sum[v];
+      }
+    }
   }
 }
 
@@ -261,10 +255,7 @@ __global__ __launch_bounds__(RED_COLS * RED_ROWS) void k_linrec_reduce(Problem p
 
 namespace {
 template <typename T, int GATE, int SCALE, bool ING> int go(const Problem& p, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(p.chunks * p.cblocks));
-  hipLaunchKernelGGL((k_linrec_bwd<T, GATE, SCALE, ING, true>), grid, dim3(THR), 0, st, p);
-  hipLaunchKernelGGL(k_linrec_rchain, dim3(static_cast<unsigned>((p.C + 63) / 64)), dim3(64), 0, st, p);
-  hipLaunchKernelGGL((k_linrec_bwd<T, GATE, SCALE, ING, false>), grid, dim3(THR), 0, st, p);
+  hipLaunchKernelGGL((k_linrec_bwd<T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(THR), 0, st, p);
   if (GATE == LINREC_GATE_DECAY && p.ddecay)
     hipLaunchKernelGGL(k_linrec_reduce, dim3(static_cast<unsigned>((p.C + RED_COLS - 1) / RED_COLS)), dim3(RED_COLS * RED_ROWS), 0, st, p);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;

@@ -45,6 +45,7 @@ size_t place(Problem& p, bool backward, char* base) {
   };
   const size_t n = static_cast<size_t>(p.chunks) * p.C;
   p.starts = reinterpret_cast<int32_t*>(take((2 * static_cast<size_t>(p.nseqs) + 1) * 4));
+  p.sync = reinterpret_cast<uint32_t*>(take((static_cast<size_t>(p.chunks) * p.cblocks + 1) * 4));
   p.agg = reinterpret_cast<float2*>(take(n * sizeof(float2)));
   p.states = reinterpret_cast<float*>(take(n * 4));
   if (backward) {
@@ -139,7 +140,8 @@ int linrec_fwd(const linrec_shape* shape, const void* x, const void* g, const vo
   if (chunk_states) p.states = chunk_states;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if ((rc = find_starts(p, st)) != SSD_OK) return rc;
-  return linrec::launch_fwd(p, *shape, true, st);
+  if ((rc = linrec::launch_clear(p, st)) != SSD_OK) return rc;
+  return linrec::launch_fwd(p, *shape, st);
 }
 
 int linrec_bwd(const linrec_shape* shape, const void* x, const void* g, const void* in_gate, const float* decay,
@@ -161,8 +163,13 @@ int linrec_bwd(const linrec_shape* shape, const void* x, const void* g, const vo
   p.dx = dx; p.dg = dg; p.di = d_in_gate; p.ddecay = ddecay; p.dh0 = d_initial_states;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if ((rc = find_starts(p, st)) != SSD_OK) return rc;
-  if (chunk_states) p.states = const_cast<float*>(chunk_states);
-  else if ((rc = linrec::launch_fwd(p, *shape, false, st)) != SSD_OK) return rc;
+  if (chunk_states) {
+    p.states = const_cast<float*>(chunk_states);
+  } else {
+    if ((rc = linrec::launch_clear(p, st)) != SSD_OK) return rc;
+    if ((rc = linrec::launch_fwd(p, *shape, st)) != SSD_OK) return rc;
+  }
+  if ((rc = linrec::launch_clear(p, st)) != SSD_OK) return rc;
   return linrec::launch_bwd(p, *shape, st);
 }
 

@@ -28,13 +28,15 @@ struct Problem {
   float *final, *ddecay, *dh0;
   // workspace
   int32_t* starts;         // (nseqs + 1) first rows (seq_idx and states given), then nseqs more that only k_delta_starts reads
+  uint32_t* sync;          // the next ticket, then (chunks, cblocks): what of a chunk is there
   float2* agg;             // (chunks, C): a chunk's factor and what it adds
   float* states;           // (chunks, C): the state after each chunk
   float* carry;            // (chunks, C): what a chunk hands to the rows before it (backward)
   float* slots;            // (chunks, C): ddecay of each chunk (backward)
 };
 
-int launch_fwd(const Problem& p, const linrec_shape& s, bool outputs, hipStream_t st);
+int launch_clear(const Problem& p, hipStream_t st);   // the tickets, before either of the others
+int launch_fwd(const Problem& p, const linrec_shape& s, hipStream_t st);   // (p.y, p.final NULL: the states only)
 int launch_bwd(const Problem& p, const linrec_shape& s, hipStream_t st);
 
 #ifdef __HIPCC__
@@ -124,6 +126,115 @@ __device__ __forceinline__ float onto(float factor, float add, float state) { re
 
 // the factor of two parts; one that drops the state drops it whatever the other holds
 __device__ __forceinline__ float both(float f, float g) { return f == 0.f || g == 0.f ? 0.f : f * g; }
+
+// ---------------------------------------------------------------------------
+// The chunks' chain.  A block takes its chunk by a ticket, so the chunks before
+// it in the chain have begun and wait for none after it: every wait ends.  It
+// leaves its own (A, H) at once (PART) and the state behind it as soon as the
+// state before it is known (WHOLE); the next ones go back to the nearest chunk
+// whose state is there and take the parts between up from it, one after the
+// other, so that every state is formed in one order, wherever they found it.
+//
+// What blocks hand each other is written and read past the caches (relaxed
+// atomics of the device's scope); a mark is written after its values have
+// arrived, and the values are read after the mark was seen.
+// ---------------------------------------------------------------------------
+enum { NOTHING = 0, PART = 1, WHOLE = 2 };
+
+__device__ __forceinline__ void put(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ float take(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ void put(float2* p, float2 v) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 take(const float2* p) {
+  return __builtin_bit_cast(float2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+
+// The place of the block in the chain times cblocks, plus its channel block; the same in all threads.
+__device__ __forceinline__ uint32_t ticket(const Problem& p) {
+  __shared__ uint32_t t;
+  if (p.chunks == 1) return blockIdx.x;
+  if (threadIdx.x == 0) t = __hip_atomic_fetch_add(p.sync, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(t);
+}
+
+// One wave, for the lane's V channels from c on: the state before the chunk at `place` of the chain, and A, H onto it left
+// for the chunks behind.  chunk_at(place): the chunk there; after: the states behind the chunks; cut: a sequence starts in it.
+template <int V, typename ChunkAt>
+__device__ __forceinline__ void join(const Problem& p, float* after, int place, int cb, int c, bool live, bool cut, const float (&A)[V],
+                                     const float (&H)[V], float (&before)[V], ChunkAt chunk_at) {
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int64_t mine = static_cast<int64_t>(chunk_at(place)) * p.C + c;
+  auto mark = [&](uint32_t m) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the values have arrived
+    if (lane == 0) __hip_atomic_store(p.sync + 1 + static_cast<int64_t>(place) * p.cblocks + cb, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
+  auto leave = [&](const float (&h)[V]) {
+    if (live) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) put(after + mine + v, h[v]);
+    }
+    mark(WHOLE);
+  };
+  if (cut) {
+    leave(H);
+  } else if (place > 0) {
+    if (live) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) put(p.agg + mine + v, float2{A[v], H[v]});
+    }
+    mark(PART);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) before[v] = 0.f;
+  if (place > 0) {
+    int back = 0;   // places to go back to a known state, less one
+    for (;;) {
+      const int at = place - 1 - lane;
+      uint32_t m = WHOLE;   // before the first chunk: a state of zero
+      if (at >= 0) m = __hip_atomic_load(p.sync + 1 + static_cast<int64_t>(at) * p.cblocks + cb, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const uint64_t whole = __ballot(m == WHOLE), nothing = __ballot(m == NOTHING);
+      if (whole) {
+        back = __builtin_ctzll(whole);
+        if ((nothing & ((uint64_t{1} << back) - 1)) == 0) break;
+      }
+      __builtin_amdgcn_s_sleep(1);
+    }
+    asm volatile("" ::: "memory");
+    int from = place - 1 - back;
+    if (from >= 0) {
+      const int64_t at = static_cast<int64_t>(chunk_at(from)) * p.C + c;
+#pragma unroll
+      for (int v = 0; v < V; ++v) before[v] = take(after + at + v);
+    }
+    constexpr int AHEAD = 4;
+    for (int q = from + 1; q < place; q += AHEAD) {
+      float2 f[AHEAD][V];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (q + i < place && q + i >= 0) {
+          const int64_t at = static_cast<int64_t>(chunk_at(q + i)) * p.C + c;
+#pragma unroll
+          for (int v = 0; v < V; ++v) f[i][v] = take(p.agg + at + v);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (q + i < place && q + i >= 0) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) before[v] = onto(f[i][v].x, f[i][v].y, before[v]);
+        }
+      }
+    }
+  }
+  if (!cut) {
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = onto(A[v], H[v], before[v]);
+    leave(h);
+  }
+}
 
 __device__ __forceinline__ int64_t row_offset(int row, const Problem& p, int64_t sb, int64_t sl) {
   if (p.flat) return row * sl;

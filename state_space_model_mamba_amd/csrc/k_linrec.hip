@@ -13,76 +13,90 @@ namespace linrec {
 
 using ssd::bf16_t;
 
-template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(THR) void k_linrec(Problem p) {
-  constexpr int V = VALS<T>, CB = 64 * V;
+template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(THR) FWD_OCC void k_linrec(Problem p) {
+  constexpr int V = VALS<T, false>, CB = 64 * V;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
   __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], enter[CB];
   __shared__ int cuts;
   const int lane = ssd::lane_id(), wave = ssd::wave_id_s();
   if (threadIdx.x == 0) cuts = 0;
-  const uint32_t id = ticket(p);
-  const int chunk = static_cast<int>(id / p.cblocks), cb = static_cast<int>(id % p.cblocks);
+  const int cb = channel_block(p), chunk = ticket(p, cb);
   const int c0 = cb * CB + lane * V;
   const bool live = c0 < p.C;
   const int c = live ? c0 : p.C - V;
-  const int r0 = chunk * CHUNK + wave * ROWS;
+  const int r0 = chunk * CHUNK + wave * ROWS, rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS];
   Raw<G, V> g[ROWS];
+  Cursor at(p, rows > 0 ? r0 : p.R - 1);
 #pragma unroll
   for (int j = 0; j < ROWS; ++j) {
-    const int r = r0 + j < p.R ? r0 + j : p.R - 1;
-    x[j].load(static_cast<const T*>(p.x) + row_offset(r, p, p.x_sb, p.x_sl) + c);
-    g[j].load(static_cast<const G*>(p.g) + row_offset(r, p, p.g_sb, p.g_sl) + c);
-    if (ING) in[j].load(static_cast<const T*>(p.i) + row_offset(r, p, p.i_sb, p.i_sl) + c);
+    x[j].load(static_cast<const T*>(p.x) + at.x + c);
+    g[j].load(static_cast<const G*>(p.g) + at.g + c);
+    if (ING) in[j].load(static_cast<const T*>(p.i) + at.i + c);
+    if (j + 1 < rows) at.next(p);
   }
-  Raw<float, V> decay;
-  if (GATE == LINREC_GATE_DECAY) decay.load(p.decay + c);
+  Raw<float, V> dk;
+  if (GATE == LINREC_GATE_DECAY) dk.load(p.decay + c);
   const uint32_t starts = starts_at(p, r0);
-  float a[ROWS][V], b[ROWS][V], A[V], H[V];
+  const bool cut = starts & ((1u << ROWS) - 1);
+  float a[ROWS][V], b[ROWS][V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const Decay<T, GATE> d(GATE == LINREC_GATE_DECAY ? dk.get(v) : 0.f);
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const Factor f = factor_of<T, GATE, false>(g[j].get(v), d);
+      float u = x[j].get(v);
+      if (ING) u *= Fn<T>::sigmoid(in[j].get(v));
+      a[j][v] = f.a;
+      b[j][v] = scale_of<T, GATE, SCALE>(f) * u;
+    }
+  }
+  if (rows < ROWS) {   // rows past the last leave a state as it is
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      if (j >= rows) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[j][v] = 1.f, b[j][v] = 0.f;
+      }
+    }
+  }
+  if (cut && p.h0) {
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const int s = (starts >> j) & 1u ? sequence_of(p, r0 + j) : -1;
+      if (s >= 0) {
+        Raw<float, V> h0;
+        h0.load(p.h0 + static_cast<int64_t>(s) * p.C + c);
+#pragma unroll
+        for (int v = 0; v < V; ++v) b[j][v] = fmaf(a[j][v], h0.get(v), b[j][v]);
+      }
+    }
+  }
+  float A[V], H[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f;
+  // a start drops the state by selection, so that nothing of it (a NaN either) passes
+  auto gather = [&](auto with_starts) {
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    if (r0 + j < p.R) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Gate q = gate_of<T, GATE, SCALE>(g[j].get(v), GATE == LINREC_GATE_DECAY ? decay.get(v) : 0.f);
-        float u = x[j].get(v);
-        if (ING) u *= Fn<T>::sigmoid(in[j].get(v));
-        a[j][v] = q.a;
-        b[j][v] = q.m * u;
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) a[j][v] = 1.f, b[j][v] = 0.f;
-    }
-    if ((starts >> j) & 1u) {
-      if (p.h0) {
-        const int s = sequence_of(p, r0 + j);
-        if (s >= 0) {
-          Raw<float, V> h0;
-          h0.load(p.h0 + static_cast<int64_t>(s) * p.C + c);
-#pragma unroll
-          for (int v = 0; v < V; ++v) b[j][v] = fmaf(a[j][v], h0.get(v), b[j][v]);
-        }
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) A[v] = 0.f, H[v] = b[j][v];
-    } else {
+    for (int j = 0; j < ROWS; ++j) {
+      const bool start = with_starts.value && ((starts >> j) & 1u);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        A[v] *= a[j][v];
-        H[v] = fmaf(a[j][v], H[v], b[j][v]);
+        A[v] = start ? 0.f : A[v] * a[j][v];
+        H[v] = start ? b[j][v] : fmaf(a[j][v], H[v], b[j][v]);
       }
     }
-  }
+  };
+  if (cut) gather(std::true_type{});
+  else gather(std::false_type{});
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     fa[wave][lane * V + v] = A[v];
     fh[wave][lane * V + v] = H[v];
   }
   if (p.chunks == 1) __syncthreads();   // cuts is cleared
-  if (lane == 0 && (starts & ((1u << ROWS) - 1))) cuts = 1;
+  if (lane == 0 && cut) cuts = 1;
   __syncthreads();
   float h[V];
 #pragma unroll
@@ -110,28 +124,32 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = onto(fa[w][lane * V + v], fh[w][lane * V + v], h[v]);
   }
-  const uint32_t lasts = starts >> 1 | (p.R - 1 - r0 < 32 && p.R > r0 ? 1u << (p.R - 1 - r0) : 0u);
+  T* y = static_cast<T*>(p.y) + static_cast<int64_t>(r0) * p.C + c;
+  const uint32_t ends = p.final ? ends_at(p, r0, starts) : 0;
+  auto walk = [&](auto with_starts) {
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    const int r = r0 + j;
-    if (r >= p.R) break;
-    const bool start = (starts >> j) & 1u;
+    for (int j = 0; j < ROWS; ++j) {
+      const bool start = with_starts.value && ((starts >> j) & 1u);
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = start ? b[j][v] : fmaf(a[j][v], h[v], b[j][v]);
-    if (live) {
-      Raw<T, V> out;
-      out.set(h);
-      out.store(static_cast<T*>(p.y) + static_cast<int64_t>(r) * p.C + c);
-      if (p.final && ((lasts >> j) & 1u)) {
-        const int s = sequence_of(p, r);
-        if (s >= 0) {
-          Raw<float, V> f;
-          f.set(h);
-          f.store(p.final + static_cast<int64_t>(s) * p.C + c);
+      for (int v = 0; v < V; ++v) h[v] = start ? b[j][v] : fmaf(a[j][v], h[v], b[j][v]);
+      if (live && j < rows) {
+        Raw<T, V> out;
+        out.set(h);
+        out.store(y);
+        if (with_starts.value && ((ends >> j) & 1u)) {
+          const int s = sequence_of(p, r0 + j);
+          if (s >= 0) {
+            Raw<float, V> f;
+            f.set(h);
+            f.store(p.final + static_cast<int64_t>(s) * p.C + c);
+          }
         }
       }
+      y += p.C;
     }
-  }
+  };
+  if (cut || ends) walk(std::true_type{});
+  else walk(std::false_type{});
   // numbered sequences past the last one
   if (p.final && p.seq_idx && chunk == 0 && wave == 0 && live) {
     for (int s = p.nseqs - 1; s >= 0 && p.starts[s] >= p.R; --s) {
@@ -147,13 +165,14 @@ __global__ __launch_bounds__(256) void k_linrec_clear(uint32_t* sync, int64_t n)
 
 int launch_clear(const Problem& p, hipStream_t st) {
   if (p.chunks == 1) return SSD_OK;
-  const int64_t n = static_cast<int64_t>(p.chunks) * p.cblocks + 1;
+  const int64_t n = static_cast<int64_t>(p.cblocks) * (p.chunks + LINE);
   hipLaunchKernelGGL(k_linrec_clear, dim3(static_cast<unsigned>(n < 256 * 1024 ? (n + 255) / 256 : 1024)), dim3(256), 0, st, p.sync, n);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
 namespace {
-template <typename T, int GATE, int SCALE, bool ING> int go(const Problem& p, hipStream_t st) {
+template <typename T, int GATE, int SCALE, bool ING> int go(Problem p, hipStream_t st) {
+  p.cblocks = (p.C + 64 * VALS<T, false> - 1) / (64 * VALS<T, false>);
   hipLaunchKernelGGL((k_linrec<T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(THR), 0, st, p);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }

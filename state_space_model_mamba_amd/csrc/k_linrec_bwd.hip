@@ -15,87 +15,119 @@ namespace linrec {
 
 using ssd::bf16_t;
 
-template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(THR) void k_linrec_bwd(Problem p) {
-  constexpr int V = VALS<T>, CB = 64 * V;
+template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(THR) BWD_OCC void k_linrec_bwd(Problem p) {
+  constexpr int V = VALS<T, true>, CB = 64 * V;
+  constexpr bool DECAY = GATE == LINREC_GATE_DECAY;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
   __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], fc[WAVES][CB], enter[CB];
   __shared__ int cuts;
   const int lane = ssd::lane_id(), wave = ssd::wave_id_s();
   if (threadIdx.x == 0) cuts = 0;
-  const uint32_t id = ticket(p);
-  const int place = static_cast<int>(id / p.cblocks), cb = static_cast<int>(id % p.cblocks);
+  const int cb = channel_block(p), place = ticket(p, cb);
   const int chunk = p.chunks - 1 - place;   // from the end
   const int c0 = cb * CB + lane * V;
   const bool live = c0 < p.C;
   const int c = live ? c0 : p.C - V;
-  const int r0 = chunk * CHUNK + wave * ROWS;
+  const int r0 = chunk * CHUNK + wave * ROWS, rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS], dy[ROWS];
   Raw<G, V> g[ROWS];
+  Cursor at(p, rows > 0 ? r0 : p.R - 1);
+  int64_t yat = static_cast<int64_t>(rows > 0 ? r0 : p.R - 1) * p.C + c;
 #pragma unroll
   for (int j = 0; j < ROWS; ++j) {
-    const int r = r0 + j < p.R ? r0 + j : p.R - 1;
-    g[j].load(static_cast<const G*>(p.g) + row_offset(r, p, p.g_sb, p.g_sl) + c);
-    dy[j].load(static_cast<const T*>(p.dy) + static_cast<int64_t>(r) * p.C + c);
-    x[j].load(static_cast<const T*>(p.x) + row_offset(r, p, p.x_sb, p.x_sl) + c);
-    if (ING) in[j].load(static_cast<const T*>(p.i) + row_offset(r, p, p.i_sb, p.i_sl) + c);
+    g[j].load(static_cast<const G*>(p.g) + at.g + c);
+    x[j].load(static_cast<const T*>(p.x) + at.x + c);
+    if (ING) in[j].load(static_cast<const T*>(p.i) + at.i + c);
+    dy[j].load(static_cast<const T*>(p.dy) + yat);
+    if (j + 1 < rows) {
+      at.next(p);
+      yat += p.C;
+    }
   }
   Raw<float, V> dk;
-  if (GATE == LINREC_GATE_DECAY) dk.load(p.decay + c);
-  auto decay = [&](int v) { return GATE == LINREC_GATE_DECAY ? dk.get(v) : 0.f; };
-  const uint32_t starts = starts_at(p, r0);
-  const uint32_t lasts = starts >> 1 | (p.R - 1 - r0 < 32 && p.R > r0 ? 1u << (p.R - 1 - r0) : 0u);
-  float a[ROWS][V], h[ROWS][V];   // h: the state before each row, from a zero one
-  float A[V], H[V];
+  if (DECAY) dk.load(p.decay + c);
+  const uint32_t starts = starts_at(p, r0), ends = p.dfinal ? ends_at(p, r0, starts) : 0;
+  const bool cut = starts & ((1u << ROWS) - 1);
+  // Of every element: a; b and later the state before the row; e's gradients' factors, dx = e kx, di = e ki,
+  // dl = e (a h + kl), dg = dl kg, and ddecay's, dl ks
+  float a[ROWS][V], h[ROWS][V], kx[ROWS][V], ki[ROWS][V], kl[ROWS][V], kg[ROWS][V], ks[ROWS][V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f;
+  for (int v = 0; v < V; ++v) {
+    const Decay<T, GATE> d(DECAY ? dk.get(v) : 0.f);
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    if (r0 + j >= p.R) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) a[j][v] = 1.f, h[j][v] = 0.f;
-      continue;
-    }
-    if ((starts >> j) & 1u) {
-      const int s = p.h0 ? sequence_of(p, r0 + j) : -1;
-#pragma unroll
-      for (int v = 0; v < V; ++v) A[v] = 0.f, H[v] = s >= 0 ? p.h0[static_cast<int64_t>(s) * p.C + c + v] : 0.f;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const Gate q = gate_of<T, GATE, SCALE>(g[j].get(v), decay(v));
-      a[j][v] = q.a;
-      h[j][v] = H[v];
-      float u = x[j].get(v);
-      if (ING) u *= Fn<T>::sigmoid(in[j].get(v));
-      H[v] = fmaf(q.a, H[v], q.m * u);
-      A[v] *= q.a;
+    for (int j = 0; j < ROWS; ++j) {
+      const Factor f = factor_of<T, GATE, true>(g[j].get(v), d);
+      const float m = scale_of<T, GATE, SCALE>(f), xv = x[j].get(v);
+      float u = xv;
+      kx[j][v] = m;
+      ki[j][v] = 0.f;
+      if (ING) {
+        const float2 s = Fn<T>::sigmoids(in[j].get(v));
+        u *= s.x;
+        kx[j][v] = m * s.x;
+        ki[j][v] = m * u * s.y;
+      }
+      a[j][v] = f.a;
+      h[j][v] = m * u;
+      kl[j][v] = slope_of<T, SCALE>(f, m) * u;
+      kg[j][v] = GATE == LINREC_GATE_LOG ? 1.f : GATE == LINREC_GATE_SIGMOID ? f.rest : f.la * f.r;
+      ks[j][v] = f.s;
+#ifdef LR_SB
+      __builtin_amdgcn_sched_barrier(0);
+#endif
     }
   }
-  // what the wave hands on, from nothing
-  auto final_gradient = [&](int j, float (&e)[V]) {
-    if (p.dfinal && ((lasts >> j) & 1u)) {
+  float e[ROWS][V];   // dy, and what the final states add
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[j][v] = dy[j].get(v);
+    if ((ends >> j) & 1u) {
       const int s = sequence_of(p, r0 + j);
       if (s >= 0) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) e[v] += p.dfinal[static_cast<int64_t>(s) * p.C + c + v];
+        for (int v = 0; v < V; ++v) e[j][v] += p.dfinal[static_cast<int64_t>(s) * p.C + c + v];
       }
     }
-  };
-  float cr[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) cr[v] = 0.f;
-#pragma unroll
-  for (int j = ROWS - 1; j >= 0; --j) {
-    if (r0 + j >= p.R) continue;
-    float e[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = dy[j].get(v) + cr[v];
-    final_gradient(j, e);
-    const bool start = (starts >> j) & 1u;
-#pragma unroll
-    for (int v = 0; v < V; ++v) cr[v] = start ? 0.f : a[j][v] * e[v];
   }
-  const bool cut = starts & ((1u << ROWS) - 1);   // whatever its decays hold: nothing passes a sequence start, either way
+  if (rows < ROWS) {   // rows past the last hand on what they get
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      if (j >= rows) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[j][v] = 1.f, h[j][v] = e[j][v] = kl[j][v] = 0.f;
+      }
+    }
+  }
+  // The wave's factor and what a zero state becomes over it, and what it hands back from nothing.  A start drops the
+  // state by selection, so that nothing of it (a NaN either) passes, in either direction.
+  float A[V], H[V], cr[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = cr[v] = 0.f;
+  auto initial = [&](int j, float (&h0)[V]) {
+    const int s = p.h0 ? sequence_of(p, r0 + j) : -1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) h0[v] = s >= 0 ? p.h0[static_cast<int64_t>(s) * p.C + c + v] : 0.f;
+  };
+  auto gather = [&](auto with_starts) {
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      if (with_starts.value && ((starts >> j) & 1u)) initial(j, H);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        A[v] *= a[j][v];
+        H[v] = fmaf(a[j][v], H[v], h[j][v]);
+      }
+    }
+#pragma unroll
+    for (int j = ROWS - 1; j >= 0; --j) {
+      const bool start = with_starts.value && ((starts >> j) & 1u);
+#pragma unroll
+      for (int v = 0; v < V; ++v) cr[v] = start ? 0.f : a[j][v] * (e[j][v] + cr[v]);
+    }
+  };
+  if (cut) gather(std::true_type{});
+  else gather(std::false_type{});
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     fa[wave][lane * V + v] = cut ? 0.f : A[v];
@@ -105,11 +137,10 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   if (p.chunks == 1) __syncthreads();   // cuts is cleared
   if (lane == 0 && cut) cuts = 1;
   __syncthreads();
-  float hin[V], sum[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    hin[v] = chunk > 0 ? p.states[static_cast<int64_t>(chunk - 1) * p.C + c + v] : 0.f;
-    cr[v] = sum[v] = 0.f;
+    H[v] = chunk > 0 ? p.states[static_cast<int64_t>(chunk - 1) * p.C + c + v] : 0.f;
+    cr[v] = 0.f;
   }
   if (p.chunks > 1) {
     if (wave == 0) {
@@ -135,87 +166,71 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   }
   for (int w = 0; w < wave; ++w) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) hin[v] = onto(fa[w][lane * V + v], fh[w][lane * V + v], hin[v]);
+    for (int v = 0; v < V; ++v) H[v] = onto(fa[w][lane * V + v], fh[w][lane * V + v], H[v]);
   }
   for (int w = WAVES - 1; w > wave; --w) {
 #pragma unroll
     for (int v = 0; v < V; ++v) cr[v] = onto(fa[w][lane * V + v], fc[w][lane * V + v], cr[v]);
   }
-  // the states before the rows up to the first start get what is left of the entering one
-  float left[V];
+  float sum[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) left[v] = hin[v];
-  bool inside = true;
+  for (int v = 0; v < V; ++v) sum[v] = 0.f;
+  int64_t out = (static_cast<int64_t>(r0) + ROWS - 1) * p.C + c;
+  auto walk = [&](auto with_starts) {
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    if ((starts >> j) & 1u) inside = false;
-    if (inside) {
+    for (int j = 0; j < ROWS; ++j) {   // h: from what a row adds to the state before it
+      if (with_starts.value && ((starts >> j) & 1u)) initial(j, H);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        h[j][v] += left[v];
-        left[v] *= a[j][v];
+        const float add = h[j][v];
+        h[j][v] = H[v];
+        H[v] = fmaf(a[j][v], H[v], add);
       }
     }
-  }
 #pragma unroll
-  for (int j = ROWS - 1; j >= 0; --j) {
-    const int r = r0 + j;
-    if (r >= p.R) continue;
-    float e[V], ox[V], og[V], oi[V];
-    const bool start = (starts >> j) & 1u;
+    for (int j = ROWS - 1; j >= 0; --j) {
+      float ox[V], og[V], oi[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = dy[j].get(v) + cr[v];
-    final_gradient(j, e);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const Gate q = gate_of<T, GATE, SCALE>(g[j].get(v), decay(v));
-      const float xv = x[j].get(v);
-      float si = 1.f, ri = 0.f;
-      if (ING) {
-        const float2 sr = Fn<T>::sigmoids(in[j].get(v));
-        si = sr.x;
-        ri = sr.y;
+      for (int v = 0; v < V; ++v) {
+        const float ev = e[j][v] + cr[v], dl = ev * (SCALE == LINREC_INPUT_ONE ? a[j][v] * h[j][v] : fmaf(a[j][v], h[j][v], kl[j][v]));
+        ox[v] = ev * kx[j][v];
+        if (ING) oi[v] = ev * ki[j][v];
+        og[v] = dl * kg[j][v];
+        if (DECAY && j < rows) sum[v] = fmaf(dl, ks[j][v], sum[v]);
+        cr[v] = a[j][v] * ev;
       }
-      const float u = xv * si, du = q.m * e[v];
-      const float dl = e[v] * fmaf(q.a, h[j][v], q.dm * u);
-      ox[v] = du * si;
-      oi[v] = du * u * ri;
-      og[v] = dl * q.dg;
-      sum[v] += dl * q.sg;
-      cr[v] = q.a * e[v];
-    }
-    if (live) {
-      const int64_t at = static_cast<int64_t>(r) * p.C + c;
-      Raw<T, V> o;
-      o.set(ox);
-      o.store(static_cast<T*>(p.dx) + at);
-      Raw<G, V> og_;
-      og_.set(og);
-      og_.store(static_cast<G*>(p.dg) + at);
-      if (ING) {
-        o.set(oi);
-        o.store(static_cast<T*>(p.di) + at);
+      if (live && j < rows) {
+        Raw<T, V> o;
+        o.set(ox);
+        o.store(static_cast<T*>(p.dx) + out);
+        Raw<G, V> q;
+        q.set(og);
+        q.store(static_cast<G*>(p.dg) + out);
+        if (ING) {
+          o.set(oi);
+          o.store(static_cast<T*>(p.di) + out);
+        }
       }
-      if (start && p.dh0) {
-        const int s = sequence_of(p, r);
-        if (s >= 0) {
+      out -= p.C;
+      if (with_starts.value && ((starts >> j) & 1u)) {
+        const int s = p.dh0 ? sequence_of(p, r0 + j) : -1;
 #pragma unroll
-          for (int v = 0; v < V; ++v) p.dh0[static_cast<int64_t>(s) * p.C + c + v] = cr[v];
+        for (int v = 0; v < V; ++v) {
+          if (live && s >= 0) p.dh0[static_cast<int64_t>(s) * p.C + c + v] = cr[v];
+          cr[v] = 0.f;
         }
       }
     }
-    if (start) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) cr[v] = 0.f;
-    }
-  }
+  };
+  if (cut) walk(std::true_type{});
+  else walk(std::false_type{});
   if (p.dh0 && p.seq_idx && chunk == 0 && wave == 0 && live) {   // numbered sequences past the last one
     for (int s = p.nseqs - 1; s >= 0 && p.starts[s] >= p.R; --s) {
 #pragma unroll
       for (int v = 0; v < V; ++v) p.dh0[static_cast<int64_t>(s) * p.C + c + v] = p.dfinal ? p.dfinal[static_cast<int64_t>(s) * p.C + c + v] : 0.f;
     }
   }
-  if constexpr (GATE == LINREC_GATE_DECAY) {
+  if constexpr (DECAY) {
     if (p.ddecay) {
       __syncthreads();
 #pragma unroll
@@ -254,7 +269,8 @@ __global__ __launch_bounds__(RED_COLS * RED_ROWS) void k_linrec_reduce(Problem p
 }
 
 namespace {
-template <typename T, int GATE, int SCALE, bool ING> int go(const Problem& p, hipStream_t st) {
+template <typename T, int GATE, int SCALE, bool ING> int go(Problem p, hipStream_t st) {
+  p.cblocks = (p.C + 64 * VALS<T, true> - 1) / (64 * VALS<T, true>);
   hipLaunchKernelGGL((k_linrec_bwd<T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(THR), 0, st, p);
   if (GATE == LINREC_GATE_DECAY && p.ddecay)
     hipLaunchKernelGGL(k_linrec_reduce, dim3(static_cast<unsigned>((p.C + RED_COLS - 1) / RED_COLS)), dim3(RED_COLS * RED_ROWS), 0, st, p);

@@ -20,7 +20,7 @@ struct StepArgs {
 };
 
 template <typename T, int GATE, int SCALE> __global__ __launch_bounds__(64) void k_linrec_step(StepArgs s) {
-  constexpr int V = VALS<T>;
+  constexpr int V = VALS<T, false>;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
   const int l = static_cast<int>(threadIdx.x);
   const int c0 = (static_cast<int>(blockIdx.x) * 64 + l) * V;
@@ -74,10 +74,10 @@ template <typename T, int GATE, int SCALE> __global__ __launch_bounds__(64) void
       if (t + 1 < s.T) request(t + 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Gate q = gate_of<T, GATE, SCALE>(g0.get(v), GATE == LINREC_GATE_DECAY ? dk.get(v) : 0.f);
+        const Factor f = factor_of<T, GATE, false>(g0.get(v), Decay<T, GATE>(GATE == LINREC_GATE_DECAY ? dk.get(v) : 0.f));
         float u = x0.get(v);
         if (s.i) u *= Fn<T>::sigmoid(i0.get(v));
-        h[v] = fmaf(q.a, h[v], q.m * u);
+        h[v] = fmaf(f.a, h[v], scale_of<T, GATE, SCALE>(f) * u);
       }
       Raw<T, V> out;
       out.set(h);
@@ -91,7 +91,7 @@ template <typename T, int GATE, int SCALE> __global__ __launch_bounds__(64) void
 
 namespace {
 template <typename T, int GATE> int by_scale(const StepArgs& s, int scale, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>((s.C + 64 * VALS<T> - 1) / (64 * VALS<T>)), static_cast<unsigned>(s.B));
+  const dim3 grid(static_cast<unsigned>((s.C + 64 * VALS<T, false> - 1) / (64 * VALS<T, false>)), static_cast<unsigned>(s.B));
   switch (scale) {
     case LINREC_INPUT_ONE: hipLaunchKernelGGL((k_linrec_step<T, GATE, LINREC_INPUT_ONE>), grid, dim3(64), 0, st, s); break;
     case LINREC_INPUT_COMPLEMENT: hipLaunchKernelGGL((k_linrec_step<T, GATE, LINREC_INPUT_COMPLEMENT>), grid, dim3(64), 0, st, s); break;

@@ -45,7 +45,7 @@ size_t place(Problem& p, bool backward, char* base) {
   };
   const size_t n = static_cast<size_t>(p.chunks) * p.C;
   p.starts = reinterpret_cast<int32_t*>(take((2 * static_cast<size_t>(p.nseqs) + 1) * 4));
-  p.sync = reinterpret_cast<uint32_t*>(take((static_cast<size_t>(p.chunks) * p.cblocks + 1) * 4));
+  p.sync = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(p.cblocks) * (p.chunks + linrec::LINE) * 4));
   p.agg = reinterpret_cast<float2*>(take(n * sizeof(float2)));
   p.states = reinterpret_cast<float*>(take(n * 4));
   if (backward) {
@@ -63,7 +63,8 @@ int problem(const linrec_shape* s, Problem& p) {
   p.C = static_cast<int>(s->channels);
   p.nseqs = static_cast<int>(s->nseqs);
   p.chunks = (p.R + linrec::CHUNK - 1) / linrec::CHUNK;
-  const int cb = 64 * (s->io_dtype == SSD_IO_BF16 ? linrec::VALS<ssd::bf16_t> : linrec::VALS<float>);
+  // the backward's, which are the narrower: what is sized by them is enough for the forward's
+  const int cb = 64 * (s->io_dtype == SSD_IO_BF16 ? linrec::VALS<ssd::bf16_t, true> : linrec::VALS<float, true>);
   p.cblocks = (p.C + cb - 1) / cb;
   if (static_cast<int64_t>(p.chunks) * p.cblocks > INT_MAX / 2) return SSD_ERR_UNSUPPORTED_SHAPE;
   int64_t st[6];
@@ -85,8 +86,6 @@ int inputs(const linrec_shape* shape, const void* x, const void* g, const void* 
   for (const void* q : {x, g, in_gate, static_cast<const void*>(decay), static_cast<const void*>(h0), static_cast<const void*>(workspace)})
     if (misaligned(q)) return SSD_ERR_MISALIGNED;
   p.x = x; p.g = g; p.i = in_gate; p.decay = decay; p.h0 = h0; p.seq_idx = seq_idx;
-  const int64_t L = p.L;
-  p.flat = p.x_sb == L * p.x_sl && p.g_sb == L * p.g_sl && (!in_gate || p.i_sb == L * p.i_sl);
   if (!seq_idx || !states) p.starts = nullptr;
   return SSD_OK;
 }

@@ -10,14 +10,28 @@
 
 namespace linrec {
 
-// A chunk's rows by a block: WAVES waves of ROWS rows each; a lane holds 8 bytes of x of each row.
-constexpr int ROWS = 8, WAVES = 8, CHUNK = ROWS * WAVES, THR = 64 * WAVES;
-template <typename T> constexpr int VALS = 8 / static_cast<int>(sizeof(T));
+// A chunk's rows by a block: WAVES waves of ROWS rows each.  A lane holds 8 bytes of x of each row in the forward, 4 in
+// the backward, which keeps up to seven values of every element over the chunks' chain and not two.
+#ifndef LR_ROWS
+#define LR_ROWS 8
+#endif
+#ifndef LR_WAVES
+#define LR_WAVES 8
+#endif
+#ifndef LR_FNB
+#define LR_FNB 8
+#endif
+#ifndef LR_BNB
+#define LR_BNB 4
+#endif
+constexpr int ROWS = LR_ROWS, WAVES = LR_WAVES, CHUNK = ROWS * WAVES, THR = 64 * WAVES;
+template <typename T, bool BWD> constexpr int VALS = (BWD ? LR_BNB : LR_FNB) / static_cast<int>(sizeof(T));
+
+constexpr int LINE = 32;   // words of a cache line
 
 struct Problem {
   int R, L, C, nseqs;      // rows (batch * seqlen), rows of a batch row, channels, sequences
   int chunks, cblocks;     // chunks of CHUNK rows, blocks of 64 VALS channels
-  int flat;                // batch rows follow each other at the row strides
   int64_t x_sb, x_sl, g_sb, g_sl, i_sb, i_sl;
   // inputs
   const void *x, *g, *i, *dy;
@@ -28,7 +42,7 @@ struct Problem {
   float *final, *ddecay, *dh0;
   // workspace
   int32_t* starts;         // (nseqs + 1) first rows (seq_idx and states given), then nseqs more that only k_delta_starts reads
-  uint32_t* sync;          // the next ticket, then (chunks, cblocks): what of a chunk is there
+  uint32_t* sync;          // (cblocks, LINE): tickets; (cblocks, chunks): what of a chunk is there
   float2* agg;             // (chunks, C): a chunk's factor and what it adds
   float* states;           // (chunks, C): the state after each chunk
   float* carry;            // (chunks, C): what a chunk hands to the rows before it (backward)
@@ -60,65 +74,73 @@ template <typename S, int V> struct Raw {
 // With bf16 io the hardware's exponential, reciprocal and root (1 ulp); with float32 io the library's.
 template <typename T> struct Fn {
   static constexpr bool FAST = sizeof(T) == 2;
-  static __device__ __forceinline__ float exp(float x) { return FAST ? __expf(x) : expf(x); }
+  static constexpr float LOG2E = 1.4426950408889634f;
+  static __device__ __forceinline__ float exp(float x) { return FAST ? __builtin_amdgcn_exp2f(x * LOG2E) : expf(x); }
   static __device__ __forceinline__ float rcp(float x) { return FAST ? __builtin_amdgcn_rcpf(x) : 1.f / x; }
   static __device__ __forceinline__ float sqrt(float x) { return FAST ? __builtin_amdgcn_sqrtf(x) : sqrtf(x); }
   static __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + exp(-x)); }
-  // sigmoid(x) and 1 - sigmoid(x), both to their last bits
+  // sigmoid(x) and 1 - sigmoid(x), both to their last bits: with e = exp(-x) the latter is e sigmoid(x) where x > 0
   static __device__ __forceinline__ float2 sigmoids(float x) {
-    const float e = exp(-fabsf(x)), big = rcp(1.f + e), small = e * big;
-    return x < 0.f ? float2{small, big} : float2{big, small};
+    const float e = exp(-x), s = rcp(1.f + e);
+    return float2{s, x > 0.f ? e * s : 1.f - s};
   }
-  // 1 - exp(y) from e = exp(y): for y above -1/2 by the series -y (1 + y/2 (1 + y/3 (...))), whose eighth term is
-  // below 2^-22 of the sum there; below it 1 - e loses at most one bit
-  static __device__ __forceinline__ float one_minus(float y, float e) {
-    float s = 1.f + y * (1.f / 8.f);
-    s = fmaf(s, y * (1.f / 7.f), 1.f);
-    s = fmaf(s, y * (1.f / 6.f), 1.f);
-    s = fmaf(s, y * (1.f / 5.f), 1.f);
-    s = fmaf(s, y * (1.f / 4.f), 1.f);
-    s = fmaf(s, y * (1.f / 3.f), 1.f);
-    s = fmaf(s, y * (1.f / 2.f), 1.f);
-    return y > -0.5f ? -y * s : 1.f - e;
+  // 1 - exp(y), y <= 0, from its direct form: above -1/2 as -y times the polynomial of degree 5 that is nearest to
+  // (exp(y) - 1) / y there (off by 7e-9 of it, found by exchange), below it the difference loses at most one bit
+  static __device__ __forceinline__ float one_minus(float y, float direct) {
+    float q = fmaf(1.1216348502784967e-3f, y, 8.187386207282543e-3f);
+    q = fmaf(q, y, 4.1629090905189514e-2f);
+    q = fmaf(q, y, 1.6666224598884583e-1f);
+    q = fmaf(q, y, 4.999998211860657e-1f);
+    q = fmaf(q, y, 1.f);
+    return y > -0.5f ? -y * q : direct;
   }
 };
 
-struct Gate {
-  float a, m;       // decay and input factor
-  float dm;         // of m by the log decay
-  float dg;         // of the log decay by g
-  float sg;         // sigmoid(g) (LINREC_GATE_DECAY)
+// A channel's decay as its gates use it
+template <typename T, int GATE> struct Decay {
+  float k, k2;   // decay, and times log2(e): exp by the hardware's exp2 takes its argument from one product
+  __device__ __forceinline__ explicit Decay(float decay) : k(decay), k2(decay * Fn<T>::LOG2E) {}
 };
-template <typename T, int GATE, int SCALE> __device__ __forceinline__ Gate gate_of(float g, float decay) {
+
+// Decay a, its logarithm la, 1 - a where the gate gives it, sigmoid(g) and 1 - it (LINREC_GATE_DECAY; SLOPES)
+struct Factor {
+  float a, la, rest, s, r;
+};
+template <typename T, int GATE, bool SLOPES> __device__ __forceinline__ Factor factor_of(float g, Decay<T, GATE> d) {
   using F = Fn<T>;
-  Gate q;
-  float la = g, rest = 0.f;   // the log decay, 1 - a
-  q.sg = 0.f;
-  if constexpr (GATE == LINREC_GATE_SIGMOID) {
+  Factor f{};
+  if constexpr (GATE == LINREC_GATE_LOG) {
+    f.la = g;
+    f.a = F::exp(g);
+  } else if constexpr (GATE == LINREC_GATE_SIGMOID) {
     const float2 s = F::sigmoids(g);
-    q.a = s.x;
-    q.dg = rest = s.y;
+    f.a = s.x;
+    f.rest = s.y;
   } else {
-    q.dg = 1.f;
-    if constexpr (GATE == LINREC_GATE_DECAY) {
+    if (SLOPES) {
       const float2 s = F::sigmoids(g);
-      q.sg = s.x;
-      la = decay * q.sg;
-      q.dg = la * s.y;
+      f.s = s.x;
+      f.r = s.y;
+    } else {
+      f.s = F::sigmoid(g);
     }
-    q.a = F::exp(la);
+    f.la = d.k * f.s;
+    f.a = F::FAST ? __builtin_amdgcn_exp2f(d.k2 * f.s) : F::exp(f.la);
   }
-  if constexpr (SCALE == LINREC_INPUT_ONE) {
-    q.m = 1.f;
-    q.dm = 0.f;
-  } else if constexpr (SCALE == LINREC_INPUT_COMPLEMENT) {
-    q.m = GATE == LINREC_GATE_SIGMOID ? rest : F::one_minus(la, q.a);
-    q.dm = -q.a;
-  } else {
-    q.m = F::sqrt(GATE == LINREC_GATE_SIGMOID ? rest * (1.f + q.a) : F::one_minus(2.f * la, q.a * q.a));
-    q.dm = q.m == 0.f ? 0.f : -q.a * q.a * F::rcp(q.m);
-  }
-  return q;
+  return f;
+}
+// the input's factor m
+template <typename T, int GATE, int SCALE> __device__ __forceinline__ float scale_of(const Factor& f) {
+  using F = Fn<T>;
+  if constexpr (SCALE == LINREC_INPUT_ONE) return 1.f;
+  else if constexpr (SCALE == LINREC_INPUT_COMPLEMENT) return GATE == LINREC_GATE_SIGMOID ? f.rest : F::one_minus(f.la, 1.f - f.a);
+  else return F::sqrt(GATE == LINREC_GATE_SIGMOID ? fmaf(f.rest, f.a, f.rest) : F::one_minus(2.f * f.la, fmaf(-f.a, f.a, 1.f)));
+}
+// its derivative by the log decay
+template <typename T, int SCALE> __device__ __forceinline__ float slope_of(const Factor& f, float m) {
+  if constexpr (SCALE == LINREC_INPUT_ONE) return 0.f;
+  else if constexpr (SCALE == LINREC_INPUT_COMPLEMENT) return -f.a;
+  else return m == 0.f ? 0.f : -f.a * f.a * Fn<T>::rcp(m);
 }
 
 // a chunk or part of it on a state: what decayed to nothing is dropped, so nothing of it (a NaN either) passes on
@@ -150,11 +172,13 @@ __device__ __forceinline__ float2 take(const float2* p) {
   return __builtin_bit_cast(float2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 
-// The place of the block in the chain times cblocks, plus its channel block; the same in all threads.
-__device__ __forceinline__ uint32_t ticket(const Problem& p) {
+// A block's channel block (blocks that follow each other take different ones), and its place in that one's chain: the next
+// of its ticket counter.  Counters of their own, a cache line apart: one for all blocks served a ticket every 13 ns.
+__device__ __forceinline__ int channel_block(const Problem& p) { return static_cast<int>(blockIdx.x % p.cblocks); }
+__device__ __forceinline__ int ticket(const Problem& p, int cb) {
   __shared__ uint32_t t;
-  if (p.chunks == 1) return blockIdx.x;
-  if (threadIdx.x == 0) t = __hip_atomic_fetch_add(p.sync, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (p.chunks == 1) return 0;
+  if (threadIdx.x == 0) t = __hip_atomic_fetch_add(p.sync + static_cast<int64_t>(cb) * LINE, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   return __builtin_amdgcn_readfirstlane(t);
 }
@@ -166,9 +190,10 @@ __device__ __forceinline__ void join(const Problem& p, float* after, int place, 
                                      const float (&H)[V], float (&before)[V], ChunkAt chunk_at) {
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int64_t mine = static_cast<int64_t>(chunk_at(place)) * p.C + c;
+  uint32_t* marks = p.sync + static_cast<int64_t>(p.cblocks) * LINE + static_cast<int64_t>(cb) * p.chunks;
   auto mark = [&](uint32_t m) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the values have arrived
-    if (lane == 0) __hip_atomic_store(p.sync + 1 + static_cast<int64_t>(place) * p.cblocks + cb, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (lane == 0) __hip_atomic_store(marks + place, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
   auto leave = [&](const float (&h)[V]) {
     if (live) {
@@ -193,7 +218,7 @@ __device__ __forceinline__ void join(const Problem& p, float* after, int place, 
     for (;;) {
       const int at = place - 1 - lane;
       uint32_t m = WHOLE;   // before the first chunk: a state of zero
-      if (at >= 0) m = __hip_atomic_load(p.sync + 1 + static_cast<int64_t>(at) * p.cblocks + cb, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (at >= 0) m = __hip_atomic_load(marks + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       const uint64_t whole = __ballot(m == WHOLE), nothing = __ballot(m == NOTHING);
       if (whole) {
         back = __builtin_ctzll(whole);
@@ -236,18 +261,41 @@ __device__ __forceinline__ void join(const Problem& p, float* after, int place, 
   }
 }
 
-__device__ __forceinline__ int64_t row_offset(int row, const Problem& p, int64_t sb, int64_t sl) {
-  if (p.flat) return row * sl;
-  const int b = row / p.L;
-  return b * sb + (row - b * p.L) * sl;
-}
+// Where a wave's row lies in x, g and in_gate, from row to row
+struct Cursor {
+  int64_t x, g, i;
+  int t;   // row of its batch row
+  __device__ __forceinline__ Cursor(const Problem& p, int row) {
+    const int b = row / p.L;
+    t = row - b * p.L;
+    x = b * p.x_sb + t * p.x_sl;
+    g = b * p.g_sb + t * p.g_sl;
+    i = b * p.i_sb + t * p.i_sl;
+  }
+  __device__ __forceinline__ void next(const Problem& p) {
+    x += p.x_sl;
+    g += p.g_sl;
+    i += p.i_sl;
+    if (++t == p.L) {   // the next batch row's first
+      t = 0;
+      x += p.x_sb - p.L * p.x_sl;
+      g += p.g_sb - p.L * p.g_sl;
+      i += p.i_sb - p.L * p.i_sl;
+    }
+  }
+};
 
-// bit j: a sequence starts at row r0 + j (j <= ROWS)
+// bit j: a sequence starts at row r0 + j (j <= ROWS; the last bit tells whether the wave's last row ends one)
 __device__ __forceinline__ uint32_t starts_at(const Problem& p, int r0) {
   const int j = static_cast<int>(threadIdx.x) & 63, r = r0 + j;
   bool s = false;
   if (j <= ROWS && r < p.R) s = r % p.L == 0 || (p.seq_idx && p.seq_idx[r] != p.seq_idx[r - 1]);
   return static_cast<uint32_t>(__ballot(s));
+}
+
+// bit j: row r0 + j is the last of its sequence
+__device__ __forceinline__ uint32_t ends_at(const Problem& p, int r0, uint32_t starts) {
+  return starts >> 1 | (r0 < p.R && p.R - r0 <= ROWS ? 1u << (p.R - 1 - r0) : 0u);
 }
 
 // the sequence of row r, or -1 past the last numbered one
@@ -264,3 +312,9 @@ __device__ __forceinline__ int sequence_of(const Problem& p, int r) {
 #endif
 
 }  // namespace linrec
+#ifndef BWD_OCC
+#define BWD_OCC
+#endif
+#ifndef FWD_OCC
+#define FWD_OCC
+#endif

@@ -21,18 +21,17 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   const int lane = ssd::lane_id(), wave = ssd::wave_id_s();
   if (threadIdx.x == 0) cuts = 0;
   const int cb = channel_block(p), chunk = ticket(p, cb);
-  const int c0 = cb * CB + lane * V;
-  const bool live = c0 < p.C;
-  const int c = live ? c0 : p.C - V;
+  // lanes past the last channels take those again: they write the same values to the same places
+  const int c = cb * CB + lane * V < p.C ? cb * CB + lane * V : p.C - V;
   const int r0 = chunk * CHUNK + wave * ROWS, rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS];
   Raw<G, V> g[ROWS];
   Cursor at(p, rows > 0 ? r0 : p.R - 1);
 #pragma unroll
   for (int j = 0; j < ROWS; ++j) {
-    x[j].load(static_cast<const T*>(p.x) + at.x + c);
-    g[j].load(static_cast<const G*>(p.g) + at.g + c);
-    if (ING) in[j].load(static_cast<const T*>(p.i) + at.i + c);
+    x[j].load_at(p.x, at.x, c);
+    g[j].load_at(p.g, at.g, c);
+    if (ING) in[j].load_at(p.i, at.i, c);
     if (j + 1 < rows) at.next(p);
   }
   Raw<float, V> dk;
@@ -45,7 +44,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
     const Decay<T, GATE> d(GATE == LINREC_GATE_DECAY ? dk.get(v) : 0.f);
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      const Factor f = factor_of<T, GATE, false>(g[j].get(v), d);
+      const Factor f = factor_of<T, GATE>(g[j].get(v), d);
       float u = x[j].get(v);
       if (ING) u *= Fn<T>::sigmoid(in[j].get(v));
       a[j][v] = f.a;
@@ -111,7 +110,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
           H[v] = onto(f, fh[w][lane * V + v], H[v]);
         }
       }
-      join<V>(p, p.states, chunk, cb, c, live, cuts != 0, A, H, h, [](int k) { return k; });
+      join<V>(p, p.states, chunk, cb, c, cuts != 0, A, H, h, [](int k) { return k; });
 #pragma unroll
       for (int v = 0; v < V; ++v) enter[lane * V + v] = h[v];
     }
@@ -124,19 +123,19 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = onto(fa[w][lane * V + v], fh[w][lane * V + v], h[v]);
   }
-  T* y = static_cast<T*>(p.y) + static_cast<int64_t>(r0) * p.C + c;
+  int64_t y = static_cast<int64_t>(r0) * p.C;
   const uint32_t ends = p.final ? ends_at(p, r0, starts) : 0;
-  auto walk = [&](auto with_starts) {
+  auto walk = [&](auto all) {   // all rows are there, and none begins or ends a sequence that matters
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      const bool start = with_starts.value && ((starts >> j) & 1u);
+      const bool start = !all.value && ((starts >> j) & 1u);
 #pragma unroll
       for (int v = 0; v < V; ++v) h[v] = start ? b[j][v] : fmaf(a[j][v], h[v], b[j][v]);
-      if (live && j < rows) {
+      if (all.value || j < rows) {
         Raw<T, V> out;
         out.set(h);
-        out.store(y);
-        if (with_starts.value && ((ends >> j) & 1u)) {
+        out.store_at(p.y, y, c);
+        if (!all.value && ((ends >> j) & 1u)) {
           const int s = sequence_of(p, r0 + j);
           if (s >= 0) {
             Raw<float, V> f;
@@ -148,10 +147,10 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
       y += p.C;
     }
   };
-  if (cut || ends) walk(std::true_type{});
-  else walk(std::false_type{});
+  if (cut || ends || rows < ROWS) walk(std::false_type{});
+  else walk(std::true_type{});
   // numbered sequences past the last one
-  if (p.final && p.seq_idx && chunk == 0 && wave == 0 && live) {
+  if (p.final && p.seq_idx && chunk == 0 && wave == 0) {
     for (int s = p.nseqs - 1; s >= 0 && p.starts[s] >= p.R; --s) {
 #pragma unroll
       for (int v = 0; v < V; ++v) p.final[static_cast<int64_t>(s) * p.C + c + v] = p.h0 ? p.h0[static_cast<int64_t>(s) * p.C + c + v] : 0.f;

@@ -15,7 +15,7 @@ namespace linrec {
 
 using ssd::bf16_t;
 
-template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(THR) BWD_OCC void k_linrec_bwd(Problem p) {
+template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(THR) void k_linrec_bwd(Problem p) {
   constexpr int V = VALS<T, true>, CB = 64 * V;
   constexpr bool DECAY = GATE == LINREC_GATE_DECAY;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
@@ -25,80 +25,75 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   if (threadIdx.x == 0) cuts = 0;
   const int cb = channel_block(p), place = ticket(p, cb);
   const int chunk = p.chunks - 1 - place;   // from the end
-  const int c0 = cb * CB + lane * V;
-  const bool live = c0 < p.C;
-  const int c = live ? c0 : p.C - V;
+  // lanes past the last channels take those again: they write the same values to the same places
+  const int c = cb * CB + lane * V < p.C ? cb * CB + lane * V : p.C - V;
   const int r0 = chunk * CHUNK + wave * ROWS, rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS], dy[ROWS];
   Raw<G, V> g[ROWS];
   Cursor at(p, rows > 0 ? r0 : p.R - 1);
-  int64_t yat = static_cast<int64_t>(rows > 0 ? r0 : p.R - 1) * p.C + c;
+  int64_t yat = static_cast<int64_t>(rows > 0 ? r0 : p.R - 1) * p.C;
 #pragma unroll
   for (int j = 0; j < ROWS; ++j) {
-    g[j].load(static_cast<const G*>(p.g) + at.g + c);
-    x[j].load(static_cast<const T*>(p.x) + at.x + c);
-    if (ING) in[j].load(static_cast<const T*>(p.i) + at.i + c);
-    dy[j].load(static_cast<const T*>(p.dy) + yat);
+    g[j].load_at(p.g, at.g, c);
+    x[j].load_at(p.x, at.x, c);
+    if (ING) in[j].load_at(p.i, at.i, c);
+    dy[j].load_at(p.dy, yat, c);
     if (j + 1 < rows) {
       at.next(p);
       yat += p.C;
     }
   }
-  Raw<float, V> dk;
-  if (DECAY) dk.load(p.decay + c);
   const uint32_t starts = starts_at(p, r0), ends = p.dfinal ? ends_at(p, r0, starts) : 0;
   const bool cut = starts & ((1u << ROWS) - 1);
-  // Of every element: a; b and later the state before the row; e's gradients' factors, dx = e kx, di = e ki,
-  // dl = e (a h + kl), dg = dl kg, and ddecay's, dl ks
-  float a[ROWS][V], h[ROWS][V], kx[ROWS][V], ki[ROWS][V], kl[ROWS][V], kg[ROWS][V], ks[ROWS][V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const Decay<T, GATE> d(DECAY ? dk.get(v) : 0.f);
-#pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-      const Factor f = factor_of<T, GATE, true>(g[j].get(v), d);
-      const float m = scale_of<T, GATE, SCALE>(f), xv = x[j].get(v);
-      float u = xv;
-      kx[j][v] = m;
-      ki[j][v] = 0.f;
-      if (ING) {
-        const float2 s = Fn<T>::sigmoids(in[j].get(v));
-        u *= s.x;
-        kx[j][v] = m * s.x;
-        ki[j][v] = m * u * s.y;
-      }
-      a[j][v] = f.a;
-      h[j][v] = m * u;
-      kl[j][v] = slope_of<T, SCALE>(f, m) * u;
-      kg[j][v] = GATE == LINREC_GATE_LOG ? 1.f : GATE == LINREC_GATE_SIGMOID ? f.rest : f.la * f.r;
-      ks[j][v] = f.s;
-#ifdef LR_SB
-      __builtin_amdgcn_sched_barrier(0);
-#endif
-    }
-  }
-  float e[ROWS][V];   // dy, and what the final states add
+  // Of every element its decay, its input factor, and what it adds to the state, later the state before it; and in LDS the
+  // sigmoids of its gates: the lane's registers for them as well would leave room for one block a CU.
+  constexpr bool KEEP_G = GATE != LINREC_GATE_LOG;
+  constexpr int KEPT = (KEEP_G ? V : 0) + (ING ? V : 0);
+  __shared__ __attribute__((aligned(16))) float kept[KEPT ? ROWS * THR * KEPT : 1];
+  float* mine = kept + static_cast<int>(threadIdx.x) * KEPT;   // row j: THR KEPT j further
+  float a[ROWS][V], m[ROWS][V], h[ROWS][V];
+  Raw<float, V> dk;
+  if (DECAY) dk.load(p.decay + c);
 #pragma unroll
   for (int j = 0; j < ROWS; ++j) {
+    float k[KEPT + 1];
 #pragma unroll
-    for (int v = 0; v < V; ++v) e[j][v] = dy[j].get(v);
-    if ((ends >> j) & 1u) {
-      const int s = sequence_of(p, r0 + j);
-      if (s >= 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) e[j][v] += p.dfinal[static_cast<int64_t>(s) * p.C + c + v];
-      }
+    for (int v = 0; v < V; ++v) {
+      const Decay<T, GATE> d(DECAY ? dk.get(v) : 0.f);
+      float2 s{0.f, 0.f};
+      float u = x[j].get(v);
+      if (KEEP_G) s.x = Fn<T>::sigmoid(g[j].get(v), k[v]);
+      if (GATE == LINREC_GATE_SIGMOID) s.y = Fn<T>::both_of(k[v]).y;
+      if (ING) u *= Fn<T>::sigmoid(in[j].get(v), k[(KEEP_G ? V : 0) + v]);
+      const Factor f = factor_of<T, GATE>(g[j].get(v), s, d);
+      a[j][v] = f.a;
+      m[j][v] = scale_of<T, GATE, SCALE>(f);
+      h[j][v] = m[j][v] * u;
     }
+#pragma unroll
+    for (int i = 0; i < KEPT; ++i) mine[THR * KEPT * j + i] = k[i];
   }
   if (rows < ROWS) {   // rows past the last hand on what they get
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
       if (j >= rows) {
+        dy[j].w = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v) a[j][v] = 1.f, h[j][v] = e[j][v] = kl[j][v] = 0.f;
+        for (int v = 0; v < V; ++v) a[j][v] = 1.f, h[j][v] = 0.f;
       }
     }
   }
+  auto gradient_of = [&](auto all, int j, float (&e)[V]) {   // dy, and the final state's where a sequence ends
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = dy[j].get(v);
+    if (!all.value && ((ends >> j) & 1u)) {
+      const int s = sequence_of(p, r0 + j);
+      if (s >= 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) e[v] += p.dfinal[static_cast<int64_t>(s) * p.C + c + v];
+      }
+    }
+  };
   // The wave's factor and what a zero state becomes over it, and what it hands back from nothing.  A start drops the
   // state by selection, so that nothing of it (a NaN either) passes, in either direction.
   float A[V], H[V], cr[V];
@@ -109,10 +104,10 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
 #pragma unroll
     for (int v = 0; v < V; ++v) h0[v] = s >= 0 ? p.h0[static_cast<int64_t>(s) * p.C + c + v] : 0.f;
   };
-  auto gather = [&](auto with_starts) {
+  auto gather = [&](auto all) {   // all rows are there, and none begins or ends a sequence that matters
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      if (with_starts.value && ((starts >> j) & 1u)) initial(j, H);
+      if (!all.value && ((starts >> j) & 1u)) initial(j, H);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         A[v] *= a[j][v];
@@ -121,13 +116,16 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
     }
 #pragma unroll
     for (int j = ROWS - 1; j >= 0; --j) {
-      const bool start = with_starts.value && ((starts >> j) & 1u);
+      const bool start = !all.value && ((starts >> j) & 1u);
+      float e[V];
+      gradient_of(all, j, e);
 #pragma unroll
-      for (int v = 0; v < V; ++v) cr[v] = start ? 0.f : a[j][v] * (e[j][v] + cr[v]);
+      for (int v = 0; v < V; ++v) cr[v] = start ? 0.f : a[j][v] * (e[v] + cr[v]);
     }
   };
-  if (cut) gather(std::true_type{});
-  else gather(std::false_type{});
+  const bool some = cut || ends || rows < ROWS;
+  if (some) gather(std::false_type{});
+  else gather(std::true_type{});
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     fa[wave][lane * V + v] = cut ? 0.f : A[v];
@@ -156,7 +154,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
         }
       }
       const int last = p.chunks - 1;
-      join<V>(p, p.carry, place, cb, c, live, cuts != 0, A, B, cr, [last](int k) { return last - k; });
+      join<V>(p, p.carry, place, cb, c, cuts != 0, A, B, cr, [last](int k) { return last - k; });
 #pragma unroll
       for (int v = 0; v < V; ++v) enter[lane * V + v] = cr[v];
     }
@@ -175,11 +173,11 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   float sum[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) sum[v] = 0.f;
-  int64_t out = (static_cast<int64_t>(r0) + ROWS - 1) * p.C + c;
-  auto walk = [&](auto with_starts) {
+  int64_t out = (static_cast<int64_t>(r0) + ROWS - 1) * p.C;
+  auto walk = [&](auto all) {
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {   // h: from what a row adds to the state before it
-      if (with_starts.value && ((starts >> j) & 1u)) initial(j, H);
+      if (!all.value && ((starts >> j) & 1u)) initial(j, H);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float add = h[j][v];
@@ -189,42 +187,63 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
     }
 #pragma unroll
     for (int j = ROWS - 1; j >= 0; --j) {
-      float ox[V], og[V], oi[V];
+      float e[V], ox[V], og[V], oi[V], k[KEPT + 1];
+      gradient_of(all, j, e);
+#pragma unroll
+      for (int i = 0; i < KEPT; ++i) k[i] = mine[THR * KEPT * j + i];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float ev = e[j][v] + cr[v], dl = ev * (SCALE == LINREC_INPUT_ONE ? a[j][v] * h[j][v] : fmaf(a[j][v], h[j][v], kl[j][v]));
-        ox[v] = ev * kx[j][v];
-        if (ING) oi[v] = ev * ki[j][v];
-        og[v] = dl * kg[j][v];
-        if (DECAY && j < rows) sum[v] = fmaf(dl, ks[j][v], sum[v]);
-        cr[v] = a[j][v] * ev;
+        const float ev = e[v] + cr[v], av = a[j][v], mv = m[j][v], du = ev * mv;
+        float u = x[j].get(v);
+        ox[v] = du;
+        if (ING) {
+          const float2 s = Fn<T>::both_of(k[(KEEP_G ? V : 0) + v]);
+          u *= s.x;
+          ox[v] = du * s.x;
+          oi[v] = du * u * s.y;
+        }
+        float dl = av * h[j][v];   // e times the log decay's share: a h, and m's slope times u
+        if constexpr (SCALE == LINREC_INPUT_COMPLEMENT) dl = av * (h[j][v] - u);
+        if constexpr (SCALE == LINREC_INPUT_UNIT) dl = mv == 0.f ? dl : av * fmaf(-av * Fn<T>::rcp(mv), u, h[j][v]);
+        dl *= ev;
+        og[v] = dl;
+        if constexpr (KEEP_G) {
+          const float2 s = Fn<T>::both_of(k[v]);
+          og[v] = dl * s.y;
+          if (DECAY) {
+            const float share = dl * s.x;
+            og[v] = dk.get(v) * share * s.y;
+            if (all.value || j < rows) sum[v] += share;
+          }
+        }
+        cr[v] = av * ev;
       }
-      if (live && j < rows) {
+      if (all.value || j < rows) {
         Raw<T, V> o;
         o.set(ox);
-        o.store(static_cast<T*>(p.dx) + out);
+        o.store_at(p.dx, out, c);
         Raw<G, V> q;
         q.set(og);
-        q.store(static_cast<G*>(p.dg) + out);
+        q.store_at(p.dg, out, c);
         if (ING) {
           o.set(oi);
-          o.store(static_cast<T*>(p.di) + out);
+          o.store_at(p.di, out, c);
         }
       }
       out -= p.C;
-      if (with_starts.value && ((starts >> j) & 1u)) {
+      if (!all.value && ((starts >> j) & 1u)) {
         const int s = p.dh0 ? sequence_of(p, r0 + j) : -1;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          if (live && s >= 0) p.dh0[static_cast<int64_t>(s) * p.C + c + v] = cr[v];
+          if (s >= 0) p.dh0[static_cast<int64_t>(s) * p.C + c + v] = cr[v];
           cr[v] = 0.f;
         }
       }
     }
   };
-  if (cut) walk(std::true_type{});
-  else walk(std::false_type{});
-  if (p.dh0 && p.seq_idx && chunk == 0 && wave == 0 && live) {   // numbered sequences past the last one
+  if (some) walk(std::false_type{});
+  else walk(std::true_type{});
+  if (p.dh0 && p.seq_idx && chunk == 0 && wave == 0) {   // numbered sequences past the last one
     for (int s = p.nseqs - 1; s >= 0 && p.starts[s] >= p.R; --s) {
 #pragma unroll
       for (int v = 0; v < V; ++v) p.dh0[static_cast<int64_t>(s) * p.C + c + v] = p.dfinal ? p.dfinal[static_cast<int64_t>(s) * p.C + c + v] : 0.f;
@@ -236,7 +255,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
 #pragma unroll
       for (int v = 0; v < V; ++v) fc[wave][lane * V + v] = sum[v];
       __syncthreads();
-      if (wave == 0 && live) {
+      if (wave == 0) {
         for (int w = 1; w < WAVES; ++w) {
 #pragma unroll
           for (int v = 0; v < V; ++v) sum[v] += fc[w][lane * V + v];

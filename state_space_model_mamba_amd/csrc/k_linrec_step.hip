@@ -74,7 +74,7 @@ template <typename T, int GATE, int SCALE> __global__ __launch_bounds__(64) void
       if (t + 1 < s.T) request(t + 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Factor f = factor_of<T, GATE, false>(g0.get(v), Decay<T, GATE>(GATE == LINREC_GATE_DECAY ? dk.get(v) : 0.f));
+        const Factor f = factor_of<T, GATE>(g0.get(v), Decay<T, GATE>(GATE == LINREC_GATE_DECAY ? dk.get(v) : 0.f));
         float u = x0.get(v);
         if (s.i) u *= Fn<T>::sigmoid(i0.get(v));
         h[v] = fmaf(f.a, h[v], scale_of<T, GATE, SCALE>(f) * u);

@@ -60,6 +60,13 @@ template <typename S, int V> struct Raw {
   typedef uint32_t words __attribute__((ext_vector_type(N)));
   words w;
   __device__ __forceinline__ void load(const S* p) { w = *reinterpret_cast<const words*>(p); }
+  // at a lane's offset from a row's address that is the wave's: no 64-bit address per lane
+  __device__ __forceinline__ void load_at(const void* base, int64_t row, uint32_t c) {
+    w = *reinterpret_cast<const words*>(reinterpret_cast<const char*>(static_cast<const S*>(base) + row) + c * static_cast<uint32_t>(sizeof(S)));
+  }
+  __device__ __forceinline__ void store_at(void* base, int64_t row, uint32_t c) const {
+    *reinterpret_cast<words*>(reinterpret_cast<char*>(static_cast<S*>(base) + row) + c * static_cast<uint32_t>(sizeof(S))) = w;
+  }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (sizeof(S) == 2) return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
     else return __uint_as_float(w[e]);
@@ -69,6 +76,15 @@ template <typename S, int V> struct Raw {
     for (int i = 0; i < N; ++i) w[i] = sizeof(S) == 2 ? ssd::pack_bf16x2(f[sizeof(S) == 2 ? 2 * i : i], f[sizeof(S) == 2 ? 2 * i + 1 : i]) : __float_as_uint(f[i]);
   }
   __device__ __forceinline__ void store(S* p) const { *reinterpret_cast<words*>(p) = w; }
+  // the same values, of which the compiler knows nothing
+  __device__ __forceinline__ void renew() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint32_t t = w[i];
+      asm volatile("" : "+v"(t));
+      w[i] = t;
+    }
+  }
 };
 
 // With bf16 io the hardware's exponential, reciprocal and root (1 ulp); with float32 io the library's.
@@ -83,6 +99,16 @@ template <typename T> struct Fn {
   static __device__ __forceinline__ float2 sigmoids(float x) {
     const float e = exp(-x), s = rcp(1.f + e);
     return float2{s, x > 0.f ? e * s : 1.f - s};
+  }
+  // sigmoid(x), and to keep the smaller of the two (1 - sigmoid(x) with its sign turned), from which both come again
+  static __device__ __forceinline__ float sigmoid(float x, float& keep) {
+    const float e = exp(-x), s = rcp(1.f + e);
+    keep = x > 0.f ? -e * s : s;
+    return s;
+  }
+  static __device__ __forceinline__ float2 both_of(float w) {
+    const float o = 1.f - fabsf(w);
+    return __float_as_int(w) < 0 ? float2{o, -w} : float2{w, o};
   }
   // 1 - exp(y), y <= 0, from its direct form: above -1/2 as -y times the polynomial of degree 5 that is nearest to
   // (exp(y) - 1) / y there (off by 7e-9 of it, found by exchange), below it the difference loses at most one bit
@@ -102,32 +128,28 @@ template <typename T, int GATE> struct Decay {
   __device__ __forceinline__ explicit Decay(float decay) : k(decay), k2(decay * Fn<T>::LOG2E) {}
 };
 
-// Decay a, its logarithm la, 1 - a where the gate gives it, sigmoid(g) and 1 - it (LINREC_GATE_DECAY; SLOPES)
+// Decay a, its logarithm la, or with LINREC_GATE_SIGMOID 1 - a
 struct Factor {
-  float a, la, rest, s, r;
+  float a, la, rest;
 };
-template <typename T, int GATE, bool SLOPES> __device__ __forceinline__ Factor factor_of(float g, Decay<T, GATE> d) {
+template <typename T, int GATE> __device__ __forceinline__ Factor factor_of(float g, float2 s, Decay<T, GATE> d) {   // s: g's sigmoids
   using F = Fn<T>;
   Factor f{};
   if constexpr (GATE == LINREC_GATE_LOG) {
     f.la = g;
     f.a = F::exp(g);
   } else if constexpr (GATE == LINREC_GATE_SIGMOID) {
-    const float2 s = F::sigmoids(g);
     f.a = s.x;
     f.rest = s.y;
   } else {
-    if (SLOPES) {
-      const float2 s = F::sigmoids(g);
-      f.s = s.x;
-      f.r = s.y;
-    } else {
-      f.s = F::sigmoid(g);
-    }
-    f.la = d.k * f.s;
-    f.a = F::FAST ? __builtin_amdgcn_exp2f(d.k2 * f.s) : F::exp(f.la);
+    f.la = d.k * s.x;
+    f.a = F::FAST ? __builtin_amdgcn_exp2f(d.k2 * s.x) : F::exp(f.la);
   }
   return f;
+}
+template <typename T, int GATE> __device__ __forceinline__ Factor factor_of(float g, Decay<T, GATE> d) {
+  if constexpr (GATE == LINREC_GATE_SIGMOID) return factor_of<T, GATE>(g, Fn<T>::sigmoids(g), d);
+  else return factor_of<T, GATE>(g, float2{GATE == LINREC_GATE_DECAY ? Fn<T>::sigmoid(g) : 0.f, 0.f}, d);
 }
 // the input's factor m
 template <typename T, int GATE, int SCALE> __device__ __forceinline__ float scale_of(const Factor& f) {
@@ -136,13 +158,6 @@ template <typename T, int GATE, int SCALE> __device__ __forceinline__ float scal
   else if constexpr (SCALE == LINREC_INPUT_COMPLEMENT) return GATE == LINREC_GATE_SIGMOID ? f.rest : F::one_minus(f.la, 1.f - f.a);
   else return F::sqrt(GATE == LINREC_GATE_SIGMOID ? fmaf(f.rest, f.a, f.rest) : F::one_minus(2.f * f.la, fmaf(-f.a, f.a, 1.f)));
 }
-// its derivative by the log decay
-template <typename T, int SCALE> __device__ __forceinline__ float slope_of(const Factor& f, float m) {
-  if constexpr (SCALE == LINREC_INPUT_ONE) return 0.f;
-  else if constexpr (SCALE == LINREC_INPUT_COMPLEMENT) return -f.a;
-  else return m == 0.f ? 0.f : -f.a * f.a * Fn<T>::rcp(m);
-}
-
 // a chunk or part of it on a state: what decayed to nothing is dropped, so nothing of it (a NaN either) passes on
 __device__ __forceinline__ float onto(float factor, float add, float state) { return factor == 0.f ? add : fmaf(factor, state, add); }
 
@@ -186,7 +201,7 @@ __device__ __forceinline__ int ticket(const Problem& p, int cb) {
 // One wave, for the lane's V channels from c on: the state before the chunk at `place` of the chain, and A, H onto it left
 // for the chunks behind.  chunk_at(place): the chunk there; after: the states behind the chunks; cut: a sequence starts in it.
 template <int V, typename ChunkAt>
-__device__ __forceinline__ void join(const Problem& p, float* after, int place, int cb, int c, bool live, bool cut, const float (&A)[V],
+__device__ __forceinline__ void join(const Problem& p, float* after, int place, int cb, int c, bool cut, const float (&A)[V],
                                      const float (&H)[V], float (&before)[V], ChunkAt chunk_at) {
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int64_t mine = static_cast<int64_t>(chunk_at(place)) * p.C + c;
@@ -196,19 +211,15 @@ __device__ __forceinline__ void join(const Problem& p, float* after, int place, 
     if (lane == 0) __hip_atomic_store(marks + place, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
   auto leave = [&](const float (&h)[V]) {
-    if (live) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) put(after + mine + v, h[v]);
-    }
+    for (int v = 0; v < V; ++v) put(after + mine + v, h[v]);
     mark(WHOLE);
   };
   if (cut) {
     leave(H);
   } else if (place > 0) {
-    if (live) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) put(p.agg + mine + v, float2{A[v], H[v]});
-    }
+    for (int v = 0; v < V; ++v) put(p.agg + mine + v, float2{A[v], H[v]});
     mark(PART);
   }
 #pragma unroll

@@ -23,15 +23,16 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   const int cb = channel_block(p), chunk = ticket(p, cb);
   // lanes past the last channels take those again: they write the same values to the same places
   const int c = cb * CB + lane * V < p.C ? cb * CB + lane * V : p.C - V;
-  const int r0 = chunk * CHUNK + wave * ROWS, rows = p.R - r0;   // rows: those there are
+  const uint32_t ct = lane_offset<T>(c), cg = lane_offset<G>(c);
+  const int r0 = __builtin_amdgcn_readfirstlane(chunk * CHUNK + wave * ROWS), rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS];
   Raw<G, V> g[ROWS];
   Cursor at(p, rows > 0 ? r0 : p.R - 1);
 #pragma unroll
   for (int j = 0; j < ROWS; ++j) {
-    x[j].load_at(p.x, at.x, c);
-    g[j].load_at(p.g, at.g, c);
-    if (ING) in[j].load_at(p.i, at.i, c);
+    x[j].load_at(p.x, at.x, ct);
+    g[j].load_at(p.g, at.g, cg);
+    if (ING) in[j].load_at(p.i, at.i, ct);
     if (j + 1 < rows) at.next(p);
   }
   Raw<float, V> dk;
@@ -134,7 +135,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
       if (all.value || j < rows) {
         Raw<T, V> out;
         out.set(h);
-        out.store_at(p.y, y, c);
+        out.store_at(p.y, y, ct);
         if (!all.value && ((ends >> j) & 1u)) {
           const int s = sequence_of(p, r0 + j);
           if (s >= 0) {

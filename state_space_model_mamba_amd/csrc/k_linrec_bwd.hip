@@ -27,17 +27,18 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   const int chunk = p.chunks - 1 - place;   // from the end
   // lanes past the last channels take those again: they write the same values to the same places
   const int c = cb * CB + lane * V < p.C ? cb * CB + lane * V : p.C - V;
-  const int r0 = chunk * CHUNK + wave * ROWS, rows = p.R - r0;   // rows: those there are
+  const uint32_t ct = lane_offset<T>(c), cg = lane_offset<G>(c);
+  const int r0 = __builtin_amdgcn_readfirstlane(chunk * CHUNK + wave * ROWS), rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS], dy[ROWS];
   Raw<G, V> g[ROWS];
   Cursor at(p, rows > 0 ? r0 : p.R - 1);
   int64_t yat = static_cast<int64_t>(rows > 0 ? r0 : p.R - 1) * p.C;
 #pragma unroll
   for (int j = 0; j < ROWS; ++j) {
-    g[j].load_at(p.g, at.g, c);
-    x[j].load_at(p.x, at.x, c);
-    if (ING) in[j].load_at(p.i, at.i, c);
-    dy[j].load_at(p.dy, yat, c);
+    g[j].load_at(p.g, at.g, cg);
+    x[j].load_at(p.x, at.x, ct);
+    if (ING) in[j].load_at(p.i, at.i, ct);
+    dy[j].load_at(p.dy, yat, ct);
     if (j + 1 < rows) {
       at.next(p);
       yat += p.C;
@@ -221,13 +222,13 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
       if (all.value || j < rows) {
         Raw<T, V> o;
         o.set(ox);
-        o.store_at(p.dx, out, c);
+        o.store_at(p.dx, out, ct);
         Raw<G, V> q;
         q.set(og);
-        q.store_at(p.dg, out, c);
+        q.store_at(p.dg, out, cg);
         if (ING) {
           o.set(oi);
-          o.store_at(p.di, out, c);
+          o.store_at(p.di, out, ct);
         }
       }
       out -= p.C;

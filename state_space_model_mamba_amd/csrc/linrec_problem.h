@@ -60,12 +60,12 @@ template <typename S, int V> struct Raw {
   typedef uint32_t words __attribute__((ext_vector_type(N)));
   words w;
   __device__ __forceinline__ void load(const S* p) { w = *reinterpret_cast<const words*>(p); }
-  // at a lane's offset from a row's address that is the wave's: no 64-bit address per lane
-  __device__ __forceinline__ void load_at(const void* base, int64_t row, uint32_t c) {
-    w = *reinterpret_cast<const words*>(reinterpret_cast<const char*>(static_cast<const S*>(base) + row) + c * static_cast<uint32_t>(sizeof(S)));
+  // at a lane's byte offset from a row's address, which is the wave's: no 64-bit address per lane
+  __device__ __forceinline__ void load_at(const void* base, int64_t row, uint32_t off) {
+    w = *reinterpret_cast<const words*>(reinterpret_cast<const char*>(static_cast<const S*>(base) + row) + off);
   }
-  __device__ __forceinline__ void store_at(void* base, int64_t row, uint32_t c) const {
-    *reinterpret_cast<words*>(reinterpret_cast<char*>(static_cast<S*>(base) + row) + c * static_cast<uint32_t>(sizeof(S))) = w;
+  __device__ __forceinline__ void store_at(void* base, int64_t row, uint32_t off) const {
+    *reinterpret_cast<words*>(reinterpret_cast<char*>(static_cast<S*>(base) + row) + off) = w;
   }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (sizeof(S) == 2) return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
@@ -76,16 +76,14 @@ template <typename S, int V> struct Raw {
     for (int i = 0; i < N; ++i) w[i] = sizeof(S) == 2 ? ssd::pack_bf16x2(f[sizeof(S) == 2 ? 2 * i : i], f[sizeof(S) == 2 ? 2 * i + 1 : i]) : __float_as_uint(f[i]);
   }
   __device__ __forceinline__ void store(S* p) const { *reinterpret_cast<words*>(p) = w; }
-  // the same values, of which the compiler knows nothing
-  __device__ __forceinline__ void renew() {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      uint32_t t = w[i];
-      asm volatile("" : "+v"(t));
-      w[i] = t;
-    }
-  }
 };
+
+// A lane's offset in a row of elements of type S: 32 bits of which the compiler knows nothing, or it would widen them
+template <typename S> __device__ __forceinline__ uint32_t lane_offset(int c) {
+  uint32_t off = static_cast<uint32_t>(c) * static_cast<uint32_t>(sizeof(S));
+  asm("" : "+v"(off));
+  return off;
+}
 
 // With bf16 io the hardware's exponential, reciprocal and root (1 ulp); with float32 io the library's.
 template <typename T> struct Fn {
@@ -110,15 +108,17 @@ template <typename T> struct Fn {
     const float o = 1.f - fabsf(w);
     return __float_as_int(w) < 0 ? float2{o, -w} : float2{w, o};
   }
-  // 1 - exp(y), y <= 0, from its direct form: above -1/2 as -y times the polynomial of degree 5 that is nearest to
-  // (exp(y) - 1) / y there (off by 7e-9 of it, found by exchange), below it the difference loses at most one bit
-  static __device__ __forceinline__ float one_minus(float y, float direct) {
-    float q = fmaf(1.1216348502784967e-3f, y, 8.187386207282543e-3f);
-    q = fmaf(q, y, 4.1629090905189514e-2f);
-    q = fmaf(q, y, 1.6666224598884583e-1f);
-    q = fmaf(q, y, 4.999998211860657e-1f);
-    q = fmaf(q, y, 1.f);
-    return y > -0.5f ? -y * q : direct;
+  // 1 - exp(S y), y <= 0, from its direct form: with S y above -1/2 as -S y times the polynomial of degree 5 that is
+  // nearest to (exp(t) - 1) / t there (off by 7e-9 of it, found by exchange), below it the difference loses at most one bit
+  template <int S> static __device__ __forceinline__ float one_minus(float y, float direct) {
+    constexpr float C[6] = {1.f, 4.999998211860657e-1f, 1.6666224598884583e-1f, 4.1629090905189514e-2f, 8.187386207282543e-3f, 1.1216348502784967e-3f};
+    float q = C[5] * (S == 2 ? 64.f : 1.f);   // S^6 and down: powers of two change no bits
+    q = fmaf(q, y, C[4] * (S == 2 ? 32.f : 1.f));
+    q = fmaf(q, y, C[3] * (S == 2 ? 16.f : 1.f));
+    q = fmaf(q, y, C[2] * (S == 2 ? 8.f : 1.f));
+    q = fmaf(q, y, C[1] * (S == 2 ? 4.f : 1.f));
+    q = fmaf(q, y, C[0] * S);
+    return y > -0.5f / S ? -y * q : direct;
   }
 };
 
@@ -155,8 +155,8 @@ template <typename T, int GATE> __device__ __forceinline__ Factor factor_of(floa
 template <typename T, int GATE, int SCALE> __device__ __forceinline__ float scale_of(const Factor& f) {
   using F = Fn<T>;
   if constexpr (SCALE == LINREC_INPUT_ONE) return 1.f;
-  else if constexpr (SCALE == LINREC_INPUT_COMPLEMENT) return GATE == LINREC_GATE_SIGMOID ? f.rest : F::one_minus(f.la, 1.f - f.a);
-  else return F::sqrt(GATE == LINREC_GATE_SIGMOID ? fmaf(f.rest, f.a, f.rest) : F::one_minus(2.f * f.la, fmaf(-f.a, f.a, 1.f)));
+  else if constexpr (SCALE == LINREC_INPUT_COMPLEMENT) return GATE == LINREC_GATE_SIGMOID ? f.rest : F::template one_minus<1>(f.la, 1.f - f.a);
+  else return F::sqrt(GATE == LINREC_GATE_SIGMOID ? fmaf(f.rest, f.a, f.rest) : F::template one_minus<2>(f.la, fmaf(-f.a, f.a, 1.f)));
 }
 // a chunk or part of it on a state: what decayed to nothing is dropped, so nothing of it (a NaN either) passes on
 __device__ __forceinline__ float onto(float factor, float add, float state) { return factor == 0.f ? add : fmaf(factor, state, add); }
@@ -277,7 +277,7 @@ struct Cursor {
   int64_t x, g, i;
   int t;   // row of its batch row
   __device__ __forceinline__ Cursor(const Problem& p, int row) {
-    const int b = row / p.L;
+    const int b = __builtin_amdgcn_readfirstlane(row / p.L);   // the same in all lanes: addresses stay scalar
     t = row - b * p.L;
     x = b * p.x_sb + t * p.x_sl;
     g = b * p.g_sb + t * p.g_sl;

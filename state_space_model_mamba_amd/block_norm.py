@@ -21,6 +21,8 @@ from torch.autograd.function import once_differentiable
 from state_space_model_mamba_amd import ssd
 from state_space_model_mamba_amd.delta import _gradient, _on, _stream
 
+F32 = torch.float32
+
 NORMS = {"rms": 0, "layer": 1}
 GATES = {"silu": 0, "sigmoid": 1}
 EXPORTED = ("add_norm_fwd", "add_norm_bwd", "gated_norm_fwd", "gated_norm_bwd", "block_norm_bwd_workspace_size")
@@ -110,6 +112,34 @@ def _strided(t, name, dtype, shape, device):
     return row_strides(t, name)
 
 
+def _check(t, name, dtype, shape, device):
+    """ssd._check, its messages formed only where something is wrong."""
+    if t is not None and (t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous()):
+        ssd._check(t, name, dtype, shape, device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, function, device, *args):
+    """function(*args, stream) with the tensors' device current (the library launches on the current device)."""
+    if torch._C._cuda_getDevice() == device.index:
+        rc = function(*args, _stream(device))
+    else:
+        with _on(device):
+            rc = function(*args, _stream(device))
+    if rc:
+        raise ssd.SsdError(rc, name)
+
+
+def _like(t, dtype=None):
+    """An uninitialised contiguous tensor of t's shape."""
+    if t.is_contiguous():
+        return torch.empty_like(t) if dtype is None or dtype == t.dtype else torch.empty_like(t, dtype=dtype)
+    return t.new_empty(t.shape, dtype=dtype)
+
+
 def _io(dtype):
     return ssd.SSD_IO_BF16 if dtype == torch.bfloat16 else ssd.SSD_IO_F32
 
@@ -119,29 +149,32 @@ def _common(what, x, z, weight, bias, residual, residual_dtype, scale, groups, e
     dev, io = x.device, x.dtype
     if dev.type != "cuda":
         raise ValueError(f"{what} runs on a HIP device; got tensors on {dev}")
-    if io not in (torch.bfloat16, torch.float32):
+    if io != torch.bfloat16 and io != F32:
         raise ValueError(f"unsupported io dtype {io}")
     if norm not in NORMS:
         raise ValueError(f"norm is one of {sorted(NORMS)}; got {norm!r}")
     if gate not in GATES:
         raise ValueError(f"gate is one of {sorted(GATES)}; got {gate!r}")
-    if x.dim() != 3:
+    size = x.shape
+    if len(size) != 3:
         raise ValueError("x is (batch, seqlen, width)")
-    b, L, D = x.shape
-    strides = (*_strided(x, "x", io, (b, L, D), dev), *_strided(z, "z", io, (b, L, D), dev))
+    b, L, D = size
+    strides = (*row_strides(x, "x"), *_strided(z, "z", io, size, dev))
     if residual is not None:
-        if residual_dtype not in (None, residual.dtype):
+        if residual_dtype is not None and residual_dtype != residual.dtype:
             raise ValueError(f"residual has dtype {residual.dtype}, residual_dtype is {residual_dtype}")
         residual_dtype = residual.dtype
-    residual_dtype = residual_dtype or io
-    if residual_dtype not in (io, torch.float32):
+    elif residual_dtype is None:
+        residual_dtype = io
+    if residual_dtype != io and residual_dtype != F32:
         raise ValueError(f"the residual's dtype is {io} or float32; got {residual_dtype}")
-    ssd._check(residual, "residual", residual_dtype, (b, L, D), dev)
-    ssd._check(weight, "weight", torch.float32, (D,), dev)
-    ssd._check(bias, "bias", torch.float32, (D,), dev)
+    vector = (D,)
+    _check(residual, "residual", residual_dtype, size, dev)
+    _check(weight, "weight", F32, vector, dev)
+    _check(bias, "bias", F32, vector, dev)
     alpha = 1.0
     if isinstance(scale, torch.Tensor):
-        ssd._check(scale, "scale", torch.float32, (D,), dev)
+        _check(scale, "scale", F32, vector, dev)
     elif scale is not None:
         alpha, scale = float(scale), None
     shape, nbytes = _sized(b, L, D, int(groups), norm, gate, bool(norm_before_gate), _io(io), _io(residual_dtype),
@@ -151,14 +184,14 @@ def _common(what, x, z, weight, bias, residual, residual_dtype, scale, groups, e
 
 def _workspace(workspace, nbytes, dev):
     if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
-    return workspace
+    return workspace, workspace.numel() * workspace.element_size()
 
 
-def _sums(D, dev, **wanted):
-    return {k: torch.empty((D,), dtype=torch.float32, device=dev) if v else None for k, v in wanted.items()}
+def _sum(x, wanted):
+    return x.new_empty((x.shape[2],), dtype=F32) if wanted else None
 
 
 def add_norm_fwd(x, residual=None, weight=None, bias=None, scale=1.0, eps: float = 1e-6, norm: str = "rms",
@@ -172,15 +205,10 @@ def add_norm_fwd(x, residual=None, weight=None, bias=None, scale=1.0, eps: float
     """
     shape, _, scale, rdtype = _common("add_norm", x, None, weight, bias, residual, residual_dtype, scale, 1, eps, norm,
                                       "silu", False)
-    dev = x.device
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    r = torch.empty(x.shape, dtype=rdtype, device=dev)
-    lib = load_library()
-    with _on(dev):
-        rc = lib.add_norm_fwd(ctypes.byref(shape), ssd._ptr(x), ssd._ptr(residual), ssd._ptr(weight), ssd._ptr(bias),
-                              ssd._ptr(scale), ssd._ptr(y), ssd._ptr(r), _stream(dev))
-    if rc:
-        raise ssd.SsdError(rc, "add_norm_fwd")
+    y = _like(x)
+    r = _like(x, rdtype)
+    _call("add_norm_fwd", load_library().add_norm_fwd, x.device, shape, x.data_ptr(), _ptr(residual), _ptr(weight),
+          _ptr(bias), _ptr(scale), y.data_ptr(), r.data_ptr())
     return y, r
 
 
@@ -195,26 +223,22 @@ def add_norm_bwd(x, residual, weight, scale, dy, dr, eps: float = 1e-6, norm: st
     """
     shape, nbytes, scale, rdtype = _common("add_norm", x, None, weight, None, residual, residual_dtype, scale, 1, eps,
                                            norm, "silu", False)
-    dev, D = x.device, x.shape[2]
+    dev, size = x.device, x.shape
     if dy is None and dr is None:
         raise ValueError("add_norm_bwd needs dy or dr")
-    ssd._check(dy, "dy", x.dtype, tuple(x.shape), dev)
-    ssd._check(dr, "dr", rdtype, tuple(x.shape), dev)
-    workspace = _workspace(workspace, nbytes, dev)
+    _check(dy, "dy", x.dtype, size, dev)
+    _check(dr, "dr", rdtype, size, dev)
+    workspace, nbytes = _workspace(workspace, nbytes, dev)
     want_dresidual = residual is not None if want_dresidual is None else want_dresidual
     same = scale is None and shape.alpha == 1.0 and rdtype == x.dtype
-    out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
-           "dresidual": torch.empty(x.shape, dtype=rdtype, device=dev) if want_dresidual and not same else None,
-           **_sums(D, dev, dweight=weight is not None if want_dweight is None else want_dweight, dbias=want_dbias,
-                   dscale=scale is not None if want_dscale is None else want_dscale)}
-    lib = load_library()
-    with _on(dev):
-        rc = lib.add_norm_bwd(ctypes.byref(shape), ssd._ptr(x), ssd._ptr(residual), ssd._ptr(weight), ssd._ptr(scale),
-                              ssd._ptr(dy), ssd._ptr(dr), ssd._ptr(out["dx"]), ssd._ptr(out["dresidual"]),
-                              ssd._ptr(out["dweight"]), ssd._ptr(out["dbias"]), ssd._ptr(out["dscale"]),
-                              ssd._ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev))
-    if rc:
-        raise ssd.SsdError(rc, "add_norm_bwd")
+    out = {"dx": _like(x),
+           "dresidual": _like(x, rdtype) if want_dresidual and not same else None,
+           "dweight": _sum(x, weight is not None if want_dweight is None else want_dweight),
+           "dbias": _sum(x, want_dbias),
+           "dscale": _sum(x, scale is not None if want_dscale is None else want_dscale)}
+    _call("add_norm_bwd", load_library().add_norm_bwd, dev, shape, x.data_ptr(), _ptr(residual), _ptr(weight),
+          _ptr(scale), _ptr(dy), _ptr(dr), out["dx"].data_ptr(), _ptr(out["dresidual"]), _ptr(out["dweight"]),
+          _ptr(out["dbias"]), _ptr(out["dscale"]), workspace.data_ptr(), nbytes)
     if want_dresidual and same:
         out["dresidual"] = out["dx"]
     return out
@@ -265,14 +289,9 @@ def gated_norm_fwd(x, z=None, weight=None, bias=None, residual=None, scale=1.0, 
     """
     shape, _, scale, rdtype = _common("gated_norm", x, z, weight, bias, residual, None, scale, groups, eps, norm, gate,
                                       norm_before_gate)
-    dev = x.device
-    out = torch.empty(x.shape, dtype=rdtype, device=dev)
-    lib = load_library()
-    with _on(dev):
-        rc = lib.gated_norm_fwd(ctypes.byref(shape), ssd._ptr(x), ssd._ptr(z), ssd._ptr(weight), ssd._ptr(bias),
-                                ssd._ptr(residual), ssd._ptr(scale), ssd._ptr(out), _stream(dev))
-    if rc:
-        raise ssd.SsdError(rc, "gated_norm_fwd")
+    out = _like(x, rdtype)
+    _call("gated_norm_fwd", load_library().gated_norm_fwd, x.device, shape, x.data_ptr(), _ptr(z), _ptr(weight),
+          _ptr(bias), _ptr(residual), _ptr(scale), out.data_ptr())
     return out
 
 
@@ -288,22 +307,17 @@ def gated_norm_bwd(x, z, weight, bias, scale, dout, groups: int = 1, eps: float 
     """
     shape, nbytes, scale, rdtype = _common("gated_norm", x, z, weight, bias, None, dout.dtype, scale, groups, eps, norm,
                                            gate, norm_before_gate)
-    dev, D = x.device, x.shape[2]
-    ssd._check(dout, "dout", rdtype, tuple(x.shape), dev)
-    workspace = _workspace(workspace, nbytes, dev)
-    out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
-           "dz": None if z is None else torch.empty(x.shape, dtype=x.dtype, device=dev),
-           **_sums(D, dev, dweight=weight is not None if want_dweight is None else want_dweight,
-                   dbias=bias is not None if want_dbias is None else want_dbias,
-                   dscale=scale is not None if want_dscale is None else want_dscale)}
-    lib = load_library()
-    with _on(dev):
-        rc = lib.gated_norm_bwd(ctypes.byref(shape), ssd._ptr(x), ssd._ptr(z), ssd._ptr(weight), ssd._ptr(bias),
-                                ssd._ptr(scale), ssd._ptr(dout), ssd._ptr(out["dx"]), ssd._ptr(out["dz"]),
-                                ssd._ptr(out["dweight"]), ssd._ptr(out["dbias"]), ssd._ptr(out["dscale"]),
-                                ssd._ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev))
-    if rc:
-        raise ssd.SsdError(rc, "gated_norm_bwd")
+    dev = x.device
+    _check(dout, "dout", rdtype, x.shape, dev)
+    workspace, nbytes = _workspace(workspace, nbytes, dev)
+    out = {"dx": _like(x),
+           "dz": None if z is None else _like(x),
+           "dweight": _sum(x, weight is not None if want_dweight is None else want_dweight),
+           "dbias": _sum(x, bias is not None if want_dbias is None else want_dbias),
+           "dscale": _sum(x, scale is not None if want_dscale is None else want_dscale)}
+    _call("gated_norm_bwd", load_library().gated_norm_bwd, dev, shape, x.data_ptr(), _ptr(z), _ptr(weight), _ptr(bias),
+          _ptr(scale), dout.data_ptr(), out["dx"].data_ptr(), _ptr(out["dz"]), _ptr(out["dweight"]),
+          _ptr(out["dbias"]), _ptr(out["dscale"]), workspace.data_ptr(), nbytes)
     return out
 
 

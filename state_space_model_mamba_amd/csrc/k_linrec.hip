@@ -159,14 +159,70 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   }
 }
 
-__global__ __launch_bounds__(256) void k_linrec_clear(uint32_t* sync, int64_t n) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) sync[i] = 0;
+// The first block numbers the sequences: their first rows in row order, from a stretch of rows at a time, a row a lane
+// and all of a stretch's seq_idx in flight; the others (the first too, without sequences) clear the tickets and marks.
+constexpr int SET_THR = 1024, SET_ROWS = 16;   // rows of a thread in a stretch
+__global__ __launch_bounds__(SET_THR) void k_linrec_setup(Problem p, int number, int64_t n) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+  if (static_cast<int>(blockIdx.x) >= number) {
+    const int64_t from = static_cast<int64_t>(blockIdx.x) - number, step = static_cast<int64_t>(gridDim.x) - number;
+    for (int64_t i = from * SET_THR + tid; i < n; i += step * SET_THR) p.sync[i] = 0;
+    return;
+  }
+  constexpr int PARTS = SET_ROWS * SET_THR / 64;   // of 64 rows
+  __shared__ int before[PARTS], all;               // starts before a part in its stretch, and in the stretch
+  int base = 0;
+  for (int64_t first = 0; first < p.R; first += SET_THR * SET_ROWS) {
+    uint64_t mask[SET_ROWS];
+    int32_t v[SET_ROWS], u[SET_ROWS];
+#pragma unroll
+    for (int k = 0; k < SET_ROWS; ++k) {
+      const int64_t r = first + k * SET_THR + tid, at = r < p.R ? r : p.R - 1;
+      v[k] = p.seq_idx[at];
+      u[k] = p.seq_idx[at > 0 ? at - 1 : 0];
+    }
+#pragma unroll
+    for (int k = 0; k < SET_ROWS; ++k) {
+      const int64_t r = first + k * SET_THR + tid;
+      mask[k] = __ballot(r < p.R && (v[k] != u[k] || static_cast<int>(r) % p.L == 0));
+      if (lane == 0) before[k * (SET_THR / 64) + wave] = __popcll(mask[k]);
+    }
+    __syncthreads();
+    if (wave == 0) {   // PARTS / 64 parts a lane
+      int mine[PARTS / 64], sum = 0;
+#pragma unroll
+      for (int i = 0; i < PARTS / 64; ++i) {
+        mine[i] = sum;
+        sum += before[lane * (PARTS / 64) + i];
+      }
+      int incl = sum;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(incl, d);
+        if (lane >= d) incl += o;
+      }
+#pragma unroll
+      for (int i = 0; i < PARTS / 64; ++i) before[lane * (PARTS / 64) + i] = incl - sum + mine[i];
+      if (lane == 63) all = incl;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < SET_ROWS; ++k) {
+      const int at = base + before[k * (SET_THR / 64) + wave] + __popcll(mask[k] & ((uint64_t{1} << lane) - 1));
+      if (((mask[k] >> lane) & 1) && at <= p.nseqs) p.starts[at] = static_cast<int>(first + k * SET_THR + tid);
+    }
+    base += all;
+    __syncthreads();
+  }
+  for (int64_t s = static_cast<int64_t>(base) + tid; s <= p.nseqs; s += SET_THR) p.starts[s] = p.R;
 }
 
-int launch_clear(const Problem& p, hipStream_t st) {
-  if (p.chunks == 1) return SSD_OK;
-  const int64_t n = static_cast<int64_t>(p.cblocks) * (p.chunks + LINE);
-  hipLaunchKernelGGL(k_linrec_clear, dim3(static_cast<unsigned>(n < 256 * 1024 ? (n + 255) / 256 : 1024)), dim3(256), 0, st, p.sync, n);
+int launch_setup(const Problem& p, bool number, hipStream_t st) {
+  const int64_t n = p.chunks == 1 ? 0 : static_cast<int64_t>(p.cblocks) * (p.chunks + LINE);
+  const int64_t blocks = (n + 4 * SET_THR - 1) / (4 * SET_THR), most = 512;
+  const int64_t grid = (blocks < most ? blocks : most) + number;
+  if (grid == 0) return SSD_OK;
+  hipLaunchKernelGGL(k_linrec_setup, dim3(static_cast<unsigned>(grid)), dim3(SET_THR), 0, st, p, number ? 1 : 0, n);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 

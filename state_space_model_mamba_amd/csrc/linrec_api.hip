@@ -3,7 +3,6 @@
 // launches.
 #include <limits.h>
 
-#include "delta_problem.h"
 #include "linrec_problem.h"
 
 int linrec_check(const linrec_shape* s) {
@@ -44,7 +43,7 @@ size_t place(Problem& p, bool backward, char* base) {
     return r;
   };
   const size_t n = static_cast<size_t>(p.chunks) * p.C;
-  p.starts = reinterpret_cast<int32_t*>(take((2 * static_cast<size_t>(p.nseqs) + 1) * 4));
+  p.starts = reinterpret_cast<int32_t*>(take((static_cast<size_t>(p.nseqs) + 1) * 4));
   p.sync = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(p.cblocks) * (p.chunks + linrec::LINE) * 4));
   p.agg = reinterpret_cast<float2*>(take(n * sizeof(float2)));
   p.states = reinterpret_cast<float*>(take(n * 4));
@@ -90,18 +89,6 @@ int inputs(const linrec_shape* shape, const void* x, const void* g, const void* 
   return SSD_OK;
 }
 
-// the first rows of the sequences, where states are numbered by them
-int find_starts(const Problem& p, hipStream_t st) {
-  if (!p.starts) return SSD_OK;
-  delta::Problem d{};
-  d.L = p.L;
-  d.total = p.R;
-  d.nseqs = p.nseqs;
-  d.seq_idx = p.seq_idx;
-  d.starts = p.starts;
-  return delta::launch_starts(d, st);
-}
-
 }  // namespace
 
 extern "C" {
@@ -138,8 +125,7 @@ int linrec_fwd(const linrec_shape* shape, const void* x, const void* g, const vo
   p.final = final_states;
   if (chunk_states) p.states = chunk_states;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if ((rc = find_starts(p, st)) != SSD_OK) return rc;
-  if ((rc = linrec::launch_clear(p, st)) != SSD_OK) return rc;
+  if ((rc = linrec::launch_setup(p, p.starts != nullptr, st)) != SSD_OK) return rc;
   return linrec::launch_fwd(p, *shape, st);
 }
 
@@ -161,14 +147,13 @@ int linrec_bwd(const linrec_shape* shape, const void* x, const void* g, const vo
   p.dy = dy; p.dfinal = d_final_states;
   p.dx = dx; p.dg = dg; p.di = d_in_gate; p.ddecay = ddecay; p.dh0 = d_initial_states;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if ((rc = find_starts(p, st)) != SSD_OK) return rc;
+  if ((rc = linrec::launch_setup(p, p.starts != nullptr, st)) != SSD_OK) return rc;
   if (chunk_states) {
     p.states = const_cast<float*>(chunk_states);
   } else {
-    if ((rc = linrec::launch_clear(p, st)) != SSD_OK) return rc;
     if ((rc = linrec::launch_fwd(p, *shape, st)) != SSD_OK) return rc;
+    if ((rc = linrec::launch_setup(p, false, st)) != SSD_OK) return rc;
   }
-  if ((rc = linrec::launch_clear(p, st)) != SSD_OK) return rc;
   return linrec::launch_bwd(p, *shape, st);
 }
 

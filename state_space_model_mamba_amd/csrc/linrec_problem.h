@@ -41,7 +41,7 @@ struct Problem {
   void *y, *dx, *dg, *di;
   float *final, *ddecay, *dh0;
   // workspace
-  int32_t* starts;         // (nseqs + 1) first rows (seq_idx and states given), then nseqs more that only k_delta_starts reads
+  int32_t* starts;         // (nseqs + 1) first rows (seq_idx and states given)
   uint32_t* sync;          // (cblocks, LINE): tickets; (cblocks, chunks): what of a chunk is there
   float2* agg;             // (chunks, C): a chunk's factor and what it adds
   float* states;           // (chunks, C): the state after each chunk
@@ -49,7 +49,8 @@ struct Problem {
   float* slots;            // (chunks, C): ddecay of each chunk (backward)
 };
 
-int launch_clear(const Problem& p, hipStream_t st);   // the tickets, before either of the others
+// the tickets and marks, and with `number` the sequences' first rows, before either of the others
+int launch_setup(const Problem& p, bool number, hipStream_t st);
 int launch_fwd(const Problem& p, const linrec_shape& s, hipStream_t st);   // (p.y, p.final NULL: the states only)
 int launch_bwd(const Problem& p, const linrec_shape& s, hipStream_t st);
 

@@ -19,8 +19,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from state_space_model_mamba_amd import ssd
-from state_space_model_mamba_amd.block_norm import _io, _strided, _workspace
-from state_space_model_mamba_amd.delta import MAX_STEP_TOKENS, _gradient, _nseqs, _on, _stream
+from state_space_model_mamba_amd.block_norm import F32, _call, _check, _io, _like, _ptr, _strided, _workspace, row_strides
+from state_space_model_mamba_amd.delta import MAX_STEP_TOKENS, _gradient, _nseqs
 
 GATES = {"log": 0, "sigmoid": 1, "decay": 2}
 INPUT_SCALES = {"one": 0, "complement": 1, "unit": 2}
@@ -92,21 +92,21 @@ def _inputs(what, x, g, in_gate, decay, nseqs, gate, input_scale):
     dev, io = x.device, x.dtype
     if dev.type != "cuda":
         raise ValueError(f"{what} runs on a HIP device; got tensors on {dev}")
-    if io not in (torch.bfloat16, torch.float32):
+    if io != torch.bfloat16 and io != F32:
         raise ValueError(f"unsupported io dtype {io}")
     if gate not in GATES:
         raise ValueError(f"gate is one of {sorted(GATES)}; got {gate!r}")
     if input_scale not in INPUT_SCALES:
         raise ValueError(f"input_scale is one of {sorted(INPUT_SCALES)}; got {input_scale!r}")
-    if x.dim() != 3:
+    size = x.shape
+    if len(size) != 3:
         raise ValueError("x, g and in_gate are (batch, seqlen, channels)")
-    b, L, C = x.shape
-    strides = (*_strided(x, "x", io, (b, L, C), dev),
-               *_strided(g, "g", torch.float32 if gate == "log" else io, (b, L, C), dev),
-               *_strided(in_gate, "in_gate", io, (b, L, C), dev))
+    strides = (*row_strides(x, "x"), *_strided(g, "g", F32 if gate == "log" else io, size, dev),
+               *_strided(in_gate, "in_gate", io, size, dev))
     if (gate == "decay") != (decay is not None):
         raise ValueError('decay goes with gate="decay"')
-    ssd._check(decay, "decay", torch.float32, (C,), dev)
+    b, L, C = size
+    _check(decay, "decay", F32, (C,), dev)
     return _sized(b, L, C, nseqs, gate, input_scale, _io(io), strides)
 
 
@@ -126,20 +126,15 @@ def linrec_fwd(x, g, in_gate=None, decay=None, initial_states=None, seq_idx=None
     shape, nbytes, _, n = _inputs("linrec_fwd", x, g, in_gate, decay, S, gate, input_scale)
     dev = x.device
     b, L, C = x.shape
-    ssd._check(initial_states, "initial_states", torch.float32, (S, C), dev)
-    ssd._check(seq_idx, "seq_idx", torch.int32, (b, L), dev)
-    workspace = _workspace(workspace, nbytes, dev)
-    out = {"y": torch.empty((b, L, C), dtype=x.dtype, device=dev),
-           "final_states": torch.empty((S, C), dtype=torch.float32, device=dev) if want_final_states else None,
-           "chunk_states": torch.empty((n, C), dtype=torch.float32, device=dev) if want_chunk_states else None}
-    lib = load_library()
-    with _on(dev):
-        rc = lib.linrec_fwd(ctypes.byref(shape), ssd._ptr(x), ssd._ptr(g), ssd._ptr(in_gate), ssd._ptr(decay),
-                            ssd._ptr(initial_states), ssd._ptr(seq_idx), ssd._ptr(out["y"]),
-                            ssd._ptr(out["final_states"]), ssd._ptr(out["chunk_states"]), ssd._ptr(workspace),
-                            workspace.numel() * workspace.element_size(), _stream(dev))
-    if rc:
-        raise ssd.SsdError(rc, "linrec_fwd")
+    _check(initial_states, "initial_states", F32, (S, C), dev)
+    _check(seq_idx, "seq_idx", torch.int32, (b, L), dev)
+    workspace, nbytes = _workspace(workspace, nbytes, dev)
+    out = {"y": _like(x),
+           "final_states": x.new_empty((S, C), dtype=F32) if want_final_states else None,
+           "chunk_states": x.new_empty((n, C), dtype=F32) if want_chunk_states else None}
+    _call("linrec_fwd", load_library().linrec_fwd, dev, shape, x.data_ptr(), g.data_ptr(), _ptr(in_gate), _ptr(decay),
+          _ptr(initial_states), _ptr(seq_idx), out["y"].data_ptr(), _ptr(out["final_states"]),
+          _ptr(out["chunk_states"]), workspace.data_ptr(), nbytes)
     return out
 
 
@@ -157,27 +152,19 @@ def linrec_bwd(x, g, in_gate, decay, dy, initial_states=None, seq_idx=None, d_fi
     shape, _, nbytes, n = _inputs("linrec_bwd", x, g, in_gate, decay, S, gate, input_scale)
     dev = x.device
     b, L, C = x.shape
-    ssd._check(dy, "dy", x.dtype, (b, L, C), dev)
-    ssd._check(initial_states, "initial_states", torch.float32, (S, C), dev)
-    ssd._check(d_final_states, "d_final_states", torch.float32, (S, C), dev)
-    ssd._check(seq_idx, "seq_idx", torch.int32, (b, L), dev)
-    ssd._check(chunk_states, "chunk_states", torch.float32, (n, C), dev)
-    workspace = _workspace(workspace, nbytes, dev)
-    out = {"dx": torch.empty((b, L, C), dtype=x.dtype, device=dev),
-           "dg": torch.empty((b, L, C), dtype=g.dtype, device=dev),
-           "d_in_gate": None if in_gate is None else torch.empty((b, L, C), dtype=x.dtype, device=dev),
-           "ddecay": torch.empty((C,), dtype=torch.float32, device=dev) if decay is not None and want_ddecay else None,
-           "d_initial_states": (torch.empty((S, C), dtype=torch.float32, device=dev)
-                                if want_d_initial_states else None)}
-    lib = load_library()
-    with _on(dev):
-        rc = lib.linrec_bwd(ctypes.byref(shape), ssd._ptr(x), ssd._ptr(g), ssd._ptr(in_gate), ssd._ptr(decay),
-                            ssd._ptr(initial_states), ssd._ptr(seq_idx), ssd._ptr(chunk_states), ssd._ptr(dy),
-                            ssd._ptr(d_final_states), ssd._ptr(out["dx"]), ssd._ptr(out["dg"]),
-                            ssd._ptr(out["d_in_gate"]), ssd._ptr(out["ddecay"]), ssd._ptr(out["d_initial_states"]),
-                            ssd._ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev))
-    if rc:
-        raise ssd.SsdError(rc, "linrec_bwd")
+    _check(dy, "dy", x.dtype, x.shape, dev)
+    _check(initial_states, "initial_states", F32, (S, C), dev)
+    _check(d_final_states, "d_final_states", F32, (S, C), dev)
+    _check(seq_idx, "seq_idx", torch.int32, (b, L), dev)
+    _check(chunk_states, "chunk_states", F32, (n, C), dev)
+    workspace, nbytes = _workspace(workspace, nbytes, dev)
+    out = {"dx": _like(x), "dg": _like(g), "d_in_gate": None if in_gate is None else _like(x),
+           "ddecay": x.new_empty((C,), dtype=F32) if decay is not None and want_ddecay else None,
+           "d_initial_states": x.new_empty((S, C), dtype=F32) if want_d_initial_states else None}
+    _call("linrec_bwd", load_library().linrec_bwd, dev, shape, x.data_ptr(), g.data_ptr(), _ptr(in_gate), _ptr(decay),
+          _ptr(initial_states), _ptr(seq_idx), _ptr(chunk_states), dy.data_ptr(), _ptr(d_final_states),
+          out["dx"].data_ptr(), out["dg"].data_ptr(), _ptr(out["d_in_gate"]), _ptr(out["ddecay"]),
+          _ptr(out["d_initial_states"]), workspace.data_ptr(), nbytes)
     return out
 
 
@@ -230,22 +217,18 @@ def linrec_step(x, g, states, in_gate=None, decay=None, state_indices=None, gate
         raise ValueError(f"linrec_step takes up to {MAX_STEP_TOKENS} tokens a row; got {T} (use linrec_fwd)")
     if states.dim() != 2:
         raise ValueError("states is (slots, channels)")
-    ssd._check(states, "states", torch.float32, (states.shape[0], C), dev)
+    _check(states, "states", F32, (states.shape[0], C), dev)
     if state_indices is None:
         if states.shape[0] < b:
             raise ValueError(f"states holds {states.shape[0]} states for {b} rows")
     else:
-        ssd._check(state_indices, "state_indices", torch.int32, (b,), dev)
+        _check(state_indices, "state_indices", torch.int32, (b,), dev)
     if out is None:
-        out = torch.empty((b, T, C), dtype=x.dtype, device=dev)
+        out = _like(x)
     else:
-        ssd._check(out, "out", x.dtype, (b, T, C), dev)
-    lib = load_library()
-    with _on(dev):
-        rc = lib.linrec_step(ctypes.byref(shape), ssd._ptr(x), ssd._ptr(g), ssd._ptr(in_gate), ssd._ptr(decay),
-                             states.data_ptr(), states.shape[0], ssd._ptr(state_indices), out.data_ptr(), _stream(dev))
-    if rc:
-        raise ssd.SsdError(rc, "linrec_step")
+        _check(out, "out", x.dtype, x.shape, dev)
+    _call("linrec_step", load_library().linrec_step, dev, shape, x.data_ptr(), g.data_ptr(), _ptr(in_gate),
+          _ptr(decay), states.data_ptr(), states.shape[0], _ptr(state_indices), out.data_ptr())
     for t in (states, out):
         if not t.is_inference():
             torch.autograd.graph.increment_version(t)

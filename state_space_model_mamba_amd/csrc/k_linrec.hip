@@ -13,8 +13,8 @@ namespace linrec {
 
 using ssd::bf16_t;
 
-template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(THR) FWD_OCC void k_linrec(Problem p) {
-  constexpr int V = VALS<T, false>, CB = 64 * V;
+template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(Fwd::THR) void k_linrec(Problem p) {
+  constexpr int ROWS = Fwd::ROWS, WAVES = Fwd::WAVES, V = Fwd::VALS<T>, CB = 64 * V;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
   __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], enter[CB];
   __shared__ int cuts;
@@ -24,7 +24,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   // lanes past the last channels take those again: they write the same values to the same places
   const int c = cb * CB + lane * V < p.C ? cb * CB + lane * V : p.C - V;
   const uint32_t ct = lane_offset<T>(c), cg = lane_offset<G>(c);
-  const int r0 = __builtin_amdgcn_readfirstlane(chunk * CHUNK + wave * ROWS), rows = p.R - r0;   // rows: those there are
+  const int r0 = __builtin_amdgcn_readfirstlane(chunk * Fwd::CHUNK + wave * ROWS), rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS];
   Raw<G, V> g[ROWS];
   Cursor at(p, rows > 0 ? r0 : p.R - 1);
@@ -37,7 +37,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   }
   Raw<float, V> dk;
   if (GATE == LINREC_GATE_DECAY) dk.load(p.decay + c);
-  const uint32_t starts = starts_at(p, r0);
+  const uint32_t starts = starts_at<ROWS>(p, r0);
   const bool cut = starts & ((1u << ROWS) - 1);
   float a[ROWS][V], b[ROWS][V];
 #pragma unroll
@@ -111,7 +111,11 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
           H[v] = onto(f, fh[w][lane * V + v], H[v]);
         }
       }
-      join<V>(p, p.states, chunk, cb, c, cuts != 0, A, H, h, [](int k) { return k; });
+      const int last = p.spans - 1;
+      join<V>(p, p.states, chunk, cb, c, cuts != 0, A, H, h, [last](int k) {
+        const int s = (k + 1) * (Fwd::CHUNK / SPAN) - 1;
+        return s < last ? s : last;
+      });
 #pragma unroll
       for (int v = 0; v < V; ++v) enter[lane * V + v] = h[v];
     }
@@ -119,13 +123,18 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = enter[lane * V + v];
   }
-  if (!p.y) return;
   for (int w = 0; w < wave; ++w) {
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = onto(fa[w][lane * V + v], fh[w][lane * V + v], h[v]);
   }
+  if (p.keep && wave * ROWS % SPAN == 0 && wave > 0 && rows > 0) {   // a span of the chunk ends before the wave's rows
+    Raw<float, V> f;
+    f.set(h);
+    f.store(p.states + (static_cast<int64_t>(chunk) * (Fwd::CHUNK / SPAN) + wave * ROWS / SPAN - 1) * p.C + c);
+  }
+  if (!p.y) return;
   int64_t y = static_cast<int64_t>(r0) * p.C;
-  const uint32_t ends = p.final ? ends_at(p, r0, starts) : 0;
+  const uint32_t ends = p.final ? ends_at<ROWS>(p, r0, starts) : 0;
   auto walk = [&](auto all) {   // all rows are there, and none begins or ends a sequence that matters
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
@@ -218,7 +227,7 @@ __global__ __launch_bounds__(SET_THR) void k_linrec_setup(Problem p, int number,
 }
 
 int launch_setup(const Problem& p, bool number, hipStream_t st) {
-  const int64_t n = p.chunks == 1 ? 0 : static_cast<int64_t>(p.cblocks) * (p.chunks + LINE);
+  const int64_t n = p.spans == 1 ? 0 : static_cast<int64_t>(p.cblocks) * (p.spans + LINE);   // the backward's, which are more
   const int64_t blocks = (n + 4 * SET_THR - 1) / (4 * SET_THR), most = 512;
   const int64_t grid = (blocks < most ? blocks : most) + number;
   if (grid == 0) return SSD_OK;
@@ -228,8 +237,9 @@ int launch_setup(const Problem& p, bool number, hipStream_t st) {
 
 namespace {
 template <typename T, int GATE, int SCALE, bool ING> int go(Problem p, hipStream_t st) {
-  p.cblocks = (p.C + 64 * VALS<T, false> - 1) / (64 * VALS<T, false>);
-  hipLaunchKernelGGL((k_linrec<T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(THR), 0, st, p);
+  p.cblocks = (p.C + 64 * Fwd::VALS<T> - 1) / (64 * Fwd::VALS<T>);
+  p.chunks = (p.R + Fwd::CHUNK - 1) / Fwd::CHUNK;
+  hipLaunchKernelGGL((k_linrec<T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(Fwd::THR), 0, st, p);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 template <typename T, int GATE, int SCALE> int by_in(const Problem& p, hipStream_t st) {

@@ -15,8 +15,8 @@ namespace linrec {
 
 using ssd::bf16_t;
 
-template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(THR) void k_linrec_bwd(Problem p) {
-  constexpr int V = VALS<T, true>, CB = 64 * V;
+template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(Bwd::THR) void k_linrec_bwd(Problem p) {
+  constexpr int ROWS = Bwd::ROWS, WAVES = Bwd::WAVES, THR = Bwd::THR, V = Bwd::VALS<T>, CB = 64 * V;
   constexpr bool DECAY = GATE == LINREC_GATE_DECAY;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
   __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], fc[WAVES][CB], enter[CB];
@@ -28,7 +28,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   // lanes past the last channels take those again: they write the same values to the same places
   const int c = cb * CB + lane * V < p.C ? cb * CB + lane * V : p.C - V;
   const uint32_t ct = lane_offset<T>(c), cg = lane_offset<G>(c);
-  const int r0 = __builtin_amdgcn_readfirstlane(chunk * CHUNK + wave * ROWS), rows = p.R - r0;   // rows: those there are
+  const int r0 = __builtin_amdgcn_readfirstlane(chunk * Bwd::CHUNK + wave * ROWS), rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS], dy[ROWS];
   Raw<G, V> g[ROWS];
   Cursor at(p, rows > 0 ? r0 : p.R - 1);
@@ -44,7 +44,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
       yat += p.C;
     }
   }
-  const uint32_t starts = starts_at(p, r0), ends = p.dfinal ? ends_at(p, r0, starts) : 0;
+  const uint32_t starts = starts_at<ROWS>(p, r0), ends = p.dfinal ? ends_at<ROWS>(p, r0, starts) : 0;
   const bool cut = starts & ((1u << ROWS) - 1);
   // Of every element its decay, its input factor, and what it adds to the state, later the state before it; and in LDS the
   // sigmoids of its gates: the lane's registers for them as well would leave room for one block a CU.
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(RED_COLS * RED_ROWS) void k_linrec_reduce(Problem p
   double s = 0.0;
   if (c < p.C) {
 #pragma unroll 4
-    for (int k = lr; k < p.chunks; k += RED_ROWS) s += static_cast<double>(p.slots[static_cast<int64_t>(k) * p.C + c]);
+    for (int k = lr; k < p.spans; k += RED_ROWS) s += static_cast<double>(p.slots[static_cast<int64_t>(k) * p.C + c]);
   }
   part[lr][lc] = s;
   __syncthreads();
@@ -290,8 +290,9 @@ __global__ __launch_bounds__(RED_COLS * RED_ROWS) void k_linrec_reduce(Problem p
 
 namespace {
 template <typename T, int GATE, int SCALE, bool ING> int go(Problem p, hipStream_t st) {
-  p.cblocks = (p.C + 64 * VALS<T, true> - 1) / (64 * VALS<T, true>);
-  hipLaunchKernelGGL((k_linrec_bwd<T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(THR), 0, st, p);
+  p.cblocks = (p.C + 64 * Bwd::VALS<T> - 1) / (64 * Bwd::VALS<T>);
+  p.chunks = p.spans;
+  hipLaunchKernelGGL((k_linrec_bwd<T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(Bwd::THR), 0, st, p);
   if (GATE == LINREC_GATE_DECAY && p.ddecay)
     hipLaunchKernelGGL(k_linrec_reduce, dim3(static_cast<unsigned>((p.C + RED_COLS - 1) / RED_COLS)), dim3(RED_COLS * RED_ROWS), 0, st, p);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;

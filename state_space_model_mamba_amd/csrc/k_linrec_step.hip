@@ -9,6 +9,8 @@ namespace linrec {
 
 using ssd::bf16_t;
 
+template <typename T> constexpr int STEP_VALS = 8 / static_cast<int>(sizeof(T));
+
 struct StepArgs {
   const void *x, *g, *i;
   const float* decay;
@@ -20,7 +22,7 @@ struct StepArgs {
 };
 
 template <typename T, int GATE, int SCALE> __global__ __launch_bounds__(64) void k_linrec_step(StepArgs s) {
-  constexpr int V = VALS<T, false>;
+  constexpr int V = STEP_VALS<T>;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
   const int l = static_cast<int>(threadIdx.x);
   const int c0 = (static_cast<int>(blockIdx.x) * 64 + l) * V;
@@ -91,7 +93,7 @@ template <typename T, int GATE, int SCALE> __global__ __launch_bounds__(64) void
 
 namespace {
 template <typename T, int GATE> int by_scale(const StepArgs& s, int scale, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>((s.C + 64 * VALS<T, false> - 1) / (64 * VALS<T, false>)), static_cast<unsigned>(s.B));
+  const dim3 grid(static_cast<unsigned>((s.C + 64 * STEP_VALS<T> - 1) / (64 * STEP_VALS<T>)), static_cast<unsigned>(s.B));
   switch (scale) {
     case LINREC_INPUT_ONE: hipLaunchKernelGGL((k_linrec_step<T, GATE, LINREC_INPUT_ONE>), grid, dim3(64), 0, st, s); break;
     case LINREC_INPUT_COMPLEMENT: hipLaunchKernelGGL((k_linrec_step<T, GATE, LINREC_INPUT_COMPLEMENT>), grid, dim3(64), 0, st, s); break;

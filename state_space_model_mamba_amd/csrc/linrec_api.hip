@@ -42,9 +42,9 @@ size_t place(Problem& p, bool backward, char* base) {
     at += (bytes + 255) / 256 * 256;
     return r;
   };
-  const size_t n = static_cast<size_t>(p.chunks) * p.C;
+  const size_t n = static_cast<size_t>(p.spans) * p.C;
   p.starts = reinterpret_cast<int32_t*>(take((static_cast<size_t>(p.nseqs) + 1) * 4));
-  p.sync = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(p.cblocks) * (p.chunks + linrec::LINE) * 4));
+  p.sync = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(p.cblocks) * (p.spans + linrec::LINE) * 4));
   p.agg = reinterpret_cast<float2*>(take(n * sizeof(float2)));
   p.states = reinterpret_cast<float*>(take(n * 4));
   if (backward) {
@@ -61,11 +61,11 @@ int problem(const linrec_shape* s, Problem& p) {
   p.L = static_cast<int>(s->seqlen);
   p.C = static_cast<int>(s->channels);
   p.nseqs = static_cast<int>(s->nseqs);
-  p.chunks = (p.R + linrec::CHUNK - 1) / linrec::CHUNK;
+  p.spans = (p.R + linrec::SPAN - 1) / linrec::SPAN;
   // the backward's, which are the narrower: what is sized by them is enough for the forward's
-  const int cb = 64 * (s->io_dtype == SSD_IO_BF16 ? linrec::VALS<ssd::bf16_t, true> : linrec::VALS<float, true>);
+  const int cb = 64 * (s->io_dtype == SSD_IO_BF16 ? linrec::Bwd::VALS<ssd::bf16_t> : linrec::Bwd::VALS<float>);
   p.cblocks = (p.C + cb - 1) / cb;
-  if (static_cast<int64_t>(p.chunks) * p.cblocks > INT_MAX / 2) return SSD_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<int64_t>(p.spans) * p.cblocks > INT_MAX / 2) return SSD_ERR_UNSUPPORTED_SHAPE;
   int64_t st[6];
   linrec_strides(*s, st);
   p.x_sb = st[0]; p.x_sl = st[1];
@@ -98,7 +98,7 @@ int linrec_chunks(const linrec_shape* shape, int64_t* chunks) {
   const int rc = problem(shape, p);
   if (rc != SSD_OK) return rc;
   if (!chunks) return SSD_ERR_INVALID_ARG;
-  *chunks = p.chunks;
+  *chunks = p.spans;
   return SSD_OK;
 }
 
@@ -124,6 +124,7 @@ int linrec_fwd(const linrec_shape* shape, const void* x, const void* g, const vo
   p.y = y;
   p.final = final_states;
   if (chunk_states) p.states = chunk_states;
+  p.keep = chunk_states != nullptr;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if ((rc = linrec::launch_setup(p, p.starts != nullptr, st)) != SSD_OK) return rc;
   return linrec::launch_fwd(p, *shape, st);
@@ -151,6 +152,7 @@ int linrec_bwd(const linrec_shape* shape, const void* x, const void* g, const vo
   if (chunk_states) {
     p.states = const_cast<float*>(chunk_states);
   } else {
+    p.keep = 1;
     if ((rc = linrec::launch_fwd(p, *shape, st)) != SSD_OK) return rc;
     if ((rc = linrec::launch_setup(p, false, st)) != SSD_OK) return rc;
   }

@@ -10,43 +10,45 @@
 
 namespace linrec {
 
-// A chunk's rows by a block: WAVES waves of ROWS rows each.  A lane holds 8 bytes of x of each row in the forward, 4 in
-// the backward, which keeps up to seven values of every element over the chunks' chain and not two.
-#ifndef LR_ROWS
-#define LR_ROWS 8
-#endif
-#ifndef LR_WAVES
-#define LR_WAVES 8
-#endif
-#ifndef LR_FNB
-#define LR_FNB 8
-#endif
-#ifndef LR_BNB
-#define LR_BNB 4
-#endif
-constexpr int ROWS = LR_ROWS, WAVES = LR_WAVES, CHUNK = ROWS * WAVES, THR = 64 * WAVES;
-template <typename T, bool BWD> constexpr int VALS = (BWD ? LR_BNB : LR_FNB) / static_cast<int>(sizeof(T));
+// The states are kept every SPAN rows, from the forward for the backward.
+constexpr int SPAN = 64;
 
+#ifndef LR_F
+#define LR_F 16, 8, 4
+#endif
+#ifndef LR_B
+#define LR_B 8, 8, 4
+#endif
+// A chunk, a block's rows: WAVES waves of ROWS rows each, a lane with BYTES of x of every row.
+template <int R, int W, int B> struct Lay {
+  static constexpr int ROWS = R, WAVES = W, BYTES = B, CHUNK = R * W, THR = 64 * W;
+  template <typename T> static constexpr int VALS = B / static_cast<int>(sizeof(T));
+};
+using Fwd = Lay<LR_F>;
+using Bwd = Lay<LR_B>;
+static_assert(Fwd::CHUNK % SPAN == 0 && SPAN % Fwd::ROWS == 0 && Bwd::CHUNK == SPAN, "states at the ends of spans");
 constexpr int LINE = 32;   // words of a cache line
 
 struct Problem {
   int R, L, C, nseqs;      // rows (batch * seqlen), rows of a batch row, channels, sequences
-  int chunks, cblocks;     // chunks of CHUNK rows, blocks of 64 VALS channels
+  int spans;               // of SPAN rows
+  int chunks, cblocks;     // a kernel's chunks and blocks of 64 VALS channels
   int64_t x_sb, x_sl, g_sb, g_sl, i_sb, i_sl;
   // inputs
   const void *x, *g, *i, *dy;
   const float *decay, *h0, *dfinal;
   const int32_t* seq_idx;
+  int keep;                // all spans' states are wanted, not only the chain's
   // outputs
   void *y, *dx, *dg, *di;
   float *final, *ddecay, *dh0;
   // workspace
   int32_t* starts;         // (nseqs + 1) first rows (seq_idx and states given)
   uint32_t* sync;          // (cblocks, LINE): tickets; (cblocks, chunks): what of a chunk is there
-  float2* agg;             // (chunks, C): a chunk's factor and what it adds
-  float* states;           // (chunks, C): the state after each chunk
-  float* carry;            // (chunks, C): what a chunk hands to the rows before it (backward)
-  float* slots;            // (chunks, C): ddecay of each chunk (backward)
+  float2* agg;             // (spans, C): a chunk's factor and what it adds, at its last span
+  float* states;           // (spans, C): the state after each span
+  float* carry;            // (spans, C): what a span hands to the rows before it (backward)
+  float* slots;            // (spans, C): ddecay of each span (backward)
 };
 
 // the tickets and marks, and with `number` the sequences' first rows, before either of the others
@@ -200,12 +202,13 @@ __device__ __forceinline__ int ticket(const Problem& p, int cb) {
 }
 
 // One wave, for the lane's V channels from c on: the state before the chunk at `place` of the chain, and A, H onto it left
-// for the chunks behind.  chunk_at(place): the chunk there; after: the states behind the chunks; cut: a sequence starts in it.
-template <int V, typename ChunkAt>
+// for the chunks behind.  row_of(place): where the chunk there has its row in agg and in `after`, the states behind the
+// chunks; cut: a sequence starts in it.
+template <int V, typename RowOf>
 __device__ __forceinline__ void join(const Problem& p, float* after, int place, int cb, int c, bool cut, const float (&A)[V],
-                                     const float (&H)[V], float (&before)[V], ChunkAt chunk_at) {
+                                     const float (&H)[V], float (&before)[V], RowOf row_of) {
   const int lane = static_cast<int>(threadIdx.x) & 63;
-  const int64_t mine = static_cast<int64_t>(chunk_at(place)) * p.C + c;
+  const int64_t mine = static_cast<int64_t>(row_of(place)) * p.C + c;
   uint32_t* marks = p.sync + static_cast<int64_t>(p.cblocks) * LINE + static_cast<int64_t>(cb) * p.chunks;
   auto mark = [&](uint32_t m) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the values have arrived
@@ -241,7 +244,7 @@ __device__ __forceinline__ void join(const Problem& p, float* after, int place, 
     asm volatile("" ::: "memory");
     int from = place - 1 - back;
     if (from >= 0) {
-      const int64_t at = static_cast<int64_t>(chunk_at(from)) * p.C + c;
+      const int64_t at = static_cast<int64_t>(row_of(from)) * p.C + c;
 #pragma unroll
       for (int v = 0; v < V; ++v) before[v] = take(after + at + v);
     }
@@ -251,7 +254,7 @@ __device__ __forceinline__ void join(const Problem& p, float* after, int place, 
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         if (q + i < place && q + i >= 0) {
-          const int64_t at = static_cast<int64_t>(chunk_at(q + i)) * p.C + c;
+          const int64_t at = static_cast<int64_t>(row_of(q + i)) * p.C + c;
 #pragma unroll
           for (int v = 0; v < V; ++v) f[i][v] = take(p.agg + at + v);
         }
@@ -297,8 +300,8 @@ struct Cursor {
   }
 };
 
-// bit j: a sequence starts at row r0 + j (j <= ROWS; the last bit tells whether the wave's last row ends one)
-__device__ __forceinline__ uint32_t starts_at(const Problem& p, int r0) {
+// bit j: a sequence starts at row r0 + j (j <= ROWS < 32; the last bit tells whether the wave's last row ends one)
+template <int ROWS> __device__ __forceinline__ uint32_t starts_at(const Problem& p, int r0) {
   const int j = static_cast<int>(threadIdx.x) & 63, r = r0 + j;
   bool s = false;
   if (j <= ROWS && r < p.R) s = r % p.L == 0 || (p.seq_idx && p.seq_idx[r] != p.seq_idx[r - 1]);
@@ -306,7 +309,7 @@ __device__ __forceinline__ uint32_t starts_at(const Problem& p, int r0) {
 }
 
 // bit j: row r0 + j is the last of its sequence
-__device__ __forceinline__ uint32_t ends_at(const Problem& p, int r0, uint32_t starts) {
+template <int ROWS> __device__ __forceinline__ uint32_t ends_at(const Problem& p, int r0, uint32_t starts) {
   return starts >> 1 | (r0 < p.R && p.R - r0 <= ROWS ? 1u << (p.R - 1 - r0) : 0u);
 }
 
@@ -324,9 +327,3 @@ __device__ __forceinline__ int sequence_of(const Problem& p, int r) {
 #endif
 
 }  // namespace linrec
-#ifndef BWD_OCC
-#define BWD_OCC
-#endif
-#ifndef FWD_OCC
-#define FWD_OCC
-#endif

@@ -39,7 +39,9 @@ struct Args {
   float eps, alpha, inv_w;
 };
 
-// V values of type S, as they lie in memory
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// V values of type S, as they lie in memory.  PASS: not to be kept in the caches (the nontemporal hint).
 template <typename S, int V> struct Raw {
   static constexpr int N = V * static_cast<int>(sizeof(S)) / 16;
   uint4 u[N];
@@ -47,9 +49,13 @@ template <typename S, int V> struct Raw {
 #pragma unroll
     for (int i = 0; i < N; ++i) u[i] = ssd::zero_u4();
   }
-  __device__ __forceinline__ void load(const S* p) {
+  template <bool PASS = false> __device__ __forceinline__ void load(const S* p) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < N; ++i) {
+      const u32x4_t* q = reinterpret_cast<const u32x4_t*>(p) + i;
+      const u32x4_t t = PASS ? __builtin_nontemporal_load(q) : *q;
+      u[i] = uint4{t[0], t[1], t[2], t[3]};
+    }
   }
   __device__ __forceinline__ float get(int e) const {
     constexpr int PER = 16 / static_cast<int>(sizeof(S));
@@ -57,9 +63,20 @@ template <typename S, int V> struct Raw {
   }
 };
 
-template <typename S, int V> __device__ __forceinline__ void store(S* p, const float (&f)[V]) {
+template <typename S, int V, bool PASS = false> __device__ __forceinline__ void store(S* p, const float (&f)[V]) {
+  constexpr int PER = 16 / static_cast<int>(sizeof(S));
 #pragma unroll
-  for (int e = 0; e < V; e += 4) ssd::store4f<S>(p + e, ssd::f32x4_t{f[e], f[e + 1], f[e + 2], f[e + 3]});
+  for (int e = 0; e < V; e += PER) {
+    u32x4_t w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(S) == 2) w[i] = ssd::pack_bf16x2(f[e + 2 * i], f[e + 2 * i + 1]);
+      else w[i] = __float_as_uint(f[e + i]);
+    }
+    u32x4_t* q = reinterpret_cast<u32x4_t*>(p + e);
+    if constexpr (PASS) __builtin_nontemporal_store(w, q);
+    else *q = w;
+  }
 }
 
 // sigmoid(z) and 1 - sigmoid(z), both to their last bits; with bf16 io by the hardware's exponential and reciprocal (1 ulp)
@@ -109,16 +126,18 @@ enum { NARROW = 0, WIDE1 = 1, WIDE2 = 2, WIDEST = 3 };
 constexpr int max_threads(int lay) { return lay == NARROW ? THR : lay == WIDEST ? 1024 : 512; }
 template <typename T> constexpr int pieces_a_lane(int lay) { return lay <= WIDE1 ? 1 : lay == WIDE2 ? 2 : sizeof(T) == 4 ? 4 : 2; }
 
+enum { FORWARD = 0, BACKWARD = 1, BACKWARD_PASS = 2 };   // the last: its operands pass the caches by
+
 // PRE: add_norm, else gated_norm.  EXTRA: with a bias, a scale or their gradients.  T: io dtype, R: residual dtype.
-template <typename T, typename R, int LAY, bool PRE, bool BWD, bool EXTRA>
+template <typename T, typename R, int LAY, bool PRE, int DIR, bool EXTRA>
 __global__ __launch_bounds__(max_threads(LAY)) void k_block_norm(Args a) {
   constexpr int V = ssd::Vec16<T>::N, VPL = pieces_a_lane<T>(LAY);
-  constexpr bool WIDE = LAY != NARROW;
+  constexpr bool WIDE = LAY != NARROW, BWD = DIR != FORWARD, PASS = DIR == BACKWARD_PASS;
   __shared__ float places1[2][16][1], places3[2][16][3];
   extern __shared__ __attribute__((aligned(16))) char smem[];   // narrow rows, backward: [THR][V] sums
   const int tid = static_cast<int>(threadIdx.x);
   // where the lane stands: its token among the block's, its group, and its first values in the group
-  int tl = 0, group = static_cast<int>(blockIdx.y), n0 = tid * V;
+  int tl = 0, group = static_cast<int>(blockIdx.x), n0 = tid * V;
   if constexpr (!WIDE) {
     const int place = tid / a.lpr;
     tl = place / a.gpb;
@@ -154,17 +173,17 @@ __global__ __launch_bounds__(max_threads(LAY)) void k_block_norm(Args a) {
       if (BWD) q.dr[i].zero();
       if (BWD && PRE) q.dy[i].zero();
       if (!in || !live[i]) continue;
-      q.x[i].load(static_cast<const T*>(a.x) + xo + col[i]);
-      if (!PRE && a.z) q.z[i].load(static_cast<const T*>(a.z) + zo + col[i]);
-      if ((PRE || !BWD) && a.res) q.res[i].load(static_cast<const R*>(a.res) + at + col[i]);
-      if (BWD && a.dr) q.dr[i].load(static_cast<const R*>(a.dr) + at + col[i]);
-      if (BWD && PRE && a.dy) q.dy[i].load(static_cast<const T*>(a.dy) + at + col[i]);
+      q.x[i].template load<PASS>(static_cast<const T*>(a.x) + xo + col[i]);
+      if (!PRE && a.z) q.z[i].template load<PASS>(static_cast<const T*>(a.z) + zo + col[i]);
+      if ((PRE || !BWD) && a.res) q.res[i].template load<PASS>(static_cast<const R*>(a.res) + at + col[i]);
+      if (BWD && a.dr) q.dr[i].template load<PASS>(static_cast<const R*>(a.dr) + at + col[i]);
+      if (BWD && PRE && a.dy) q.dy[i].template load<PASS>(static_cast<const T*>(a.dy) + at + col[i]);
     }
   };
   RowSum<1, WIDE> sum1{places1, a.lpr, 0};
   RowSum<3, WIDE> sum3{places3, a.lpr, 0};
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * a.tpb;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * a.tpb;
+  const int64_t stride = static_cast<int64_t>(gridDim.y) * a.tpb;
+  int64_t t = static_cast<int64_t>(blockIdx.y) * a.tpb;
   Row next;
   request(next, t + tl);
   float w[VPL][V], s[VPL][V], b[VPL][V], gw[VPL][V], gb[VPL][V], gs[VPL][V];
@@ -298,18 +317,18 @@ __global__ __launch_bounds__(max_threads(LAY)) void k_block_norm(Args a) {
           }
         }
         if (in && live[i]) {
-          if (a.dx) store<T, V>(static_cast<T*>(a.dx) + at + col[i], o1);
+          if (a.dx) store<T, V, PASS>(static_cast<T*>(a.dx) + at + col[i], o1);
           if constexpr (PRE) {
-            if (a.dres) store<R, V>(static_cast<R*>(a.dres) + at + col[i], o2);
+            if (a.dres) store<R, V, PASS>(static_cast<R*>(a.dres) + at + col[i], o2);
           } else {
-            if (a.dz) store<T, V>(static_cast<T*>(a.dz) + at + col[i], o2);
+            if (a.dz) store<T, V, PASS>(static_cast<T*>(a.dz) + at + col[i], o2);
           }
         }
       }
     }
   }
   if constexpr (BWD) {
-    float* slot = a.slots + static_cast<int64_t>(blockIdx.x) * SUMS * a.D;
+    float* slot = a.slots + static_cast<int64_t>(blockIdx.y) * SUMS * a.D;
     for (int k = 0; k < SUMS; ++k) {
       if ((!EXTRA && k) || !((a.sums >> k) & 1)) continue;
 #pragma unroll
@@ -386,7 +405,7 @@ bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) !
 // How a row lies in the lanes, and the grid.
 struct Plan {
   int lay, threads, lpr, gpb, tpb;
-  int64_t gx, gy;
+  int64_t gx, gy;                      // blocks of tokens, and of groups (which run side by side)
 };
 
 Plan plan(const block_norm_shape& s, bool bwd) {
@@ -411,29 +430,36 @@ Plan plan(const block_norm_shape& s, bool bwd) {
     p.tpb = places / p.gpb;
     p.gy = (s.groups + p.gpb - 1) / p.gpb;
   }
-  // Blocks for twice the threads that the card holds at once (forward), or half of them: each block of the backward
-  // leaves its sums in a slot
-  const int64_t most = static_cast<int64_t>(256) * (bwd ? 1024 : 4096) / p.threads / p.gy;
+  // Threads in all: the forward eight times what the card holds at once (16384 rows of 8 gated groups of 1024 bf16: 163 us
+  // at twice, 150 at four times, 144 at eight; 16384 rows of 4096 with a float32 residual: 150 us, at 16 times 160), the
+  // backward half of it, since each block leaves its sums in a slot (278 us there at half, 305 at once and at a quarter)
+  const int64_t most = static_cast<int64_t>(256) * (bwd ? 1024 : 16384) / p.threads / p.gy;
   p.gx = (tokens + p.tpb - 1) / p.tpb;
   if (p.gx > most) p.gx = most < 1 ? 1 : most;
   return p;
 }
 
-template <typename T, typename R, int LAY, bool PRE, bool BWD> int go(const Plan& p, const Args& a, hipStream_t st) {
-  const size_t lds = BWD && LAY == NARROW ? sizeof(float) * THR * ssd::Vec16<T>::N : 0;
-  const dim3 grid(static_cast<unsigned>(p.gx), static_cast<unsigned>(p.gy)), block(static_cast<unsigned>(p.threads));
-  if (a.b || a.s || (a.sums & ~1)) hipLaunchKernelGGL((k_block_norm<T, R, LAY, PRE, BWD, true>), grid, block, lds, st, a);
-  else hipLaunchKernelGGL((k_block_norm<T, R, LAY, PRE, BWD, false>), grid, block, lds, st, a);
+template <typename T, typename R, int LAY, bool PRE, int DIR> int go(const Plan& p, const Args& a, hipStream_t st) {
+  const size_t lds = DIR != FORWARD && LAY == NARROW ? sizeof(float) * THR * ssd::Vec16<T>::N : 0;
+  const dim3 grid(static_cast<unsigned>(p.gy), static_cast<unsigned>(p.gx)), block(static_cast<unsigned>(p.threads));
+  if (a.b || a.s || (a.sums & ~1)) hipLaunchKernelGGL((k_block_norm<T, R, LAY, PRE, DIR, true>), grid, block, lds, st, a);
+  else hipLaunchKernelGGL((k_block_norm<T, R, LAY, PRE, DIR, false>), grid, block, lds, st, a);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
-template <typename T, typename R, bool PRE, bool BWD> int by_width(const Plan& p, const Args& a, hipStream_t st) {
+template <typename T, typename R, bool PRE, int DIR> int by_width(const Plan& p, const Args& a, hipStream_t st) {
   switch (p.lay) {
-    case NARROW: return go<T, R, NARROW, PRE, BWD>(p, a, st);
-    case WIDE1: return go<T, R, WIDE1, PRE, BWD>(p, a, st);
-    case WIDE2: return go<T, R, WIDE2, PRE, BWD>(p, a, st);
-    default: return go<T, R, WIDEST, PRE, BWD>(p, a, st);
+    case NARROW: return go<T, R, NARROW, PRE, DIR>(p, a, st);
+    case WIDE1: return go<T, R, WIDE1, PRE, DIR>(p, a, st);
+    case WIDE2: return go<T, R, WIDE2, PRE, DIR>(p, a, st);
+    default: return go<T, R, WIDEST, PRE, DIR>(p, a, st);
   }
+}
+
+template <bool PRE, int DIR> int by_type(const block_norm_shape& s, const Plan& p, const Args& a, hipStream_t st) {
+  if (s.io_dtype == SSD_IO_F32) return by_width<float, float, PRE, DIR>(p, a, st);
+  if (s.residual_dtype == SSD_IO_F32) return by_width<bf16_t, float, PRE, DIR>(p, a, st);
+  return by_width<bf16_t, bf16_t, PRE, DIR>(p, a, st);
 }
 
 template <bool PRE, bool BWD> int launch(const block_norm_shape& s, Args& a, hipStream_t st) {
@@ -456,9 +482,11 @@ template <bool PRE, bool BWD> int launch(const block_norm_shape& s, Args& a, hip
   a.eps = s.eps;
   a.alpha = s.alpha;
   a.inv_w = 1.f / static_cast<float>(a.W);
-  if (s.io_dtype == SSD_IO_F32) return by_width<float, float, PRE, BWD>(p, a, st);
-  if (s.residual_dtype == SSD_IO_F32) return by_width<bf16_t, float, PRE, BWD>(p, a, st);
-  return by_width<bf16_t, bf16_t, PRE, BWD>(p, a, st);
+  if constexpr (!BWD) return by_type<PRE, FORWARD>(s, p, a, st);
+  // The backward's operands pass the caches by where they are more than the 256 MB of the last one: 16384 x 8192 bf16 with
+  // a gate 271 us, 286 by the caches; 1999 x 4096 float32 (164 MB, what the forward left is still there) 42 us, 33.
+  const int64_t bytes = static_cast<int64_t>(a.tokens) * a.D * (s.io_dtype == SSD_IO_BF16 ? 2 : 4) * 5;
+  return bytes > (int64_t{256} << 20) ? by_type<PRE, BACKWARD_PASS>(s, p, a, st) : by_type<PRE, BACKWARD>(s, p, a, st);
 }
 
 // The backward of either: its kernel, then the slots' sums that are wanted

@@ -27,14 +27,19 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   const int r0 = __builtin_amdgcn_readfirstlane(chunk * Fwd::CHUNK + wave * ROWS), rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS];
   Raw<G, V> g[ROWS];
-  Cursor at(p, rows > 0 ? r0 : p.R - 1);
+  auto request = [&](auto pass) {
+    constexpr bool PASS = decltype(pass)::value;
+    Cursor at(p, rows > 0 ? r0 : p.R - 1);
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    x[j].load_at(p.x, at.x, ct);
-    g[j].load_at(p.g, at.g, cg);
-    if (ING) in[j].load_at(p.i, at.i, ct);
-    if (j + 1 < rows) at.next(p);
-  }
+    for (int j = 0; j < ROWS; ++j) {
+      x[j].template load_at<PASS>(p.x, at.x, ct);
+      g[j].template load_at<PASS>(p.g, at.g, cg);
+      if (ING) in[j].template load_at<PASS>(p.i, at.i, ct);
+      if (j + 1 < rows) at.next(p);
+    }
+  };
+  if (p.pass) request(std::true_type{});
+  else request(std::false_type{});
   Raw<float, V> dk;
   if (GATE == LINREC_GATE_DECAY) dk.load(p.decay + c);
   const uint32_t starts = starts_at<ROWS>(p, r0);

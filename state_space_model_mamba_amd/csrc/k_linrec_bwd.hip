@@ -31,19 +31,24 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   const int r0 = __builtin_amdgcn_readfirstlane(chunk * Bwd::CHUNK + wave * ROWS), rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS], dy[ROWS];
   Raw<G, V> g[ROWS];
-  Cursor at(p, rows > 0 ? r0 : p.R - 1);
-  int64_t yat = static_cast<int64_t>(rows > 0 ? r0 : p.R - 1) * p.C;
+  auto request = [&](auto pass) {
+    constexpr bool PASS = decltype(pass)::value;
+    Cursor at(p, rows > 0 ? r0 : p.R - 1);
+    int64_t yat = static_cast<int64_t>(rows > 0 ? r0 : p.R - 1) * p.C;
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    g[j].load_at(p.g, at.g, cg);
-    x[j].load_at(p.x, at.x, ct);
-    if (ING) in[j].load_at(p.i, at.i, ct);
-    dy[j].load_at(p.dy, yat, ct);
-    if (j + 1 < rows) {
-      at.next(p);
-      yat += p.C;
+    for (int j = 0; j < ROWS; ++j) {
+      g[j].template load_at<PASS>(p.g, at.g, cg);
+      x[j].template load_at<PASS>(p.x, at.x, ct);
+      if (ING) in[j].template load_at<PASS>(p.i, at.i, ct);
+      dy[j].template load_at<PASS>(p.dy, yat, ct);
+      if (j + 1 < rows) {
+        at.next(p);
+        yat += p.C;
+      }
     }
-  }
+  };
+  if (p.pass) request(std::true_type{});
+  else request(std::false_type{});
   const uint32_t starts = starts_at<ROWS>(p, r0), ends = p.dfinal ? ends_at<ROWS>(p, r0, starts) : 0;
   const bool cut = starts & ((1u << ROWS) - 1);
   // Of every element its decay, its input factor, and what it adds to the state, later the state before it; and in LDS the

@@ -86,6 +86,9 @@ int inputs(const linrec_shape* shape, const void* x, const void* g, const void* 
     if (misaligned(q)) return SSD_ERR_MISALIGNED;
   p.x = x; p.g = g; p.i = in_gate; p.decay = decay; p.h0 = h0; p.seq_idx = seq_idx;
   if (!seq_idx || !states) p.starts = nullptr;
+  // Read past the caches what is more than the 256 MB of the last one holds with the results.
+  const int64_t io = shape->io_dtype == SSD_IO_BF16 ? 2 : 4, gates = shape->gate == LINREC_GATE_LOG ? 4 : io;
+  p.pass = static_cast<int64_t>(p.R) * p.C * (2 * io + gates + (in_gate ? io : 0)) > (int64_t{256} << 20);
   return SSD_OK;
 }
 

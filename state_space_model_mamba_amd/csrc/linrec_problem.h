@@ -38,6 +38,7 @@ struct Problem {
   const void *x, *g, *i, *dy;
   const float *decay, *h0, *dfinal;
   const int32_t* seq_idx;
+  int pass;                // the operands are more than the last cache holds
   int keep;                // all spans' states are wanted, not only the chain's
   // outputs
   void *y, *dx, *dg, *di;
@@ -57,15 +58,16 @@ int launch_fwd(const Problem& p, const linrec_shape& s, hipStream_t st);   // (p
 int launch_bwd(const Problem& p, const linrec_shape& s, hipStream_t st);
 
 #ifdef __HIPCC__
-// V values of type S as they lie in memory (4 to 16 bytes)
+// V values of type S as they lie in memory (4 to 16 bytes).  PASS: not to be kept in the caches (the nontemporal hint).
 template <typename S, int V> struct Raw {
   static constexpr int N = V * static_cast<int>(sizeof(S)) / 4;
   typedef uint32_t words __attribute__((ext_vector_type(N)));
   words w;
   __device__ __forceinline__ void load(const S* p) { w = *reinterpret_cast<const words*>(p); }
   // at a lane's byte offset from a row's address, which is the wave's: no 64-bit address per lane
-  __device__ __forceinline__ void load_at(const void* base, int64_t row, uint32_t off) {
-    w = *reinterpret_cast<const words*>(reinterpret_cast<const char*>(static_cast<const S*>(base) + row) + off);
+  template <bool PASS> __device__ __forceinline__ void load_at(const void* base, int64_t row, uint32_t off) {
+    const words* p = reinterpret_cast<const words*>(reinterpret_cast<const char*>(static_cast<const S*>(base) + row) + off);
+    w = PASS ? __builtin_nontemporal_load(p) : *p;
   }
   __device__ __forceinline__ void store_at(void* base, int64_t row, uint32_t off) const {
     *reinterpret_cast<words*>(reinterpret_cast<char*>(static_cast<S*>(base) + row) + off) = w;

@@ -137,6 +137,14 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
     f.set(h);
     f.store(p.states + (static_cast<int64_t>(chunk) * (Fwd::CHUNK / SPAN) + wave * ROWS / SPAN - 1) * p.C + c);
   }
+  if (p.keep && p.chunks == 1 && wave == WAVES - 1) {   // the last, which no chain leaves
+    Raw<float, V> f;
+    float e[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = onto(A[v], H[v], h[v]);
+    f.set(e);
+    f.store(p.states + static_cast<int64_t>(p.spans - 1) * p.C + c);
+  }
   if (!p.y) return;
   int64_t y = static_cast<int64_t>(r0) * p.C;
   const uint32_t ends = p.final ? ends_at<ROWS>(p, r0, starts) : 0;

@@ -49,6 +49,9 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   };
   if (p.pass) request(std::true_type{});
   else request(std::false_type{});
+  Raw<float, V> entering;   // the state that enters the chunk
+  if (chunk > 0) entering.load(p.states + static_cast<int64_t>(chunk - 1) * p.C + c);
+  else entering.w = 0;
   const uint32_t starts = starts_at<ROWS>(p, r0), ends = p.dfinal ? ends_at<ROWS>(p, r0, starts) : 0;
   const bool cut = starts & ((1u << ROWS) - 1);
   // Of every element its decay, its input factor, and what it adds to the state, later the state before it; and in LDS the
@@ -142,10 +145,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   if (lane == 0 && cut) cuts = 1;
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    H[v] = chunk > 0 ? p.states[static_cast<int64_t>(chunk - 1) * p.C + c + v] : 0.f;
-    cr[v] = 0.f;
-  }
+  for (int v = 0; v < V; ++v) H[v] = entering.get(v), cr[v] = 0.f;
   if (p.chunks > 1) {
     if (wave == 0) {
       float B[V];

@@ -21,9 +21,10 @@
  * the SSD layer's state update with one state value a channel and a decay of
  * its own for every channel and token (an SSD head shares one).
  *
- * Determinism.  Every output element has one writer and every sum one order;
- * no floating-point atomics.  The output bytes depend on the inputs, the shape
- * and the library build only.
+ * Determinism.  Every output element has one value and every sum one order;
+ * the only atomics hand out work and pass finished values on (blocks wait for
+ * blocks that began before them).  The output bytes depend on the inputs, the
+ * shape and the library build only.
  *
  * Layouts (row-major), C = channels:
  *   x, y, in_gate, dy, dx, d_in_gate   (batch, seqlen, C)   io dtype (ssd_io_dtype)
@@ -77,15 +78,16 @@ typedef struct {
   int32_t reserved;    /* must be 0 */
 } linrec_shape;
 
-/* Chunks that a whole-sequence call takes the batch * seqlen rows in: the rows of chunk_states. */
+/* The rows of chunk_states, which holds the state after every 64 of the batch * seqlen rows, and after the last. */
 int linrec_chunks(const linrec_shape* shape, int64_t* chunks);
 
-/* Workspace bytes of linrec_fwd (backward == 0) or linrec_bwd (backward != 0). */
+/* Workspace bytes of linrec_fwd (backward == 0) or linrec_bwd (backward != 0): 12 or 20 for every channel and 64 rows,
+ * some KB besides. */
 int linrec_workspace_size(const linrec_shape* shape, int backward, size_t* bytes);
 
 /*
  * y, final_states (nullable): the state after each sequence's last position,
- * and chunk_states (nullable): the states between chunks, for linrec_bwd.
+ * and chunk_states (nullable): the states between chunks of rows, for linrec_bwd.
  * in_gate, initial_states and seq_idx may be NULL; decay goes with
  * LINREC_GATE_DECAY.  nseqs must be the number of sequences that seq_idx marks
  * whenever states are given or asked for: sequences past nseqs enter with

@@ -7,6 +7,11 @@
 // makes A zero.  So do a wave's rows within a chunk: their (A, H) meet in LDS,
 // the chunks' in memory (linrec_problem.h).  A lane keeps its rows' a and b
 // meanwhile, so every input is read once.
+//
+// Bound by HBM, and by how well two blocks a CU cover each other's phases.
+// 16384 rows of 8192 bf16 channels with all gates (1.07 GB): 239 to 260 us,
+// 4.1 to 4.5 TB/s; 230 with the chain cut out, 220 without the gates'
+// arithmetic as well, which takes 143 us of the vector units' time.
 #include "linrec_problem.h"
 
 namespace linrec {

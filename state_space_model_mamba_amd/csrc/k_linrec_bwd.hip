@@ -8,7 +8,14 @@
 //
 // and the gates' gradients follow from dl and du row by row.  The c form the
 // same recurrence as the h, read from the end; the h are formed again from the
-// states between the chunks, in float32.
+// states between the spans, in float32, so neither they nor y are read.
+//
+// Bound by HBM and, beside it, by the gates' arithmetic: of 485 us at 16384
+// rows of 8192 bf16 channels with all gates (1.88 GB, 3.9 TB/s) the vector units
+// are busy for 295; 453 with the chain cut out, 406 without the gates as well.
+// With all seven values of an element kept in registers over the chain, one
+// block a CU, it took 900; with the next chunk's operands requested ahead by
+// blocks that stay, 735.
 #include "linrec_problem.h"
 
 namespace linrec {

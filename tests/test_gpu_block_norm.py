@@ -231,6 +231,18 @@ def test_autograd_matches_the_entry_points_and_a_replayed_graph():
             t.zero_()
 
 
+def test_one_tensor_in_two_places_and_a_broadcast_gate():
+    d = cuda(make(2, 30, 64, "f32", seed=11))
+    x = d["x"].clone().requires_grad_(True)
+    got = torch.autograd.grad(bn.add_norm(x, x, d["weight"]), x, (d["dy"], d["dr"]))[0]
+    g = bn.add_norm_bwd(d["x"], d["x"], d["weight"], 1.0, d["dy"], d["dr"])
+    assert torch.equal(got, g["dx"] + g["dresidual"])
+    z = torch.randn((1, 30, 64), device="cuda").expand(2, 30, 64)
+    a, b = (bn.gated_norm_bwd(d["x"], t, d["weight"], None, 1.0, d["dr"]) for t in (z, z.contiguous()))
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dz"], b["dz"])
+    assert torch.equal(bn.gated_norm_fwd(d["x"], z, d["weight"]), bn.gated_norm_fwd(d["x"], z.contiguous(), d["weight"]))
+
+
 def test_another_stream():
     d = cuda(make(1, 64, 512, "bf16", seed=10))
     ref = bn.add_norm_fwd(d["x"], None, d["weight"])

@@ -188,6 +188,36 @@ def test_many_blocks_repeat_their_bits():
         near(t[..., at], ref[k], ref[k + "_err"], k)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_a_chain_of_many_chunks(io):
+    # one channel block: hundreds of chunks are under way at once, each behind the one before it
+    check(make(1, 60000, 8, io, "decay", initial=False, seed=40), f"{io} 60000 rows", "decay", "unit")
+
+
+@pytest.mark.parametrize("gate,scale", [("sigmoid", "complement"), ("sigmoid", "unit"), ("decay", "unit")])
+def test_infinite_gates(gate, scale):
+    d = make(1, 100, 32, "f32", gate, seed=41)
+    d["g"][0, ::9], d["g"][0, 4::9] = float("inf"), float("-inf")
+    d["in_gate"][0, ::7], d["in_gate"][0, 3::7] = float("inf"), float("-inf")
+    kw = dict(gate=gate, input_scale=scale)
+    c = cuda(d)
+    r, g = forward(c, **kw), backward(c, **kw)
+    # the same as gates that float32 cannot tell from them
+    e = {k: v.clamp(-200, 200) if k in ("g", "in_gate") else v for k, v in c.items()}
+    s, f = forward(e, **kw), backward(e, **kw)
+    assert torch.equal(r["y"], s["y"]) and all(torch.equal(g[k], f[k]) for k in GRADS if g[k] is not None)
+    assert bool(torch.isfinite(r["y"]).all()) and bool(torch.isfinite(g["dg"]).all()) and bool(torch.isfinite(g["d_in_gate"]).all())
+
+
+def test_operands_broadcast_over_batch_or_rows():
+    d = cuda(make(3, 70, 40, "bf16", seed=42))
+    b = dict(d, g=d["g"][:1].expand(3, 70, 40), in_gate=d["in_gate"][:, :1].expand(3, 70, 40))
+    f = dict(b, g=b["g"].contiguous(), in_gate=b["in_gate"].contiguous())
+    x, y = forward(b), forward(f)
+    p, q = backward(b), backward(f)
+    assert torch.equal(x["y"], y["y"]) and all(torch.equal(p[k], q[k]) for k in ("dx", "dg", "d_in_gate"))
+
+
 def test_rows_past_32_bits():
     wide = torch.empty((300, 1 << 23), dtype=torch.bfloat16, device="cuda")   # rows 2^23 elements apart: the last past 2^31
     d = cuda(make(1, 300, 64, "bf16", seed=12))

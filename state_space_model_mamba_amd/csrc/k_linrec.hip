@@ -18,8 +18,8 @@ namespace linrec {
 
 using ssd::bf16_t;
 
-template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(Fwd::THR) void k_linrec(Problem p) {
-  constexpr int ROWS = Fwd::ROWS, WAVES = Fwd::WAVES, V = Fwd::VALS<T>, CB = 64 * V;
+template <typename L, typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(L::THR) void k_linrec(Problem p) {
+  constexpr int ROWS = L::ROWS, WAVES = L::WAVES, V = L::template VALS<T>, CB = 64 * V;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
   __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], enter[CB];
   __shared__ int cuts;
@@ -29,7 +29,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   // lanes past the last channels take those again: they write the same values to the same places
   const int c = cb * CB + lane * V < p.C ? cb * CB + lane * V : p.C - V;
   const uint32_t ct = lane_offset<T>(c), cg = lane_offset<G>(c);
-  const int r0 = __builtin_amdgcn_readfirstlane(chunk * Fwd::CHUNK + wave * ROWS), rows = p.R - r0;   // rows: those there are
+  const int r0 = __builtin_amdgcn_readfirstlane(chunk * L::CHUNK + wave * ROWS), rows = p.R - r0;   // rows: those there are
   Raw<T, V> x[ROWS], in[ROWS];
   Raw<G, V> g[ROWS];
   auto request = [&](auto pass) {
@@ -124,7 +124,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
       }
       const int last = p.spans - 1;
       join<V>(p, p.states, chunk, cb, c, cuts != 0, A, H, h, [last](int k) {
-        const int s = (k + 1) * (Fwd::CHUNK / SPAN) - 1;
+        const int s = (k + 1) * (L::CHUNK / SPAN) - 1;
         return s < last ? s : last;
       });
 #pragma unroll
@@ -142,7 +142,7 @@ template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds_
   if (p.keep && wave * ROWS % SPAN == 0 && wave > 0 && rows > 0) {   // a span of the chunk ends before the wave's rows
     Raw<float, V> f;
     f.set(h);
-    f.store(p.states + (static_cast<int64_t>(chunk) * (Fwd::CHUNK / SPAN) + wave * ROWS / SPAN - 1) * p.C + c);
+    f.store(p.states + (static_cast<int64_t>(chunk) * (L::CHUNK / SPAN) + wave * ROWS / SPAN - 1) * p.C + c);
   }
   if (p.keep && p.chunks == 1 && wave == WAVES - 1) {   // the last, which no chain leaves
     Raw<float, V> f;
@@ -246,8 +246,8 @@ __global__ __launch_bounds__(SET_THR) void k_linrec_setup(Problem p, int number,
   for (int64_t s = static_cast<int64_t>(base) + tid; s <= p.nseqs; s += SET_THR) p.starts[s] = p.R;
 }
 
-int launch_setup(const Problem& p, bool number, hipStream_t st) {
-  const int64_t n = p.spans == 1 ? 0 : static_cast<int64_t>(p.cblocks) * (p.spans + LINE);   // the backward's, which are more
+int launch_setup(const Problem& p, bool chain, bool number, hipStream_t st) {
+  const int64_t n = !chain ? 0 : static_cast<int64_t>(p.cblocks) * (p.spans + LINE);   // the backward's, which are more
   const int64_t blocks = (n + 4 * SET_THR - 1) / (4 * SET_THR), most = 512;
   const int64_t grid = (blocks < most ? blocks : most) + number;
   if (grid == 0) return SSD_OK;
@@ -256,11 +256,14 @@ int launch_setup(const Problem& p, bool number, hipStream_t st) {
 }
 
 namespace {
-template <typename T, int GATE, int SCALE, bool ING> int go(Problem p, hipStream_t st) {
-  p.cblocks = (p.C + 64 * Fwd::VALS<T> - 1) / (64 * Fwd::VALS<T>);
-  p.chunks = (p.R + Fwd::CHUNK - 1) / Fwd::CHUNK;
-  hipLaunchKernelGGL((k_linrec<T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(Fwd::THR), 0, st, p);
+template <typename L, typename T, int GATE, int SCALE, bool ING> int run(Problem p, hipStream_t st) {
+  p.cblocks = (p.C + 64 * L::template VALS<T> - 1) / (64 * L::template VALS<T>);
+  p.chunks = (p.R + L::CHUNK - 1) / L::CHUNK;
+  hipLaunchKernelGGL((k_linrec<L, T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(L::THR), 0, st, p);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+template <typename T, int GATE, int SCALE, bool ING> int go(const Problem& p, hipStream_t st) {
+  return p.R > Fwd::CHUNK && !chained_fwd(p) ? run<Short, T, GATE, SCALE, ING>(p, st) : run<Fwd, T, GATE, SCALE, ING>(p, st);
 }
 template <typename T, int GATE, int SCALE> int by_in(const Problem& p, hipStream_t st) {
   return p.i ? go<T, GATE, SCALE, true>(p, st) : go<T, GATE, SCALE, false>(p, st);

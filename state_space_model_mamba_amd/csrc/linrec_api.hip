@@ -129,7 +129,7 @@ int linrec_fwd(const linrec_shape* shape, const void* x, const void* g, const vo
   if (chunk_states) p.states = chunk_states;
   p.keep = chunk_states != nullptr;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if ((rc = linrec::launch_setup(p, p.starts != nullptr, st)) != SSD_OK) return rc;
+  if ((rc = linrec::launch_setup(p, linrec::chained_fwd(p), p.starts != nullptr, st)) != SSD_OK) return rc;
   return linrec::launch_fwd(p, *shape, st);
 }
 
@@ -151,13 +151,13 @@ int linrec_bwd(const linrec_shape* shape, const void* x, const void* g, const vo
   p.dy = dy; p.dfinal = d_final_states;
   p.dx = dx; p.dg = dg; p.di = d_in_gate; p.ddecay = ddecay; p.dh0 = d_initial_states;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if ((rc = linrec::launch_setup(p, p.starts != nullptr, st)) != SSD_OK) return rc;
+  if ((rc = linrec::launch_setup(p, linrec::chained_bwd(p), p.starts != nullptr, st)) != SSD_OK) return rc;
   if (chunk_states) {
     p.states = const_cast<float*>(chunk_states);
   } else {
     p.keep = 1;
     if ((rc = linrec::launch_fwd(p, *shape, st)) != SSD_OK) return rc;
-    if ((rc = linrec::launch_setup(p, false, st)) != SSD_OK) return rc;
+    if (linrec::chained_fwd(p) && (rc = linrec::launch_setup(p, true, false, st)) != SSD_OK) return rc;
   }
   return linrec::launch_bwd(p, *shape, st);
 }

@@ -63,6 +63,10 @@ template <typename S, int V> struct Raw {
       u[i] = uint4{t[0], t[1], t[2], t[3]};
     }
   }
+  __device__ __forceinline__ void renew() {   // the same values, of which the compiler knows nothing
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(u[i].x), "+v"(u[i].y), "+v"(u[i].z), "+v"(u[i].w));
+  }
   __device__ __forceinline__ float get(int e) const {
     constexpr int PER = 16 / static_cast<int>(sizeof(S));
     return ssd::vget<S>(u[e / PER], e % PER);
@@ -126,11 +130,13 @@ template <int K, bool WIDE> struct RowSum {
   }
 };
 
-// How a row lies in the lanes: in some lanes of a wave, or in all of a block of up to 512 or 1024 threads (512 leave a
-// lane 256 registers: the gradients of two pieces a lane fit, as they do not in 1024)
-enum { NARROW = 0, WIDE1 = 1, WIDE2 = 2, WIDEST = 3 };
+// How a row lies in the lanes: in some lanes of a wave, or in all of a block of up to 512 threads (which leaves a lane 256
+// registers: the gradients of 16 values fit) with 1, 2 or 4 pieces a lane, or of up to 1024.
+enum { NARROW = 0, WIDE1 = 1, WIDE2 = 2, WIDE4 = 3, WIDEST = 4 };
 constexpr int max_threads(int lay) { return lay == NARROW ? THR : lay == WIDEST ? 1024 : 512; }
-template <typename T> constexpr int pieces_a_lane(int lay) { return lay <= WIDE1 ? 1 : lay == WIDE2 ? 2 : sizeof(T) == 4 ? 4 : 2; }
+template <typename T> constexpr int pieces_a_lane(int lay) {
+  return lay <= WIDE1 ? 1 : lay == WIDE2 || (lay == WIDEST && sizeof(T) == 2) ? 2 : 4;
+}
 
 enum { FORWARD = 0, BACKWARD = 1, BACKWARD_PASS = 2 };   // the last: its operands pass the caches by
 
@@ -139,6 +145,11 @@ template <typename T, typename R, int LAY, bool PRE, int DIR, bool EXTRA>
 __global__ __launch_bounds__(max_threads(LAY)) void k_block_norm(Args a) {
   constexpr int V = ssd::Vec16<T>::N, VPL = pieces_a_lane<T>(LAY);
   constexpr bool WIDE = LAY != NARROW, BWD = DIR != FORWARD, PASS = DIR == BACKWARD_PASS;
+  // Sixteen values a lane with all their sums leave no registers for the next row's, nor for the gates' values over the
+  // exchange of the sums, which are then formed again (4096 rows of 8192 bf16, gated, with a bias and a scale: 119 us, 265
+  // with spilled registers; without bias and scale 88 us, 104 formed again).
+  constexpr bool AHEAD = !(BWD && (LAY == WIDEST || (EXTRA && VPL * V == 16 && (!PRE || sizeof(T) == 4))));
+  constexpr bool AGAIN = !PRE && !AHEAD;
   __shared__ float places1[2][16][1], places3[2][16][3];
   extern __shared__ __attribute__((aligned(16))) char smem[];   // narrow rows, backward: [THR][V] sums
   const int tid = static_cast<int>(threadIdx.x);
@@ -191,7 +202,7 @@ __global__ __launch_bounds__(max_threads(LAY)) void k_block_norm(Args a) {
   const int64_t stride = static_cast<int64_t>(gridDim.y) * a.tpb;
   int64_t t = static_cast<int64_t>(blockIdx.y) * a.tpb;
   Row next;
-  request(next, t + tl);
+  if (AHEAD) request(next, t + tl);
   float w[VPL][V], s[VPL][V], b[VPL][V], gw[VPL][V], gb[VPL][V], gs[VPL][V];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -211,26 +222,48 @@ __global__ __launch_bounds__(max_threads(LAY)) void k_block_norm(Args a) {
     }
   }
   for (; t < a.tokens; t += stride) {
-    const Row q = next;
-    if (t + stride < a.tokens) request(next, t + stride + tl);
+    Row q;
+    if (AHEAD) {
+      q = next;
+      if (t + stride < a.tokens) request(next, t + stride + tl);
+    } else {
+      request(q, t + tl);
+    }
     const bool in = t + tl < a.tokens;
     const int64_t at = (t + tl) * a.D;
-    float v[VPL][V], act[VPL][V], slope[VPL][V];   // v: the normed values, then without their mean
+    float v[VPL][V];   // the normed values, then without their mean
+    constexpr int KI = AGAIN ? 1 : VPL, KE = AGAIN ? 1 : V;
+    float acts[KI][KE], slopes[KI][KE];
+    auto gate_of = [&](int i, int e, float& act, float& slope) {   // the gate's value, and its slope
+      act = 1.f;
+      slope = 0.f;
+      if (!PRE && a.z) {
+        const float z = q.z[i].get(e);
+        const float2 sg = sigmoids<T>(z);
+        act = a.sigmoid ? sg.x : z * sg.x;
+        if (BWD) slope = a.sigmoid ? sg.x * sg.y : sg.x * fmaf(z, sg.y, 1.f);
+      }
+    };
+    auto gate_at = [&](int i, int e, float& act, float& slope) {   // the same, kept or formed again
+      if constexpr (AGAIN) {
+        gate_of(i, e, act, slope);
+      } else {
+        act = acts[i][e];
+        slope = slopes[i][e];
+      }
+    };
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         float u = q.x[i].get(e);
-        act[i][e] = 1.f;
-        slope[i][e] = 0.f;
         if constexpr (PRE) {
           u = live[i] ? fmaf(s[i][e], u, a.res ? q.res[i].get(e) : 0.f) : 0.f;
-        } else if (a.z) {
-          const float z = q.z[i].get(e);
-          const float2 sg = sigmoids<T>(z);
-          act[i][e] = a.sigmoid ? sg.x : z * sg.x;
-          if (BWD) slope[i][e] = a.sigmoid ? sg.x * sg.y : sg.x * fmaf(z, sg.y, 1.f);
-          if (!a.norm_first) u *= act[i][e];
+        } else {
+          float act, slope;
+          gate_of(i, e, act, slope);
+          if constexpr (!AGAIN) acts[i][e] = act, slopes[i][e] = slope;
+          if (!a.norm_first) u *= act;
         }
         v[i][e] = u;
       }
@@ -267,7 +300,11 @@ __global__ __launch_bounds__(max_threads(LAY)) void k_block_norm(Args a) {
         for (int e = 0; e < V; ++e) {
           y[e] = fmaf(v[i][e] * r, w[i][e], b[i][e]);
           if constexpr (!PRE) {
-            if (a.norm_first) y[e] *= act[i][e];
+            if (a.norm_first) {
+              float act, slope;
+              gate_at(i, e, act, slope);
+              y[e] *= act;
+            }
             y[e] = a.res ? fmaf(s[i][e], y[e], q.res[i].get(e)) : s[i][e] * y[e];
           }
         }
@@ -283,7 +320,9 @@ __global__ __launch_bounds__(max_threads(LAY)) void k_block_norm(Args a) {
       for (int i = 0; i < VPL; ++i) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          float dn = PRE ? (a.dy ? q.dy[i].get(e) : 0.f) : q.dr[i].get(e) * s[i][e] * (a.norm_first ? act[i][e] : 1.f);
+          float act = 1.f, slope;
+          if (!PRE && a.norm_first) gate_at(i, e, act, slope);
+          const float dn = PRE ? (a.dy ? q.dy[i].get(e) : 0.f) : q.dr[i].get(e) * s[i][e] * act;
           d[i][e] = dn * w[i][e];
           if (!live[i]) d[i][e] = 0.f;
           k[0] += v[i][e] * v[i][e];
@@ -292,6 +331,10 @@ __global__ __launch_bounds__(max_threads(LAY)) void k_block_norm(Args a) {
         }
       }
       sum3(k);
+      if constexpr (AGAIN) {   // or the compiler would keep what was formed before
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) q.z[i].renew();
+      }
       const float r = 1.f / sqrtf(k[0] * a.inv_w + a.eps);
       const float dot = k[1] * a.inv_w * r * r, mean = a.layer ? k[2] * a.inv_w : 0.f;
 #pragma unroll
@@ -311,15 +354,17 @@ __global__ __launch_bounds__(max_threads(LAY)) void k_block_norm(Args a) {
             o1[e] = dr * s[i][e];
             o2[e] = dr;
           } else {
-            const float dout = q.dr[i].get(e), after = a.norm_first ? act[i][e] : 1.f;
+            float act, slope;
+            gate_at(i, e, act, slope);
+            const float dout = q.dr[i].get(e), after = a.norm_first ? act : 1.f;
             const float dn = dout * s[i][e] * after, n = fmaf(hat, w[i][e], b[i][e]);
             if (in) {
               gw[i][e] += dn * hat;
               if (EXTRA) gb[i][e] += dn;
               if (EXTRA) gs[i][e] += dout * n * after;
             }
-            o1[e] = a.norm_first ? du : du * act[i][e];
-            o2[e] = (a.norm_first ? dout * s[i][e] * n : du * q.x[i].get(e)) * slope[i][e];
+            o1[e] = a.norm_first ? du : du * act;
+            o2[e] = (a.norm_first ? dout * s[i][e] * n : du * q.x[i].get(e)) * slope;
           }
         }
         if (in && live[i]) {
@@ -419,9 +464,13 @@ Plan plan(const block_norm_shape& s, bool bwd) {
   const int64_t tokens = s.batch * s.seqlen;
   const int pieces = static_cast<int>(s.width / s.groups) / (s.io_dtype == SSD_IO_BF16 ? 8 : 4);
   if (pieces > 64) {
-    p.lay = pieces <= 512 ? WIDE1 : pieces <= 1024 ? WIDE2 : WIDEST;
-    const int vpl = s.io_dtype == SSD_IO_BF16 ? pieces_a_lane<bf16_t>(p.lay) : pieces_a_lane<float>(p.lay);
-    p.threads = ((pieces + vpl - 1) / vpl + 63) / 64 * 64;
+    auto threads = [&](int lay) {
+      const int vpl = s.io_dtype == SSD_IO_BF16 ? pieces_a_lane<bf16_t>(lay) : pieces_a_lane<float>(lay);
+      return ((pieces + vpl - 1) / vpl + 63) / 64 * 64;
+    };
+    p.lay = threads(WIDE1) <= 512 ? WIDE1 : threads(WIDE2) <= 512 ? WIDE2 : WIDEST;
+    if (p.lay == WIDEST && s.io_dtype == SSD_IO_F32 && threads(WIDE4) <= 512) p.lay = WIDE4;
+    p.threads = threads(p.lay);
     p.lpr = 64;
     p.gpb = p.tpb = 1;
     p.gy = s.groups;
@@ -458,6 +507,9 @@ template <typename T, typename R, bool PRE, int DIR> int by_width(const Plan& p,
     case NARROW: return go<T, R, NARROW, PRE, DIR>(p, a, st);
     case WIDE1: return go<T, R, WIDE1, PRE, DIR>(p, a, st);
     case WIDE2: return go<T, R, WIDE2, PRE, DIR>(p, a, st);
+    case WIDE4:
+      if constexpr (sizeof(T) == 4) return go<T, R, WIDE4, PRE, DIR>(p, a, st);
+      return SSD_ERR_UNSUPPORTED_SHAPE;   // plan() takes it for float32 only
     default: return go<T, R, WIDEST, PRE, DIR>(p, a, st);
   }
 }

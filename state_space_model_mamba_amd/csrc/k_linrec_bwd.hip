@@ -22,7 +22,10 @@ namespace linrec {
 
 using ssd::bf16_t;
 
-template <typename T, int GATE, int SCALE, bool ING> __global__ __launch_bounds__(Bwd::THR) void k_linrec_bwd(Problem p) {
+// Two blocks a CU, at most 128 registers: asked for where the compiler would take 132 (decay gates without input gate, 8192
+// rows of 4096 bf16 channels: 156 us with one block a CU, 115 with two); where it stays below by itself asking costs 2%.
+template <typename T, int GATE, int SCALE, bool ING>
+__global__ __launch_bounds__(Bwd::THR, GATE == LINREC_GATE_DECAY && SCALE != LINREC_INPUT_ONE && !ING ? 4 : 1) void k_linrec_bwd(Problem p) {
   constexpr int ROWS = Bwd::ROWS, WAVES = Bwd::WAVES, THR = Bwd::THR, V = Bwd::VALS<T>, CB = 64 * V;
   constexpr bool DECAY = GATE == LINREC_GATE_DECAY;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;

@@ -182,7 +182,9 @@ __device__ __forceinline__ float both(float f, float g) { return f == 0.f || g =
 //
 // What blocks hand each other is written and read past the caches (relaxed
 // atomics of the device's scope); a mark is written after its values have
-// arrived, and the values are read after the mark was seen.
+// arrived, and the values are read after the mark was seen.  Nothing else has
+// to be seen, so no fence writes an XCD's cache back for it (16384 x 8192
+// forward 839 us with one, 238 without).
 // ---------------------------------------------------------------------------
 enum { NOTHING = 0, PART = 1, WHOLE = 2 };
 

@@ -186,6 +186,25 @@ def test_slices_of_wider_rows_and_bits_on_repeat():
         assert all(torch.equal(p, q) for p, q in zip(first, out))
 
 
+def test_operands_larger_than_the_caches():
+    # 16384 x 2048: read past the caches, as a part of its rows is not; rows are alone but for the weight's gradient
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    x, z, dout = (torch.randn((1, 16384, 2048), generator=gen, device="cuda").bfloat16() for _ in range(3))
+    w = 1 + 0.1 * torch.randn((2048,), generator=gen, device="cuda")
+    whole = bn.gated_norm_bwd(x, z, w, None, 1.0, dout, groups=2)
+    add = bn.add_norm_bwd(x, z, w, 1.0, dout, z)
+    sums = [torch.zeros(2048, dtype=torch.float64, device="cuda") for _ in range(2)]
+    for r in range(0, 16384, 4096):
+        at = slice(r, r + 4096)
+        g = bn.gated_norm_bwd(x[:, at], z[:, at], w, None, 1.0, dout[:, at], groups=2)
+        a = bn.add_norm_bwd(x[:, at], z[:, at], w, 1.0, dout[:, at], z[:, at])
+        assert torch.equal(g["dx"], whole["dx"][:, at]) and torch.equal(g["dz"], whole["dz"][:, at]) and torch.equal(a["dx"], add["dx"][:, at])
+        sums[0] += g["dweight"]
+        sums[1] += a["dweight"]
+    for s, t in zip(sums, (whole["dweight"], add["dweight"])):   # at most 64 rows of a block are added in float32, then rounded
+        assert float((t - s).norm() / s.norm()) < 2 * 64 * 2.0 ** -24 * (16384 ** 0.5)
+
+
 def test_rows_past_32_bits():
     # rows 2^23 elements apart: the last begins past 2^31 elements
     wide = torch.empty((300, 1 << 23), dtype=torch.bfloat16, device="cuda")

@@ -218,6 +218,23 @@ def test_operands_broadcast_over_batch_or_rows():
     assert torch.equal(x["y"], y["y"]) and all(torch.equal(p[k], q[k]) for k in ("dx", "dg", "d_in_gate"))
 
 
+def test_operands_larger_than_the_caches():
+    # 16384 x 4096 with all gates: read past the caches, as its slices of 1024 channels are not; channels are alone
+    gen = torch.Generator(device="cuda").manual_seed(43)
+    d = {k: torch.randn((1, 16384, 4096), generator=gen, device="cuda").bfloat16() for k in ("x", "g", "in_gate", "dy")}
+    d.update(decay=-8 * torch.rand((4096,), generator=gen, device="cuda"), seq_idx=None, h0=None, dfinal=None, nseqs=1)
+    kw = dict(gate="decay", input_scale="unit")
+    r = forward(d, want_chunk_states=True, **kw)
+    g = backward(d, chunk_states=r["chunk_states"], **kw)
+    for c in range(0, 4096, 1024):
+        at = slice(c, c + 1024)
+        part = {k: v[..., at].contiguous() if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+        q = forward(part, want_chunk_states=True, **kw)
+        h = backward(part, chunk_states=q["chunk_states"], **kw)
+        assert all(torch.equal(r[k][..., at], q[k]) for k in ("y", "final_states", "chunk_states")), c
+        assert all(torch.equal(g[k][..., at], h[k]) for k in ("dx", "dg", "d_in_gate", "ddecay")), c
+
+
 def test_rows_past_32_bits():
     wide = torch.empty((300, 1 << 23), dtype=torch.bfloat16, device="cuda")   # rows 2^23 elements apart: the last past 2^31
     d = cuda(make(1, 300, 64, "bf16", seed=12))

@@ -32,6 +32,7 @@ __global__ __launch_bounds__(Bwd::THR, GATE == LINREC_GATE_DECAY && SCALE != LIN
   __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], fc[WAVES][CB], enter[CB];
   __shared__ int cuts;
   const int lane = ssd::lane_id(), wave = ssd::wave_id_s();
+  __builtin_amdgcn_s_setprio(2);   // until the requests are out, ahead of the other block's arithmetic (486 -> 479 us)
   if (threadIdx.x == 0) cuts = 0;
   const int cb = channel_block(p), place = ticket(p, cb);
   const int chunk = p.chunks - 1 - place;   // from the end
@@ -59,6 +60,7 @@ __global__ __launch_bounds__(Bwd::THR, GATE == LINREC_GATE_DECAY && SCALE != LIN
   };
   if (p.pass) request(std::true_type{});
   else request(std::false_type{});
+  __builtin_amdgcn_s_setprio(0);
   Raw<float, V> entering;   // the state that enters the chunk
   if (chunk > 0) entering.load(p.states + static_cast<int64_t>(chunk - 1) * p.C + c);
   else entering.w = 0;

@@ -10,9 +10,10 @@
 // same recurrence as the h, read from the end; the h are formed again from the
 // states between the spans, in float32, so neither they nor y are read.
 //
-// Bound by HBM and, beside it, by the gates' arithmetic: of 485 us at 16384
-// rows of 8192 bf16 channels with all gates (1.88 GB, 3.9 TB/s) the vector units
-// are busy for 295; 453 with the chain cut out, 406 without the gates as well.
+// Bound by HBM and, beside it, by the gates' arithmetic: 479 us at 16384
+// rows of 8192 bf16 channels with all gates (1.88 GB, 3.9 TB/s).  Of 485, before
+// the requests had priority, the vector units were busy for 295; with the chain
+// cut out it took 453, without the gates as well 406.
 // With all seven values of an element kept in registers over the chain, one
 // block a CU, it took 900; with the next chunk's operands requested ahead by
 // blocks that stay, 735.

@@ -40,9 +40,13 @@
  *
  * Values.  States, gates and every sum are float32; y and the gradients are
  * rounded to their dtype once (the state that goes on is not).  Decays are
- * <= 0 and so are log decays, -inf included (the state is dropped).  The
+ * <= 0 and so are log decays, -inf included (a finite state is dropped).  The
  * gradient of sqrt(1 - a^2) is taken as zero where a is one.  A NaN or an
- * infinity stays in its sequence and channel.
+ * infinity stays in its sequence and channel, and lasts there: products are
+ * taken as they stand, a decay of zero times an infinity or a NaN is a NaN, so
+ * whatever the sizes, once it is in the state the rest of the sequence (of the
+ * gradients: the rows before) is not finite.  Which of the two it is then may
+ * depend on how the rows lie in chunks; only a sequence's start drops it.
  *
  * Ownership and calling convention: as for ssd_bwd (device pointers of the
  * caller, 16-byte aligned; outputs fully overwritten; no allocation; work

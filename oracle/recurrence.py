@@ -115,8 +115,9 @@ def backward(x, g, in_gate, decay, dy, h0=None, seq_idx=None, d_final=None, gate
             ee[t] = ee[t] + 2 * ULP * (np.abs(dy[t]) + np.abs(e[t]))
             c, ce = a[t] * e[t], a[t] * ee[t] + K[t] * np.abs(a[t] * e[t])
         d0[s], d0e[s] = c, ce
-    inner = a * prev + dm * u
-    inner_err = a * prev_err + K * (np.abs(a * prev) + 2 * np.abs(dm * u))
+    add = np.zeros_like(x) if input_scale == "one" else dm * u   # a factor of one has no share, whatever x is
+    inner = a * prev + add
+    inner_err = a * prev_err + K * (np.abs(a * prev) + 2 * np.abs(add))
     dl, dle = e * inner, ee * np.abs(inner) + np.abs(e) * inner_err
     du, due = e * m, ee * np.abs(m) + K * np.abs(e * m) + M * np.abs(e)
     lost = M * np.abs(e * u)

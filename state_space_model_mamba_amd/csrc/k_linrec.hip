@@ -3,8 +3,8 @@
 //
 // All batch rows lie behind each other as one run of rows, cut into chunks.  A
 // chunk turns the state h that enters it into A h + H, A the product of its
-// decays and H what a zero state would have become; a sequence start inside
-// makes A zero.  So do a wave's rows within a chunk: their (A, H) meet in LDS,
+// decays and H what a zero state would have become, and one with a sequence
+// start inside into H.  So do a wave's rows within a chunk: their (A, H) meet in LDS,
 // the chunks' in memory (linrec_problem.h).  A lane keeps its rows' a and b
 // meanwhile, so every input is read once.
 //
@@ -24,7 +24,7 @@ __global__ __launch_bounds__(L::THR, GATE == LINREC_GATE_LOG && !ING ? 4 : 1) vo
   constexpr int ROWS = L::ROWS, WAVES = L::WAVES, V = L::template VALS<T>, CB = 64 * V;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
   __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], enter[CB];
-  __shared__ int cuts;
+  __shared__ uint32_t cuts;   // bit w: a sequence starts in the rows of wave w
   const int lane = ssd::lane_id(), wave = ssd::wave_id_s();
   if (threadIdx.x == 0) cuts = 0;
   const int cb = channel_block(p), chunk = ticket(p, cb);
@@ -53,10 +53,10 @@ __global__ __launch_bounds__(L::THR, GATE == LINREC_GATE_LOG && !ING ? 4 : 1) vo
   const bool cut = starts & ((1u << ROWS) - 1);
   float a[ROWS][V], b[ROWS][V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const Decay<T, GATE> d(GATE == LINREC_GATE_DECAY ? dk.get(v) : 0.f);
+  for (int j = 0; j < ROWS; ++j) {   // rows outside: a row's operands make room for its a and b at once
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
+    for (int v = 0; v < V; ++v) {
+      const Decay<T, GATE> d(GATE == LINREC_GATE_DECAY ? dk.get(v) : 0.f);
       const Factor f = factor_of<T, GATE>(g[j].get(v), d);
       float u = x[j].get(v);
       if (ING) u *= Fn<T>::sigmoid(in[j].get(v));
@@ -88,14 +88,14 @@ __global__ __launch_bounds__(L::THR, GATE == LINREC_GATE_LOG && !ING ? 4 : 1) vo
   float A[V], H[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f;
-  // a start drops the state by selection, so that nothing of it (a NaN either) passes
+  // a start drops the state by selection, so that nothing of it (a NaN either) passes; A is then not read
   auto gather = [&](auto with_starts) {
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
       const bool start = with_starts.value && ((starts >> j) & 1u);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        A[v] = start ? 0.f : A[v] * a[j][v];
+        A[v] *= a[j][v];
         H[v] = start ? b[j][v] : fmaf(a[j][v], H[v], b[j][v]);
       }
     }
@@ -108,8 +108,9 @@ __global__ __launch_bounds__(L::THR, GATE == LINREC_GATE_LOG && !ING ? 4 : 1) vo
     fh[wave][lane * V + v] = H[v];
   }
   if (p.chunks == 1) __syncthreads();   // cuts is cleared
-  if (lane == 0 && cut) cuts = 1;
+  if (lane == 0 && cut) atomicOr(&cuts, 1u << wave);
   __syncthreads();
+  const uint32_t cut_waves = __builtin_amdgcn_readfirstlane(cuts);
   float h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) h[v] = 0.f;
@@ -120,12 +121,12 @@ __global__ __launch_bounds__(L::THR, GATE == LINREC_GATE_LOG && !ING ? 4 : 1) vo
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float f = fa[w][lane * V + v];
-          A[v] = both(A[v], f);
-          H[v] = onto(f, fh[w][lane * V + v], H[v]);
+          A[v] *= f;
+          H[v] = onto((cut_waves >> w) & 1u, f, fh[w][lane * V + v], H[v]);
         }
       }
       const int last = p.spans - 1;
-      join<V>(p, p.states, chunk, cb, c, cuts != 0, A, H, h, [last](int k) {
+      join<V>(p, p.states, chunk, cb, c, cut_waves != 0, A, H, h, [last](int k) {
         const int s = (k + 1) * (L::CHUNK / SPAN) - 1;
         return s < last ? s : last;
       });
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(L::THR, GATE == LINREC_GATE_LOG && !ING ? 4 : 1) vo
   }
   for (int w = 0; w < wave; ++w) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = onto(fa[w][lane * V + v], fh[w][lane * V + v], h[v]);
+    for (int v = 0; v < V; ++v) h[v] = onto((cut_waves >> w) & 1u, fa[w][lane * V + v], fh[w][lane * V + v], h[v]);
   }
   if (p.keep && wave * ROWS % SPAN == 0 && wave > 0 && rows > 0) {   // a span of the chunk ends before the wave's rows
     Raw<float, V> f;
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(L::THR, GATE == LINREC_GATE_LOG && !ING ? 4 : 1) vo
     Raw<float, V> f;
     float e[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = onto(A[v], H[v], h[v]);
+    for (int v = 0; v < V; ++v) e[v] = onto(cut, A[v], H[v], h[v]);
     f.set(e);
     f.store(p.states + static_cast<int64_t>(p.spans - 1) * p.C + c);
   }

@@ -31,7 +31,7 @@ __global__ __launch_bounds__(Bwd::THR, GATE == LINREC_GATE_DECAY && SCALE != LIN
   constexpr bool DECAY = GATE == LINREC_GATE_DECAY;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
   __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], fc[WAVES][CB], enter[CB];
-  __shared__ int cuts;
+  __shared__ uint32_t cuts;   // bit w: a sequence starts in the rows of wave w
   const int lane = ssd::lane_id(), wave = ssd::wave_id_s();
   __builtin_amdgcn_s_setprio(2);   // until the requests are out, ahead of the other block's arithmetic (486 -> 479 us)
   if (threadIdx.x == 0) cuts = 0;
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(Bwd::THR, GATE == LINREC_GATE_DECAY && SCALE != LIN
     }
   };
   // The wave's factor and what a zero state becomes over it, and what it hands back from nothing.  A start drops the
-  // state by selection, so that nothing of it (a NaN either) passes, in either direction.
+  // state by selection, so that nothing of it (a NaN either) passes, in either direction; A is then not read.
   float A[V], H[V], cr[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = cr[v] = 0.f;
@@ -150,13 +150,14 @@ __global__ __launch_bounds__(Bwd::THR, GATE == LINREC_GATE_DECAY && SCALE != LIN
   else gather(std::true_type{});
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    fa[wave][lane * V + v] = cut ? 0.f : A[v];
+    fa[wave][lane * V + v] = A[v];
     fh[wave][lane * V + v] = H[v];
     fc[wave][lane * V + v] = cr[v];
   }
   if (p.chunks == 1) __syncthreads();   // cuts is cleared
-  if (lane == 0 && cut) cuts = 1;
+  if (lane == 0 && cut) atomicOr(&cuts, 1u << wave);
   __syncthreads();
+  const uint32_t cut_waves = __builtin_amdgcn_readfirstlane(cuts);
 #pragma unroll
   for (int v = 0; v < V; ++v) H[v] = entering.get(v), cr[v] = 0.f;
   if (p.chunks > 1) {
@@ -168,12 +169,12 @@ __global__ __launch_bounds__(Bwd::THR, GATE == LINREC_GATE_DECAY && SCALE != LIN
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float f = fa[w][lane * V + v];
-          B[v] = onto(f, fc[w][lane * V + v], B[v]);
-          A[v] = both(A[v], f);
+          B[v] = onto((cut_waves >> w) & 1u, f, fc[w][lane * V + v], B[v]);
+          A[v] *= f;
         }
       }
       const int last = p.chunks - 1;
-      join<V>(p, p.carry, place, cb, c, cuts != 0, A, B, cr, [last](int k) { return last - k; });
+      join<V>(p, p.carry, place, cb, c, cut_waves != 0, A, B, cr, [last](int k) { return last - k; });
 #pragma unroll
       for (int v = 0; v < V; ++v) enter[lane * V + v] = cr[v];
     }
@@ -183,11 +184,11 @@ __global__ __launch_bounds__(Bwd::THR, GATE == LINREC_GATE_DECAY && SCALE != LIN
   }
   for (int w = 0; w < wave; ++w) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) H[v] = onto(fa[w][lane * V + v], fh[w][lane * V + v], H[v]);
+    for (int v = 0; v < V; ++v) H[v] = onto((cut_waves >> w) & 1u, fa[w][lane * V + v], fh[w][lane * V + v], H[v]);
   }
   for (int w = WAVES - 1; w > wave; --w) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) cr[v] = onto(fa[w][lane * V + v], fc[w][lane * V + v], cr[v]);
+    for (int v = 0; v < V; ++v) cr[v] = onto((cut_waves >> w) & 1u, fa[w][lane * V + v], fc[w][lane * V + v], cr[v]);
   }
   float sum[V];
 #pragma unroll

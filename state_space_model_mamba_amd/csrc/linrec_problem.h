@@ -166,11 +166,9 @@ template <typename T, int GATE, int SCALE> __device__ __forceinline__ float scal
   else if constexpr (SCALE == LINREC_INPUT_COMPLEMENT) return GATE == LINREC_GATE_SIGMOID ? f.rest : F::template one_minus<1>(f.la, 1.f - f.a);
   else return F::sqrt(GATE == LINREC_GATE_SIGMOID ? fmaf(f.rest, f.a, f.rest) : F::template one_minus<2>(f.la, fmaf(-f.a, f.a, 1.f)));
 }
-// a chunk or part of it on a state: what decayed to nothing is dropped, so nothing of it (a NaN either) passes on
-__device__ __forceinline__ float onto(float factor, float add, float state) { return factor == 0.f ? add : fmaf(factor, state, add); }
-
-// the factor of two parts; one that drops the state drops it whatever the other holds
-__device__ __forceinline__ float both(float f, float g) { return f == 0.f || g == 0.f ? 0.f : f * g; }
+// Rows, a wave's or a chunk's, on a state.  Whether a sequence starts in them is known apart (`cut`), the same in all lanes:
+// a product of decays that came to zero is a factor like others, on which a NaN or an infinity stays one, as it does row by row.
+__device__ __forceinline__ float onto(bool cut, float factor, float add, float state) { return cut ? add : fmaf(factor, state, add); }
 
 // ---------------------------------------------------------------------------
 // The chunks' chain.  A block takes its chunk by a ticket, so the chunks before
@@ -210,7 +208,7 @@ __device__ __forceinline__ int ticket(const Problem& p, int cb) {
 
 // One wave, for the lane's V channels from c on: the state before the chunk at `place` of the chain, and A, H onto it left
 // for the chunks behind.  row_of(place): where the chunk there has its row in agg and in `after`, the states behind the
-// chunks; cut: a sequence starts in it.
+// chunks; cut: a sequence starts in it (then H is the state behind it, and A is not read).
 template <int V, typename RowOf>
 __device__ __forceinline__ void join(const Problem& p, float* after, int place, int cb, int c, bool cut, const float (&A)[V],
                                      const float (&H)[V], float (&before)[V], RowOf row_of) {
@@ -270,7 +268,7 @@ __device__ __forceinline__ void join(const Problem& p, float* after, int place, 
       for (int i = 0; i < AHEAD; ++i) {
         if (q + i < place && q + i >= 0) {
 #pragma unroll
-          for (int v = 0; v < V; ++v) before[v] = onto(f[i][v].x, f[i][v].y, before[v]);
+          for (int v = 0; v < V; ++v) before[v] = fmaf(f[i][v].x, before[v], f[i][v].y);   // no chunk between has a start: those leave a state
         }
       }
     }
@@ -278,7 +276,7 @@ __device__ __forceinline__ void join(const Problem& p, float* after, int place, 
   if (!cut) {
     float h[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = onto(A[v], H[v], before[v]);
+    for (int v = 0; v < V; ++v) h[v] = fmaf(A[v], before[v], H[v]);
     leave(h);
   }
 }

@@ -262,8 +262,7 @@ namespace {
 template <typename L, typename T, int GATE, int SCALE, bool ING> int run(Problem p, hipStream_t st) {
   p.cblocks = (p.C + 64 * L::template VALS<T> - 1) / (64 * L::template VALS<T>);
   p.chunks = (p.R + L::CHUNK - 1) / L::CHUNK;
-  hipLaunchKernelGGL((k_linrec<L, T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(L::THR), 0, st, p);
-  return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+  return in_launches(p, L::THR, [&](dim3 grid) { hipLaunchKernelGGL((k_linrec<L, T, GATE, SCALE, ING>), grid, dim3(L::THR), 0, st, p); });
 }
 template <typename T, int GATE, int SCALE, bool ING> int go(const Problem& p, hipStream_t st) {
   return p.R > Fwd::CHUNK && !chained_fwd(p) ? run<Short, T, GATE, SCALE, ING>(p, st) : run<Fwd, T, GATE, SCALE, ING>(p, st);

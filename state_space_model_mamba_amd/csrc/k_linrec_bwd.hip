@@ -311,7 +311,8 @@ namespace {
 template <typename T, int GATE, int SCALE, bool ING> int go(Problem p, hipStream_t st) {
   p.cblocks = (p.C + 64 * Bwd::VALS<T> - 1) / (64 * Bwd::VALS<T>);
   p.chunks = p.spans;
-  hipLaunchKernelGGL((k_linrec_bwd<T, GATE, SCALE, ING>), dim3(static_cast<unsigned>(p.chunks * p.cblocks)), dim3(Bwd::THR), 0, st, p);
+  const int rc = in_launches(p, Bwd::THR, [&](dim3 grid) { hipLaunchKernelGGL((k_linrec_bwd<T, GATE, SCALE, ING>), grid, dim3(Bwd::THR), 0, st, p); });
+  if (rc != SSD_OK) return rc;
   if (GATE == LINREC_GATE_DECAY && p.ddecay)
     hipLaunchKernelGGL(k_linrec_reduce, dim3(static_cast<unsigned>((p.C + RED_COLS - 1) / RED_COLS)), dim3(RED_COLS * RED_ROWS), 0, st, p);
   return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;

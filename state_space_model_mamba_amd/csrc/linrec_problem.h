@@ -57,6 +57,17 @@ struct Problem {
 int launch_setup(const Problem& p, bool chain, bool number, hipStream_t st);
 inline bool chained_fwd(const Problem& p) { return p.R > Short::CHUNK; }
 inline bool chained_bwd(const Problem& p) { return p.R > Bwd::CHUNK; }
+// The chunks of one launch: a grid holds less than 2^32 threads (more are cut off without an error).  Those of the next go
+// on with the tickets, in the same places of the chain.
+inline int64_t chunks_a_launch(int64_t cblocks, int threads) { return ((int64_t{1} << 32) - 1) / threads / cblocks; }
+template <typename Launch> int in_launches(const Problem& p, int threads, Launch launch) {
+  const int64_t most = chunks_a_launch(p.cblocks, threads);
+  for (int64_t left = p.chunks; left > 0; left -= most) {
+    launch(dim3(static_cast<unsigned>((left < most ? left : most) * p.cblocks)));
+    if (hipGetLastError() != hipSuccess) return SSD_ERR_HIP;
+  }
+  return SSD_OK;
+}
 int launch_fwd(const Problem& p, const linrec_shape& s, hipStream_t st);   // (p.y, p.final NULL: the states only)
 int launch_bwd(const Problem& p, const linrec_shape& s, hipStream_t st);
 

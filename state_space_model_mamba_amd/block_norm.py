@@ -94,7 +94,7 @@ def row_strides(t, name):
     if L == 1:
         sl = w
     if b == 1:
-        sb = L * sl
+        sb = L * sl or w   # one row for all: any step that is not 0 (0, 0 says contiguous)
     if sb == 0 and sl == 0:
         raise ValueError(f"{name} may be broadcast over batch or rows, not over both")
     return sb, sl

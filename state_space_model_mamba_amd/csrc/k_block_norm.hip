@@ -541,9 +541,17 @@ template <bool PRE, bool BWD> int launch(const block_norm_shape& s, Args& a, hip
   a.alpha = s.alpha;
   a.inv_w = 1.f / static_cast<float>(a.W);
   if constexpr (!BWD) return by_type<PRE, FORWARD>(s, p, a, st);
-  // The backward's operands pass the caches by where they are more than the 256 MB of the last one: 16384 x 8192 bf16 with
-  // a gate 271 us, 286 by the caches; 1999 x 4096 float32 (164 MB, what the forward left is still there) 42 us, 33.
-  const int64_t bytes = static_cast<int64_t>(a.tokens) * a.D * (s.io_dtype == SSD_IO_BF16 ? 2 : 4) * 5;
+  // The backward's operands pass the caches by where it moves more than the 256 MB of the last one: what is given, and for
+  // add_norm the residual's rows also where there is none, as the forward's r then lies there.  Microseconds past the caches
+  // and by them, in brackets with the forward before: gated 16384 x 8192 bf16 271 and 286; 7000 x 4096 (273 MB) 59 and 56 (92,
+  // 91), 8500 69 and 74 (109, 108); no z, 9000 x 4096 (210 MB) 52 and 50 (88, 86), float32 3500 x 4096 (164 MB) 49 and 42 (69,
+  // 64).  add_norm bf16, float32 residual: 4200 x 4096 (295 MB) 63 and 59 (91, 91), 5500 (386 MB) 79 and 86 (115, 134); no
+  // residual, 6300 x 4096 (246 MB with r) 44 and 40 (69, 69), 9000 60 and 56 (91, 101).
+  const int64_t io = s.io_dtype == SSD_IO_BF16 ? 2 : 4, res = s.residual_dtype == SSD_IO_BF16 ? 2 : 4;
+  int64_t bytes = PRE ? res : 0;   // of a value
+  for (const void* t : {a.x, a.z, a.dy, static_cast<const void*>(a.dx), static_cast<const void*>(a.dz)}) bytes += t ? io : 0;
+  for (const void* t : {a.dr, static_cast<const void*>(a.dres)}) bytes += t ? res : 0;
+  bytes *= static_cast<int64_t>(a.tokens) * a.D;
   return bytes > (int64_t{256} << 20) ? by_type<PRE, BACKWARD_PASS>(s, p, a, st) : by_type<PRE, BACKWARD>(s, p, a, st);
 }
 

@@ -18,9 +18,10 @@ namespace linrec {
 
 using ssd::bf16_t;
 
-// (two blocks a CU, at most 128 registers: asked for where the compiler would take 134; 74 us, 62 with two, at 8192 x 4096)
+// Two blocks a CU, at most 128 registers: asked for where the compiler would take 133 or 134 (log decays with a factor other
+// than one and no input gate, bf16: 74 us with one block a CU, 62 with two and a register spilled, at 8192 x 4096).
 template <typename L, typename T, int GATE, int SCALE, bool ING>
-__global__ __launch_bounds__(L::THR, GATE == LINREC_GATE_LOG && !ING ? 4 : 1) void k_linrec(Problem p) {
+__global__ __launch_bounds__(L::THR, GATE == LINREC_GATE_LOG && SCALE != LINREC_INPUT_ONE && !ING ? 4 : 1) void k_linrec(Problem p) {
   constexpr int ROWS = L::ROWS, WAVES = L::WAVES, V = L::template VALS<T>, CB = 64 * V;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;
   __shared__ __attribute__((aligned(16))) float fa[WAVES][CB], fh[WAVES][CB], enter[CB];

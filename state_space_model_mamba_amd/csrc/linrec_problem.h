@@ -39,7 +39,7 @@ struct Problem {
   const void *x, *g, *i, *dy;
   const float *decay, *h0, *dfinal;
   const int32_t* seq_idx;
-  int pass;                // the operands are more than the last cache holds
+  int pass;                // the forward's operands are more than the last cache holds
   int keep;                // all spans' states are wanted, not only the chain's
   // outputs
   void *y, *dx, *dg, *di;
@@ -128,7 +128,9 @@ template <typename T> struct Fn {
     return __float_as_int(w) < 0 ? float2{o, -w} : float2{w, o};
   }
   // 1 - exp(S y), y <= 0, from its direct form: with S y above -1/2 as -S y times the polynomial of degree 5 that is
-  // nearest to (exp(t) - 1) / t there (off by 7e-9 of it, found by exchange), below it the difference loses at most one bit
+  // nearest to (exp(t) - 1) / t there (off by 7e-9 of it, found by exchange).  Below it the direct form takes over what exp(y)
+  // is off by, times S e / (1 - e) with e = exp(S y), which is most at -1/2: 1.5 for 1 - a, 3.1 for 1 - a^2, halved again by
+  // the root that is taken of it.
   template <int S> static __device__ __forceinline__ float one_minus(float y, float direct) {
     constexpr float C[6] = {1.f, 4.999998211860657e-1f, 1.6666224598884583e-1f, 4.1629090905189514e-2f, 8.187386207282543e-3f, 1.1216348502784967e-3f};
     float q = C[5] * (S == 2 ? 64.f : 1.f);   // S^6 and down: powers of two change no bits

@@ -10,10 +10,14 @@
 // same recurrence as the h, read from the end; the h are formed again from the
 // states between the spans, in float32, so neither they nor y are read.
 //
-// Bound by HBM and, beside it, by the gates' arithmetic: 479 us at 16384
-// rows of 8192 bf16 channels with all gates (1.88 GB, 3.9 TB/s).  Of 485, before
-// the requests had priority, the vector units were busy for 295; with the chain
-// cut out it took 453, without the gates as well 406.
+// Bound by HBM and, beside it, by the gates' arithmetic: 476 us at 16384
+// rows of 8192 bf16 channels with all gates (1.88 GB, 3.9 TB/s) by itself, 513 to
+// 543 in a training pass (least and median of the kernel trace); the vector units
+// are busy for 288 of it.  Of 485, before the requests had priority, it took 453
+// with the chain cut out, 406 without the gates as well.  Without input gate it
+// stands further from the copy's rate: 386 us (1.34 GB, 3.5 TB/s), and 108 to 111 at
+// 8192 rows of 4096 (3.1 TB/s); what bounds that was not found out.  8192 rows of 4096
+// float32 channels: 215 us with all gates (4.4 TB/s), 144 with log decays (4.7).
 // With all seven values of an element kept in registers over the chain, one
 // block a CU, it took 900; with the next chunk's operands requested ahead by
 // blocks that stay, 735.
@@ -23,10 +27,10 @@ namespace linrec {
 
 using ssd::bf16_t;
 
-// Two blocks a CU, at most 128 registers: asked for where the compiler would take 132 (decay gates without input gate, 8192
-// rows of 4096 bf16 channels: 156 us with one block a CU, 115 with two); where it stays below by itself asking costs 2%.
+// Two blocks a CU need at most 128 registers: the compiler takes up to 126 (decay gates without input gate; 156 us with one
+// block a CU, 108 to 111 with two, at 8192 rows of 4096 bf16 channels).
 template <typename T, int GATE, int SCALE, bool ING>
-__global__ __launch_bounds__(Bwd::THR, GATE == LINREC_GATE_DECAY && SCALE != LINREC_INPUT_ONE && !ING ? 4 : 1) void k_linrec_bwd(Problem p) {
+__global__ __launch_bounds__(Bwd::THR) void k_linrec_bwd(Problem p) {
   constexpr int ROWS = Bwd::ROWS, WAVES = Bwd::WAVES, THR = Bwd::THR, V = Bwd::VALS<T>, CB = 64 * V;
   constexpr bool DECAY = GATE == LINREC_GATE_DECAY;
   using G = std::conditional_t<GATE == LINREC_GATE_LOG, float, T>;

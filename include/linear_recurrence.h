@@ -107,6 +107,7 @@ int linrec_fwd(const linrec_shape* shape, const void* x, const void* g, const vo
  * inputs.  chunk_states: as linrec_fwd wrote them for the same inputs, or
  * NULL (they are formed again).  d_final_states (zeros), d_initial_states and
  * ddecay (not computed) may be NULL; d_in_gate goes with in_gate.
+ * d_initial_states may not be d_final_states, nor any other gradient an input.
  */
 int linrec_bwd(const linrec_shape* shape, const void* x, const void* g, const void* in_gate, const float* decay,
                const float* initial_states, const int32_t* seq_idx, const float* chunk_states, const void* dy,

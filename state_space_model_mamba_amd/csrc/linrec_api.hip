@@ -151,6 +151,7 @@ int linrec_bwd(const linrec_shape* shape, const void* x, const void* g, const vo
   for (const void* o : {static_cast<const void*>(dx), static_cast<const void*>(dg), static_cast<const void*>(d_in_gate)})
     for (const void* i : {x, g, in_gate, dy})
       if (o && o == i) return SSD_ERR_INVALID_ARG;
+  if (d_initial_states && d_initial_states == d_final_states) return SSD_ERR_INVALID_ARG;   // written while others still read
   p.dy = dy; p.dfinal = d_final_states;
   p.dx = dx; p.dg = dg; p.di = d_in_gate; p.ddecay = ddecay; p.dh0 = d_initial_states;
   hipStream_t st = static_cast<hipStream_t>(stream);

@@ -12,11 +12,18 @@
 // registers and the gradients over rows are sums in registers; the next row's
 // pieces are requested before the present row's sums are exchanged.
 //
-// 16384 rows of 8192 bf16 in 8 gated groups: forward 142 us (5.7 TB/s), backward
-// 243 to 270 (5.0 to 5.5 TB/s).  16384 rows of 4096 bf16 with a float32 residual
-// and a scale a channel: 147 (5.5) and 199 to 210 us (5.8 to 6.1).  1999 rows of
-// 64 float32 heads of 64, gated, with a residual: 25 and 29 us.  The slots' sum
-// takes 4 to 5 us.  One row of 4096: 3 us.
+// 16384 rows of 8192 bf16 in 8 gated groups: forward 144 us (5.6 TB/s), backward
+// 268 (5.0 TB/s), each by itself; in turn in a training pass, by the kernel
+// trace, 144 to 160 and 240 to 290 us (least and median).  16384 rows of 4096
+// bf16 with a float32 residual and a scale a channel: 147 to 151 and 200 to 206
+// us there.  1999 rows of 64 float32 heads of 64, gated, with a residual: 25 and
+// 29 us.  The slots' sum takes 4 to 5 us.  One row of 4096: 3 us.
+//
+// Rows past 8192 (1024 threads, 128 registers) keep part of their values in
+// scratch memory: nearly every backward, and the forwards but for add_norm of
+// bf16 and, without bias and scale, gated_norm of bf16 and add_norm of float32.
+// 4096 rows of 16384, gated, without them: bf16 113 and 224 us (3.6 and 3.0
+// TB/s), float32 252 and 490 (3.2 and 2.7 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "block_norm.h"

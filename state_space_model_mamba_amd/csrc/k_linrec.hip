@@ -9,9 +9,12 @@
 // meanwhile, so every input is read once.
 //
 // Bound by HBM, and by how well two blocks a CU cover each other's phases.
-// 16384 rows of 8192 bf16 channels with all gates (1.07 GB): 239 to 260 us,
-// 4.1 to 4.5 TB/s; 230 with the chain cut out, 220 without the gates'
-// arithmetic as well, which takes 143 us of the vector units' time.
+// 16384 rows of 8192 bf16 channels with all gates (1.07 GB): 240 to 246 us by
+// itself (4.4 TB/s), 238 to 260 in a training pass (least and median of the
+// kernel trace); 230 with the chain cut out, 220 without the gates' arithmetic
+// as well, which takes 137 us of the vector units' time.  8192 rows of 4096
+// float32 channels: 117 us (4.6 TB/s); 89 with decay gates without input gate
+// (4.5), 79 with log decays (5.1).
 #include "linrec_problem.h"
 
 namespace linrec {

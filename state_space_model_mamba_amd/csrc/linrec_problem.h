@@ -15,9 +15,10 @@ constexpr int SPAN = 64;
 
 // A chunk, a block's rows: WAVES waves of ROWS rows each, a lane with BYTES of x of every row.  The more rows a chunk has,
 // the fewer links the chain; the more values a lane keeps over the chain, the fewer blocks share a CU and its loads.
-// Microseconds at 16384 rows of 8192 bf16 channels with all gates, forward (and of 4096 channels, packed): 16 x 8 x 4 bytes
-// 247 (150), 16 x 4 x 4 256 (161), 8 x 8 x 8 267 (168), 16 x 16 x 4 285 (166), 8 x 16 x 4 343 (192).  Backward: 8 x 8 x 4
-// 485, 16 x 4 x 4 524, 8 x 4 x 4 521, 8 x 4 x 8 575, 4 x 16 x 4 748.
+// Microseconds when they were chosen, at 16384 rows of 8192 bf16 channels with all gates, forward (and of 4096 channels,
+// packed): 16 x 8 x 4 bytes 247 (150), 16 x 4 x 4 256 (161), 8 x 8 x 8 267 (168), 16 x 16 x 4 285 (166), 8 x 16 x 4 343
+// (192).  Backward: 8 x 8 x 4 485, 16 x 4 x 4 524, 8 x 4 x 4 521, 8 x 4 x 8 575, 4 x 16 x 4 748.  For float32, one channel a
+// lane, others were not tried: at 8192 rows of 4096 it stands 1.1 times the copy's time, 1.2 backward.
 template <int R, int W, int B> struct Lay {
   static constexpr int ROWS = R, WAVES = W, BYTES = B, CHUNK = R * W, THR = 64 * W;
   template <typename T> static constexpr int VALS = B / static_cast<int>(sizeof(T));
@@ -184,8 +185,11 @@ template <typename T, int GATE, int SCALE> __device__ __forceinline__ float scal
 __device__ __forceinline__ float onto(bool cut, float factor, float add, float state) { return cut ? add : fmaf(factor, state, add); }
 
 // ---------------------------------------------------------------------------
-// The chunks' chain.  A block takes its chunk by a ticket, so the chunks before
-// it in the chain have begun and wait for none after it: every wait ends.  It
+// The chunks' chain: a single-pass scan with look-back over the chunks before
+// (Merrill and Garland, "Single-pass Parallel Prefix Scan with Decoupled
+// Look-back", 2016), on states instead of sums, in an order of its own.
+// A block takes its chunk by a ticket, so the chunks before it in the chain have
+// begun and wait for none after it: every wait ends.  It
 // leaves its own (A, H) at once (PART) and the state behind it as soon as the
 // state before it is known (WHOLE); the next ones go back to the nearest chunk
 // whose state is there and take the parts between up from it, one after the
